@@ -1,8 +1,10 @@
 """kvx: paged KV-cache gather / scatter / gather-scatter and the HF
-[1, H, S, D] <-> [S, H, D] permutes on one MI355X (gfx950).
+[1, H, S, D] <-> [S, H, D] permutes on one MI355X (gfx950), and the serving
+step around a pool: page tables built from lengths, rows appended, attention
+with shared prefixes.
 
-A thin ctypes binding over ``libkvx.so`` (C ABI and contract: include/kvx.h).
-It only marshals arguments -- torch tensors become device pointers and sizes,
+A thin ctypes binding over ``libkvx.so`` (C ABI and contract: include/kvx.h and
+include/kvx_serve.h).  It only marshals arguments -- torch tensors become device pointers and sizes,
 streams become ``hipStream_t`` handles -- and every byte is moved by the HIP
 kernels in the library.  PyTorch is used for device memory and streams only.
 
@@ -21,7 +23,8 @@ import torch
 
 __all__ = ["KvxError", "Layout", "Pool", "Requests", "Table", "Heads", "gather", "scatter",
            "gather_scatter", "gather_scatter_heads", "extract_permute", "rebuild_permute",
-           "check_tables", "check_disjoint", "library_path", "DTYPE_CODES", "load_library"]
+           "check_tables", "check_disjoint", "library_path", "DTYPE_CODES", "load_library",
+           "BatchTables", "Prefix", "build_tables", "append", "attend", "attend_workspace"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkvx.so")
@@ -67,6 +70,34 @@ class _CHeads(ctypes.Structure):
                 ("block_layout", ctypes.c_int32)]
 
 
+class _CBatchTables(ctypes.Structure):
+    _fields_ = [("ctx_len", ctypes.c_void_p), ("tok_off", ctypes.c_void_p),
+                ("pg_off", ctypes.c_void_p), ("page_ids", ctypes.c_void_p),
+                ("cap_ids", ctypes.c_int64), ("slots", ctypes.c_void_p),
+                ("cap_tokens", ctypes.c_int64), ("totals", ctypes.c_void_p)]
+
+
+class _CRows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("num_tokens", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+class _CPrefix(ctypes.Structure):
+    _fields_ = [("num_groups", ctypes.c_int32), ("grp_off", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("table", _CTable)]
+
+
+class _CAttention(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -101,6 +132,14 @@ def load_library():
     lib.kvx_check_disjoint.argtypes = [P(_CLayout), P(_CReqs), P(_CPool), P(_CTable), P(_CPool),
                                        P(_CTable), vp, p64, P(p64)]
     lib.kvx_check_disjoint.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    lib.kvx_build_tables.argtypes = [i32, i32, vp, vp, P(_CTable), vp, p64, P(_CBatchTables), vp]
+    lib.kvx_append.argtypes = [P(_CLayout), i32, P(_CPool), i32, vp, P(_CRows), vp, vp]
+    lib.kvx_attend.argtypes = [P(_CLayout), i32, P(_CPool), i32, P(_CReqs), vp, P(_CTable),
+                               P(_CPrefix), P(_CAttention), vp, vp]
+    lib.kvx_attend_workspace.argtypes = [P(_CLayout), i32, i32, p64, i32, P(p64)]
+    for f in (lib.kvx_build_tables, lib.kvx_append, lib.kvx_attend, lib.kvx_attend_workspace):
+        f.restype = ctypes.c_int
     lib.kvx_status_str.argtypes = [ctypes.c_int]
     lib.kvx_status_str.restype = ctypes.c_char_p
     lib.kvx_abi_version.argtypes = []
@@ -570,3 +609,221 @@ def check_disjoint(layout: Layout, reqs: Requests, src: Optional[Pool] = None,
         _ptr(staging), _nbytes(staging), ctypes.byref(bad))
     if st != 0:
         raise KvxError(st, f"kvx_check_disjoint (batch token {bad.value})")
+
+
+# ------------------------------------------------- the serving step (kvx_serve.h)
+
+_TORCH_CODES = {torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.float32: 4}
+_BLOCK_LAYOUTS = {"nhd": 0, "hnd": 1}
+ATTEND_CAUSAL = 1       # kvx_serve.h KVX_ATTEND_CAUSAL
+
+
+def _vector(what: str, t: torch.Tensor, dtype: torch.dtype, least: int) -> int:
+    """Device pointer of a dense 1-D tensor of at least `least` elements."""
+    if t.dtype != dtype or t.dim() != 1 or t.numel() < least or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous 1-D {dtype} tensor of at least {least} "
+                         f"elements, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _token_rows(what: str, t: torch.Tensor, heads: int, dim: int) -> int:
+    """Bytes between the tokens of a [tokens, heads, dim] tensor that is dense
+    in its last two dimensions."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{what} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
+    if (dim > 1 and stride[2] != 1) or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{what} must be dense in its last two dimensions (strides {stride})")
+    return (stride[0] if shape[0] > 1 else heads * dim) * t.element_size()
+
+
+def _one_device(first: torch.Tensor, *others) -> torch.device:
+    """All tensors of a call on one GPU, which the launch goes to."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"kvx calls take device tensors; got a {dev} tensor")
+    for t in others:
+        if t is not None and not isinstance(t, int) and t.device != dev:
+            raise ValueError(f"tensors on {dev} and on {t.device} in one call")
+    return dev
+
+
+def _pool_tensor(pool: "Pool") -> Optional[torch.Tensor]:
+    keep = pool._keep
+    if isinstance(keep, torch.Tensor):
+        return keep
+    return next((t for t in keep if isinstance(t, torch.Tensor)), None)
+
+
+def _on(dev: torch.device, stream, call) -> int:
+    """call(stream handle) with `dev` current; the default stream is dev's current one."""
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def _block_layout(name: str) -> int:
+    if name not in _BLOCK_LAYOUTS:
+        raise ValueError('block_layout is "nhd" or "hnd"')
+    return _BLOCK_LAYOUTS[name]
+
+
+class BatchTables:
+    """Output buffers of build_tables: ``ctx_len`` [num_reqs] int32, ``tok_off``
+    and ``pg_off`` [num_reqs + 1] int64, ``page_ids`` [cap_pages] int32,
+    ``slots`` [cap_tokens] int64 and ``totals`` [4] int64 (new tokens, pages,
+    pages taken from the free list, pages it was short of).  ``table`` and
+    ``requests(total_tokens)`` are what the other calls take."""
+
+    def __init__(self, num_reqs: int, cap_tokens: int, cap_pages: int, device="cuda"):
+        def full(n, dtype, value=0):
+            return torch.full((n,), value, dtype=dtype, device=device)
+        self.num_reqs = num_reqs
+        self.ctx_len = full(num_reqs, torch.int32)
+        self.tok_off = full(num_reqs + 1, torch.int64)
+        self.pg_off = full(num_reqs + 1, torch.int64)
+        self.page_ids = full(cap_pages, torch.int32, -1)
+        self.slots = full(cap_tokens, torch.int64, -1)
+        self.totals = full(4, torch.int64)
+        self.table = Table(self.pg_off, self.page_ids)
+        self._c = _CBatchTables(_ptr(self.ctx_len), _ptr(self.tok_off), _ptr(self.pg_off),
+                                _ptr(self.page_ids), cap_pages, _ptr(self.slots), cap_tokens,
+                                _ptr(self.totals))
+
+    def requests(self, total_tokens: int) -> Requests:
+        """The batch of the new tokens (total_tokens: the sum of add_len, which
+        the caller knows; the device's count is totals[0])."""
+        return Requests(self.tok_off, total_tokens)
+
+
+def build_tables(out: BatchTables, page_size: int, add_len: torch.Tensor, free_ids: torch.Tensor,
+                 have_len: Optional[torch.Tensor] = None, held: Optional[Table] = None,
+                 stream=None) -> None:
+    """Page table, token offsets and slots of a batch in which request r holds
+    have_len[r] tokens in the pages of `held` and gets add_len[r] more, new
+    pages taken from free_ids in order (kvx_build_tables).  `out` must not
+    share memory with `held`: a loop keeps two BatchTables and alternates."""
+    n = out.num_reqs
+    add, free = _vector("add_len", add_len, torch.int32, n), _vector("free_ids", free_ids,
+                                                                     torch.int32, 0)
+    have = 0
+    if have_len is not None:
+        have = _vector("have_len", have_len, torch.int32, n)
+        if held is None:
+            raise ValueError("have_len needs the held table")
+        if held.pg_off.numel() < n:
+            raise ValueError(f"held: pg_off needs at least {n} entries")
+        if held.page_ids.data_ptr() == out.page_ids.data_ptr() and held.page_ids.numel() > 0:
+            raise ValueError("held is the output's own table: alternate two BatchTables")
+        _one_device(out.ctx_len, have_len, held.pg_off, held.page_ids)
+    dev = _one_device(out.ctx_len, add_len, free_ids)
+    lib = load_library()
+    _check(_on(dev, stream, lambda st: lib.kvx_build_tables(
+        n, page_size, have, add, held._c if have else None, free, free_ids.numel(), out._c, st)),
+        "kvx_build_tables")
+
+
+def append(layout: Layout, layer: int, pool: Pool, slots: torch.Tensor, k: torch.Tensor,
+           v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0, block_layout: str = "nhd",
+           skipped: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows k[t], v[t] ([tokens, kv_heads, head_dim], dense in the last two
+    dimensions) to slot slots[t] of the layer's planes; an "fp8" pool holds
+    e4m3 of x / scale (kvx_append)."""
+    _check_pool("pool", layout, pool)
+    h, d = layout.kv_heads, layout.head_dim
+    ks, vs = _token_rows("k", k, h, d), _token_rows("v", v, h, d)
+    n = k.shape[0]
+    if v.shape[0] != n or k.dtype != v.dtype:
+        raise ValueError("k and v must have one shape and type")
+    if k.dtype not in _TORCH_CODES:
+        raise ValueError(f"k and v are f16, bf16, f32 or float8_e4m3fn, got {k.dtype}")
+    at = _vector("slots", slots, torch.int64, n)
+    _counter(skipped)
+    dev = _one_device(k, v, slots, _pool_tensor(pool), skipped)
+    rows = _CRows(k.data_ptr(), v.data_ptr(), ks, vs, n, _TORCH_CODES[k.dtype], k_scale, v_scale)
+    lib, bl = load_library(), _block_layout(block_layout)
+    _check(_on(dev, stream, lambda st: lib.kvx_append(
+        layout._c, layer, pool._c, bl, at, rows, _ptr(skipped), st)), "kvx_append")
+
+
+class Prefix:
+    """Shared prefixes: group g is requests [grp_off[g], grp_off[g + 1]), which
+    all see the first lens[g] tokens of entry g of `table` (grp_off int64
+    [groups + 1] over the requests, lens int32 [groups])."""
+
+    def __init__(self, grp_off: torch.Tensor, lens: torch.Tensor, table: Table):
+        self.num_groups = grp_off.numel() - 1
+        if self.num_groups < 0:
+            raise ValueError("grp_off needs at least one entry")
+        off = _vector("grp_off", grp_off, torch.int64, 1)
+        ln = _vector("lens", lens, torch.int32, self.num_groups)
+        if table.pg_off.numel() < self.num_groups + 1:
+            raise ValueError(f"the prefix table's pg_off needs {self.num_groups + 1} entries")
+        self.grp_off, self.lens, self.table = grp_off, lens, table
+        self._c = _CPrefix(self.num_groups, off, ln, table._c)
+
+
+def attend_workspace(layout: Layout, reqs: Requests, q_heads: int,
+                     prefix: Optional[Prefix] = None) -> int:
+    """Bytes of workspace that attend needs for this batch or a smaller one
+    (kvx_attend_workspace)."""
+    n = ctypes.c_int64(0)
+    _check(load_library().kvx_attend_workspace(
+        layout._c, reqs.num_reqs, prefix.num_groups if prefix is not None else 0,
+        reqs.total_tokens, q_heads, ctypes.byref(n)), "kvx_attend_workspace")
+    return n.value
+
+
+def attend(layout: Layout, layer: int, pool: Pool, reqs: Requests, ctx_len: torch.Tensor,
+           table: Table, q: torch.Tensor, out: torch.Tensor, prefix: Optional[Prefix] = None,
+           lse: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
+           k_scale: float = 1.0, v_scale: float = 1.0, block_layout: str = "nhd",
+           workspace: Optional[torch.Tensor] = None, skipped: Optional[torch.Tensor] = None,
+           stream=None) -> None:
+    """Attention of query tokens q [tokens, q_heads, head_dim] over one layer of
+    the pool into `out`: each request's own ctx_len[r] tokens (causal: its
+    query tokens are the last of them) and, with `prefix`, its group's shared
+    ones (kvx_attend).  ``scale`` defaults to head_dim ** -0.5.  ``lse``: float32
+    [tokens, q_heads].  ``workspace``: a uint8 tensor of attend_workspace bytes,
+    kept by a caller whose calls do not overlap; by default one is allocated
+    for the call."""
+    _check_pool("pool", layout, pool)
+    _check_table("table", table, reqs)
+    t, d = reqs.total_tokens, layout.head_dim
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, q_heads, head_dim], got {tuple(q.shape)}")
+    hq = q.shape[1]
+    qs, os_ = _token_rows("q", q, hq, d), _token_rows("out", out, hq, d)
+    if q.shape[0] < t or out.shape[0] < t:
+        raise ValueError(f"q and out need total_tokens = {t} rows")
+    if q.dtype != out.dtype or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q and out are both f16 or both bf16, got {q.dtype} and {out.dtype}")
+    if lse is not None and (lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < t or
+                            lse.shape[1] != hq or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 [{t}, {hq}] tensor")
+    ctx = _vector("ctx_len", ctx_len, torch.int32, reqs.num_reqs)
+    _counter(skipped)
+    dev = _one_device(q, out, lse, ctx_len, reqs.tok_off, table.pg_off, table.page_ids,
+                      _pool_tensor(pool), workspace, skipped)
+    if prefix is not None:
+        _one_device(q, prefix.grp_off, prefix.lens, prefix.table.pg_off, prefix.table.page_ids)
+    lib, bl = load_library(), _block_layout(block_layout)
+    if workspace is None:
+        need = attend_workspace(layout, reqs, hq, prefix)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:       # allocated in the order of the stream that uses it
+            s = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(int(stream), device=dev)
+            with torch.cuda.stream(s):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _dense("workspace", workspace)
+    a = _CAttention(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0, qs, os_,
+                    hq, _TORCH_CODES[q.dtype], d ** -0.5 if scale is None else scale, k_scale,
+                    v_scale, ATTEND_CAUSAL if causal else 0, workspace.data_ptr(),
+                    _nbytes(workspace))
+    _check(_on(dev, stream, lambda st: lib.kvx_attend(
+        layout._c, layer, pool._c, bl, reqs._c, ctx, table._c,
+        prefix._c if prefix is not None else None, a, _ptr(skipped), st)), "kvx_attend")

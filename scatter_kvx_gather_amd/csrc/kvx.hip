@@ -1488,3 +1488,5 @@ const char* kvx_status_str(int32_t status) {
 int32_t kvx_abi_version(void) { return KVX_ABI_VERSION; }
 
 }  // extern "C"
+
+#include "kvx_serve_host.hpp"

@@ -1,0 +1,1309 @@
+// kvx_attend.hpp -- attention over a paged pool for batches whose requests
+// share prefixes (gfx950 / CDNA4).
+//
+// Mathematics.  Query token i of request r (n tokens, context c) sees every
+// key of its group's prefix and, in its own context, keys 0 .. c - n + i
+// (all c of them without the causal flag).  With s = scale * q.k,
+//   m = max s,  l = sum 2^(s' - m'),  o = sum 2^(s' - m') v   (s' = s log2 e)
+// over any subset of the keys, and two subsets join by
+//   m = max(m1, m2),  l = l1 2^(m1-m) + l2 2^(m2-m),  o likewise,
+// so a prefix is computed once for all rows of its group, a long axis is cut
+// anywhere, and out = o / l, lse = m + ln l at the end.  m, l and o are 32
+// bits throughout; weights are rounded to the query's type for the second
+// product (relative 2^-9 for bf16, 2^-12 for f16, averaged over the keys),
+// while l sums them unrounded.
+//
+// Work.  A segment is a group's prefix or a request's own context; an item is
+// (segment, head set, tile of query rows), and its length is the number of
+// keys its last row sees.  All items laid end to end make one line of keys
+// that the workgroups cut into equal pieces, whatever the lengths are: they
+// stand in device memory, so each workgroup finds its piece itself from a
+// scan over the segments, and the host needs to know none of them.  A piece
+// that is not a whole item leaves (m, l, o) in the workgroup's two slots of
+// the workspace; a whole item of a row that has two parts (prefix and own)
+// leaves them in that part's row buffer; a whole item of a row with one part
+// is written out at once.  k_attend_join joins the rest.
+//
+// Thin tiles (16 query rows a wave) are for segments with few rows, where the
+// KV rows' bytes are the bound: the waves of a workgroup take the heads of
+// one key range, so a pool row is read whole by one workgroup, and K and V go
+// from memory to the matrix instructions through registers alone.  Wide tiles
+// (128 or 256 rows a workgroup) are for segments with many rows, where the
+// matrix units are the bound: the workgroup stages fragments of K and V in
+// shared memory, each read by all of its waves.
+//
+// Fragments.  S^T = K Q^T by 16x16x32 products: K rows are loaded as the A
+// operand holds them (lane a + 16 g: key a, 8 dims at 8 g).  The result has
+// query row a in lanes a + 16 g, keys 4 g + r of two 16-key tiles, which is
+// how the B operand of O^T = V^T P^T holds them when its 8 k-slots of lane
+// group g stand for keys {4g..4g+3, 16+4g..16+4g+3}: the weights never leave
+// their registers.  V is loaded row by row (lane a: dims 8a .. 8a+7 of the
+// group's 8 keys) and its 8 x 8 blocks are transposed in registers with byte
+// permutes; row a of the j-th product is then dim 8 a + j.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+namespace kvx {
+namespace attend {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 8;               // waves of an attention workgroup
+constexpr int kThreads = 64 * kWaves;
+constexpr int kKeys = 32;               // keys of one step of a wave
+constexpr int kThinRows = 16;
+constexpr int kJoinWaves = 4;
+
+// A running maximum may lag the true one by this much (in log2) before the
+// accumulators are rescaled: weights stay below 2^8, exact in every type here.
+constexpr float kLag = 8.0f;
+
+struct Lists {                          // where a kind of segment's keys live
+    const int64_t* pg_off;
+    const int32_t* ids;
+    int64_t num_ids;
+};
+
+struct Args {
+    const char* k;                      // the layer's planes
+    const char* v;
+    int64_t row_stride;                 // bytes between the rows of a page, of one head
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t page_shift;                 // log2(page_size), or -1
+    const int64_t* tok_off;             // [num_reqs + 1]
+    const int32_t* ctx;                 // [num_reqs]
+    const int64_t* grp_off;             // [num_groups + 1]
+    const int32_t* plen;                // [num_groups]
+    Lists own;
+    Lists pre;
+    const char* q;
+    char* out;
+    float* lse;                         // or NULL
+    int64_t q_stride;                   // bytes between tokens
+    int64_t out_stride;
+    unsigned long long* skipped;        // or NULL
+    int32_t T;                          // query tokens
+    int32_t num_reqs;
+    int32_t num_groups;
+    int32_t H;                          // kv heads
+    int32_t G;                          // query heads per kv head
+    int32_t D;
+    int32_t causal;
+    float scale;                        // softmax scale * k scale * log2 e
+    float v_scale;
+    // tilings: thin heads are (kv head, part of its query heads) pairs
+    int32_t parts;                      // parts of a kv head's query heads
+    int32_t gv;                         // query heads of a part (the last may have fewer)
+    int32_t sets;                       // head sets of a thin segment
+    int32_t hs;                         // thin heads per set
+    int32_t kp;                         // waves that share a thin head's keys
+    int32_t thin_tokens;                // tokens per thin tile
+    int32_t wide_tokens;                // tokens per wide tile
+    int32_t pre_wide;                   // prefixes run in wide tiles
+    int32_t own_wide;                   // own contexts run in wide tiles
+    int32_t thin_min;                   // fewest keys of a piece
+    int32_t wide_min;
+    float wide_weight;                  // time of a wide key over a thin key's
+    // workspace
+    int64_t* starts;                    // [num_groups + num_reqs]: segment starts on its line
+    int64_t* plan;                      // [4]: keys and workgroups of the thin and the wide line
+    float* slot_o;                      // [2 * grid][slot rows][D]
+    float* slot_ml;                     // [2 * grid][slot rows][2]
+    float* row_o;                       // [2][T][Hq][D]: own, prefix (only with prefixes)
+    float* row_ml;                      // [2][T][Hq][2]
+    int32_t slot_rows;
+};
+
+// ------------------------------------------------------------- segments --
+
+struct Seg {
+    int32_t tok0;                       // first query token
+    int32_t ntok;
+    int32_t keys;
+    int32_t base;                       // keys the token before the first would see
+    int32_t tiles;
+    int32_t tp;                         // tokens per tile
+    int32_t sets;                       // head sets
+    bool wide;
+    bool causal;
+};
+
+__device__ inline int32_t clamp_to(int64_t x, int64_t lo, int64_t hi) {
+    return static_cast<int32_t>(x < lo ? lo : (x > hi ? hi : x));
+}
+
+// Segment s: prefix s of group s, or the own context of request s - groups.
+// (Offsets that break their contract are held inside the batch.)
+__device__ inline Seg segment(const Args& A, int32_t s) {
+    Seg g;
+    const bool pre = s < A.num_groups;
+    int32_t r0 = s - A.num_groups, r1 = r0 + 1, keys;
+    if (pre) {
+        r0 = clamp_to(A.grp_off[s], 0, A.num_reqs);
+        r1 = clamp_to(A.grp_off[s + 1], r0, A.num_reqs);
+        keys = A.plen[s];
+    } else {
+        keys = A.ctx[r0];
+    }
+    g.keys = keys > 0 ? keys : 0;
+    g.tok0 = clamp_to(A.tok_off[r0], 0, A.T);
+    g.ntok = clamp_to(A.tok_off[r1], g.tok0, A.T) - g.tok0;
+    g.causal = !pre && A.causal != 0;
+    g.base = !g.causal ? g.keys : (g.keys > g.ntok ? g.keys - g.ntok : 0);
+    g.wide = (pre ? A.pre_wide : A.own_wide) != 0;
+    g.tp = g.wide ? A.wide_tokens : A.thin_tokens;
+    g.sets = g.wide ? A.H : A.sets;
+    g.tiles = g.keys > 0 ? (g.ntok + g.tp - 1) / g.tp : 0;
+    return g;
+}
+
+// Keys before tile i of a head set, and the keys of tile i (one more row tile
+// of a causal segment sees up to tp more keys).
+__device__ inline int64_t tile_start(const Seg& g, int32_t i) {
+    const int64_t n = i;
+    return n * g.base + (g.causal ? g.tp * (n * (n + 1) / 2) : 0);
+}
+__device__ inline int64_t tile_keys(const Seg& g, int32_t i) {
+    if (!g.causal) return g.base;
+    const int64_t last = (static_cast<int64_t>(i) + 1) * g.tp;
+    return g.base + (last < g.ntok ? last : g.ntok);
+}
+__device__ inline int64_t set_keys(const Seg& g) {
+    return g.tiles > 0 ? tile_start(g, g.tiles - 1) + tile_keys(g, g.tiles - 1) : 0;
+}
+
+// First key of workgroup w's piece of a line of n keys cut in `wgs` pieces, and the piece that key x is in.
+__device__ inline int64_t piece_start(int64_t n, int64_t wgs, int64_t w) { return n * w / wgs; }
+__device__ inline int64_t piece_of(int64_t n, int64_t wgs, int64_t x) {
+    return ((x + 1) * wgs - 1) / n;
+}
+
+// Byte offset of key t's row (of head 0), or -1 when its page is out of range.
+__device__ inline int64_t key_offset(const Args& A, const Lists& L, int64_t pg0, int32_t t) {
+    const uint32_t tu = static_cast<uint32_t>(t);
+    const uint32_t kp = A.page_shift >= 0 ? tu >> A.page_shift : tu / static_cast<uint32_t>(A.page_size);
+    const uint32_t row = tu - kp * static_cast<uint32_t>(A.page_size);
+    // the index is range-checked before the sum is formed: no pg_off value makes it wrap
+    if (pg0 < -static_cast<int64_t>(kp) || pg0 >= L.num_ids - static_cast<int64_t>(kp)) return -1;
+    const int64_t page = L.ids[pg0 + kp];
+    if (page < 0 || page >= A.num_pages) return -1;
+    return page * A.page_stride + row * A.row_stride;
+}
+
+// ------------------------------------------------------------ elements --
+
+template <class T>
+struct Mma;
+template <>
+struct Mma<__bf16> {
+    static __device__ f32x4 run(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    static __device__ uint32_t pack(float x, float y) {
+        bf16x2 r = {static_cast<__bf16>(x), static_cast<__bf16>(y)};
+        return __builtin_bit_cast(uint32_t, r);
+    }
+    template <bool HI>
+    static __device__ uint32_t from_fp8(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+    }
+    static __device__ float lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+    static __device__ float hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+    static constexpr uint32_t kExp = 0x7f807f80u;       // exponent bits of both halves
+};
+template <>
+struct Mma<_Float16> {
+    static __device__ f32x4 run(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+    static __device__ uint32_t pack(float x, float y) {
+        f16x2 r = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+        return __builtin_bit_cast(uint32_t, r);
+    }
+    template <bool HI>
+    static __device__ uint32_t from_fp8(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+    }
+    static __device__ float lo(uint32_t w) {
+        return static_cast<float>(__builtin_bit_cast(f16x2, w).x);
+    }
+    static __device__ float hi(uint32_t w) {
+        return static_cast<float>(__builtin_bit_cast(f16x2, w).y);
+    }
+    static constexpr uint32_t kExp = 0x7c007c00u;
+};
+
+// Whether either half of w is an infinity or a NaN.
+template <class T>
+__device__ inline bool odd_pair(uint32_t w) {
+    const uint32_t e = w & Mma<T>::kExp;
+    return (e & 0xffffu) == (Mma<T>::kExp & 0xffffu) || (e >> 16) == (Mma<T>::kExp >> 16);
+}
+
+// Shapes of one (query type, pool element, padded head dim) combination.
+template <class T, bool FP8, int DP>
+struct Cfg {
+    static constexpr int EB = FP8 ? 1 : 2;
+    static constexpr int KS = DP / 32;                  // k-steps of the first product
+    static constexpr int NK = DP * EB / 64;             // 16-byte loads of K per key tile
+    static constexpr int VE = DP >= 128 ? 8 : 4;        // dims of V a lane holds per chunk
+    static constexpr int NC = DP / (16 * VE);           // chunks of V
+    static constexpr int VW = VE * EB / 4;              // dwords of a V chunk as loaded
+    static constexpr int NJ = NC * VE;                  // products of the second product
+};
+
+// First dim of the 8 that k-step ks takes from lane group g.
+template <class C>
+__device__ inline int k_dim(int ks, int g) {
+    return C::EB == 2 ? ks * 32 + g * 8 : (ks >> 1) * 64 + g * 16 + (ks & 1) * 8;
+}
+
+template <int W>
+struct Words {
+    uint32_t w[W];
+};
+
+template <int W>
+__device__ inline Words<W> load_words(const char* p) {
+    Words<W> r;
+    if constexpr (W == 4) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+        r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+    } else if constexpr (W == 2) {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+        r.w[0] = x.x; r.w[1] = x.y;
+    } else {
+        r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+    return r;
+}
+
+// K of one 16-key tile as loaded, and its k-step ks as the product takes it.
+template <class C>
+struct KTile {
+    u32x4 raw[C::NK];
+};
+
+template <class C>
+__device__ inline void load_k(KTile<C>* t, const char* row, int g, int D) {
+#pragma unroll
+    for (int x = 0; x < C::NK; ++x) {
+        const int b = x * 64 + g * 16;
+        const bool in = b < D * C::EB;
+        t->raw[x] = *reinterpret_cast<const u32x4*>(row + (in ? b : 0));
+    }
+}
+
+template <class T, class C>
+__device__ inline u32x4 k_frag(const KTile<C>& t, int ks, int g, int D) {
+    u32x4 f;
+    if constexpr (C::EB == 2) {
+        f = t.raw[ks];
+    } else {
+        const u32x4 r = t.raw[ks >> 1];
+        const uint32_t lo = (ks & 1) ? r.z : r.x, hi = (ks & 1) ? r.w : r.y;
+        f = u32x4{Mma<T>::template from_fp8<false>(lo), Mma<T>::template from_fp8<true>(lo),
+                  Mma<T>::template from_fp8<false>(hi), Mma<T>::template from_fp8<true>(hi)};
+    }
+    // dims past the head: another head's values must not meet the query's zeros
+    // (an infinity there would make a NaN)
+    if (D < C::KS * 32 && k_dim<C>(ks, g) >= D) f = u32x4{0, 0, 0, 0};
+    return f;
+}
+
+// V of the 8 keys of a lane group, one chunk, in the query's type: x[i][w] = dims 2w, 2w+1 of key i.
+template <class T, class C>
+__device__ inline void v_pairs(const Words<C::VW>& raw, uint32_t* x) {
+    if constexpr (C::EB == 2) {
+#pragma unroll
+        for (int w = 0; w < C::VE / 2; ++w) x[w] = raw.w[w];
+    } else {
+#pragma unroll
+        for (int w = 0; w < C::VW; ++w) {
+            x[2 * w] = Mma<T>::template from_fp8<false>(raw.w[w]);
+            x[2 * w + 1] = Mma<T>::template from_fp8<true>(raw.w[w]);
+        }
+    }
+}
+
+// Operands of dims 2w and 2w+1 from the pairs of 8 keys.
+__device__ inline void v_transpose(const uint32_t (&x)[8], u32x4* even, u32x4* odd) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        (*even)[p] = __builtin_amdgcn_perm(x[2 * p + 1], x[2 * p], 0x05040100u);
+        (*odd)[p] = __builtin_amdgcn_perm(x[2 * p + 1], x[2 * p], 0x07060302u);
+    }
+}
+
+// ------------------------------------------------------ running softmax --
+
+// State of 16 query rows: the lane's row a = lane % 16.
+template <class C>
+struct Rows {
+    float m;                    // reference maximum (log2), the same in a row's four lanes
+    float l;                    // this lane's share of the sum
+    f32x4 o[C::NJ];             // o[c * VE + j][r]: dim 16 VE c + (4 g + r) VE + j
+};
+
+template <class C>
+__device__ inline void clear(Rows<C>* R) {
+    R->m = -INFINITY;
+    R->l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) R->o[j] = f32x4{0, 0, 0, 0};
+}
+
+// Scores s of 32 keys to weights p, with the row's maximum moved and the
+// accumulators rescaled when a score passes it by more than kLag.
+template <class C>
+__device__ inline void weigh(Rows<C>* R, const f32x4 (&s)[2], float scale, float (&p)[8]) {
+    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * scale;
+    if (__any(top > R->m + kLag)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m = fmaxf(R->m, top);
+        const float a = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(R->m - m);
+        R->m = m;
+        R->l *= a;
+#pragma unroll
+        for (int j = 0; j < C::NJ; ++j) R->o[j] *= a;
+    }
+    const float m = R->m == -INFINITY ? 0.0f : R->m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], scale, -m));
+        sum += p[i];
+    }
+    R->l += sum;
+}
+
+template <class T>
+__device__ inline u32x4 pack_weights(const float (&p)[8]) {
+    return u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]), Mma<T>::pack(p[4], p[5]),
+                 Mma<T>::pack(p[6], p[7])};
+}
+
+// The second product for a step in which some rows do not see a key whose
+// value row holds an infinity or a NaN: in one matrix product 0 times it would
+// reach them.  Row by row, with the keys that the row does not see cleared
+// from the operand, and only the row's own column kept.  `vf(j, z)` is operand
+// j; z is 0, but not known to be: it keeps the operands from being formed
+// ahead of the loop, whose registers the usual path would pay for.
+template <class T, class C, class VF>
+__device__ inline void add_values_by_row(Rows<C>* R, u32x4 pf, int32_t key0, int32_t limit, VF vf) {
+    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+#pragma unroll 1
+    for (int row = 0; row < 16; ++row) {
+        const int32_t lim = __shfl(limit, row) - key0;
+        uint32_t z = 0;
+        u32x4 keep;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int key = (p >> 1) * 16 + 4 * g + (p & 1) * 2;
+            keep[p] = (key < lim ? 0xffffu : 0u) | (key + 1 < lim ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < C::NJ; ++j) {
+            asm volatile("" : "+v"(z) : "v"(R->o[j > 0 ? j - 1 : 0][0]));
+            const f32x4 d = Mma<T>::run(vf(j, z) & keep, pf, f32x4{0, 0, 0, 0});
+            if (a == row) R->o[j] += d;
+        }
+    }
+}
+
+// ------------------------------------------------------------- results --
+
+enum : int { kSlot = 0, kRowBuffer = 1, kFinal = 2 };
+
+// Where a piece's rows go.
+struct Dest {
+    int kind;
+    int32_t slot;               // kSlot
+    int part;                   // kRowBuffer: 0 own, 1 prefix
+};
+
+template <class T, class C>
+__device__ inline void store_rows(const Args& A, const Dest& to, const Rows<C>& R, int slot_row,
+                                  int32_t token, int32_t head, bool live) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    float l = R.l;
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (!live) return;
+    const int64_t hq = static_cast<int64_t>(A.H) * A.G;
+    if (to.kind == kFinal) {
+        const float inv = l == 0.0f ? 0.0f : A.v_scale / l;
+        char* row = A.out + static_cast<int64_t>(token) * A.out_stride + static_cast<int64_t>(head) * A.D * 2;
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = c * 16 * C::VE + (4 * g + r) * C::VE;
+                if (d >= A.D) continue;
+                uint32_t w[C::VE / 2];
+#pragma unroll
+                for (int j = 0; j < C::VE; j += 2)
+                    w[j / 2] = Mma<T>::pack(R.o[c * C::VE + j][r] * inv,
+                                            R.o[c * C::VE + j + 1][r] * inv);
+                if constexpr (C::VE == 8)
+                    *reinterpret_cast<u32x4*>(row + d * 2) = u32x4{w[0], w[1], w[2], w[3]};
+                else
+                    *reinterpret_cast<u32x2*>(row + d * 2) = u32x2{w[0], w[1]};
+            }
+        if (g == 0 && A.lse != nullptr)
+            A.lse[static_cast<int64_t>(token) * hq + head] =
+                l == 0.0f ? -INFINITY : (R.m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+        return;
+    }
+    int64_t row;
+    float *o, *ml;
+    if (to.kind == kSlot) {
+        row = static_cast<int64_t>(to.slot) * A.slot_rows + slot_row;
+        o = A.slot_o + row * A.D;
+        ml = A.slot_ml + row * 2;
+    } else {
+        row = (static_cast<int64_t>(to.part) * A.T + token) * hq + head;
+        o = A.row_o + row * A.D;
+        ml = A.row_ml + row * 2;
+    }
+    if (g == 0) *reinterpret_cast<float2*>(ml) = make_float2(R.m, l);
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int d = c * 16 * C::VE + (4 * g + r) * C::VE;
+            if (d >= A.D) continue;
+#pragma unroll
+            for (int j = 0; j < C::VE; j += 4)
+                *reinterpret_cast<f32x4*>(o + d + j) =
+                    f32x4{R.o[c * C::VE + j][r], R.o[c * C::VE + j + 1][r],
+                          R.o[c * C::VE + j + 2][r], R.o[c * C::VE + j + 3][r]};
+        }
+}
+
+// --------------------------------------------------------------- thin --
+
+// A piece of an item: keys [key0, key1) of tile `tile` of head set `set`.
+struct Piece {
+    Seg seg;
+    Lists lists;
+    int64_t pg0;
+    int32_t set;
+    int32_t tile;
+    int32_t key0, key1;
+    bool counts;                // this piece counts the out-of-range keys
+};
+
+// Counts the out-of-range keys of a piece's range, once per key of a segment:
+// the pieces of the segment's last tile (which sees every key) and first head
+// set cover its keys exactly once.
+__device__ inline void count_skipped(const Args& A, const Piece& P, int wave) {
+    if (A.skipped == nullptr || !P.counts) return;
+    const int lane = threadIdx.x & 63;
+    unsigned long long n = 0;
+    for (int64_t t = static_cast<int64_t>(P.key0) + wave * 64; t < P.key1; t += kThreads) {
+        const bool bad = t + lane < P.key1 && key_offset(A, P.lists, P.pg0, static_cast<int32_t>(t) + lane) < 0;
+        n += __popcll(__ballot(bad));
+    }
+    if (lane == 0 && n != 0) atomicAdd(A.skipped, n);
+}
+
+template <class T, class C>
+__device__ inline void load_q(const Args& A, u32x4 (&q)[C::KS], int32_t token, int32_t head,
+                              bool live) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const char* row = A.q + static_cast<int64_t>(token) * A.q_stride + static_cast<int64_t>(head) * A.D * 2;
+#pragma unroll
+    for (int ks = 0; ks < C::KS; ++ks) {
+        const int d = k_dim<C>(ks, g);
+        q[ks] = u32x4{0, 0, 0, 0};
+        if (live && d < A.D) q[ks] = *reinterpret_cast<const u32x4*>(row + d * 2);
+    }
+}
+
+// One step of 32 keys against 16 query rows, K as fragments from `kf(kt, ks)`
+// and V as operands from `vf(j)`.
+template <class T, class C, class KF>
+__device__ inline void scores(const u32x4 (&q)[C::KS], f32x4 (&s)[2], KF kf) {
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+        s[kt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < C::KS; ++ks) s[kt] = Mma<T>::run(kf(kt, ks), q[ks], s[kt]);
+    }
+}
+
+// Keys this lane's row does not see get -inf: key index key0 + ..., seen below
+// `limit` and where `valid` has its bit.
+__device__ inline void mask_scores(f32x4 (&s)[2], int32_t key0, int32_t limit, uint32_t valid) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int key = (i >> 2) * 16 + 4 * g + (i & 3);
+        if (key0 + key >= limit || !((valid >> key) & 1)) s[i >> 2][i & 3] = -INFINITY;
+    }
+}
+
+template <class T, class C>
+__device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* lds) {
+    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = wave % A.hs, part = wave / A.hs;
+    const int32_t vh = P.set * A.hs + h;                  // thin head
+    const int32_t kvh = vh / A.parts, sub = vh % A.parts;
+    const bool works = part < A.kp && vh < A.H * A.parts;
+    count_skipped(A, P, wave);
+
+    // this lane's query row
+    const int32_t local = P.tile * A.thin_tokens + a / A.gv;
+    const int32_t hsub = sub * A.gv + a % A.gv;
+    const bool live = works && a < A.thin_tokens * A.gv && local < P.seg.ntok && hsub < A.G;
+    const int32_t token = P.seg.tok0 + local;
+    const int32_t head = kvh * A.G + hsub;
+    const int32_t past = P.seg.keys - P.seg.ntok;
+    // keys that this row sees, and the fewest that a row of the tile sees
+    int32_t limit = P.key1, all_see = P.key1;
+    if (P.seg.causal) {
+        if (live && past + local + 1 < limit) limit = past + local + 1;
+        all_see = past + P.tile * A.thin_tokens + 1;
+    }
+
+    Rows<C> R;
+    clear(&R);
+    if (works) {
+        u32x4 q[C::KS];
+        load_q<T, C>(A, q, token, head, live);
+        const char* kh = A.k + kvh * A.head_stride;
+        const char* vhd = A.v + kvh * A.head_stride;
+        const int32_t step = kKeys * A.kp;
+
+        // K and V of a step as loaded.  Up to 128 dims both are loaded a step
+        // ahead; above, K and then V of the present step, one after the other.
+        constexpr bool AHEAD = C::NC == 1;
+        KTile<C> kt[2];
+        Words<C::VW> vr[8][C::NC];
+        auto offset_of = [&](int32_t key0) -> int64_t {
+            const int32_t t = key0 + (lane & 31);
+            return t < P.key1 ? key_offset(A, P.lists, P.pg0, t) : -1;
+        };
+        auto load_keys = [&](int64_t off) {
+            const int64_t safe = off < 0 ? 0 : off;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) load_k<C>(&kt[x], kh + __shfl(safe, x * 16 + a), g, A.D);
+        };
+        auto load_values = [&](int64_t off) {
+            const int64_t safe = off < 0 ? 0 : off;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const char* row = vhd + __shfl(safe, (i >> 2) * 16 + 4 * g + (i & 3));
+#pragma unroll
+                for (int c = 0; c < C::NC; ++c) {
+                    const int d = (c * 16 + a) * C::VE;
+                    vr[i][c] = load_words<C::VW>(row + (d < A.D ? d * C::EB : 0));
+                }
+            }
+        };
+        // operands of products 2 w and 2 w + 1 of chunk c
+        auto value_pair = [&](int c, int w, uint32_t z, u32x4* even, u32x4* odd) {
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t x[C::VE / 2];
+                v_pairs<T, C>(vr[i][c], x);
+                y[i] = x[w] ^ z;
+            }
+            v_transpose(y, even, odd);
+        };
+
+        int32_t key0 = P.key0 + part * kKeys;
+        int64_t off = key0 < P.key1 ? offset_of(key0) : -1;
+        if (AHEAD && key0 < P.key1) {
+            load_keys(off);
+            load_values(off);
+        }
+        int64_t off_next = key0 + step < P.key1 ? offset_of(key0 + step) : -1;
+        for (; key0 < P.key1; key0 += step) {
+            const uint32_t valid = static_cast<uint32_t>(__ballot(off >= 0));
+            const bool more = key0 + step < P.key1;
+            if (!AHEAD) load_keys(off);
+            f32x4 s[2];
+            scores<T, C>(q, s, [&](int x, int ks) { return k_frag<T, C>(kt[x], ks, g, A.D); });
+            if (!AHEAD) load_values(off);
+            if (AHEAD && more) load_keys(off_next);
+            const int64_t off_after = key0 + 2 * step < P.key1 ? offset_of(key0 + 2 * step) : -1;
+            const bool partial = all_see < key0 + kKeys;
+            if (valid != 0xffffffffu || partial) mask_scores(s, key0, limit, valid);
+            float p[8];
+            weigh<C>(&R, s, A.scale, p);
+            if (valid != 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!((valid >> ((i >> 2) * 16 + 4 * g + (i & 3))) & 1))
+#pragma unroll
+                        for (int c = 0; c < C::NC; ++c)
+#pragma unroll
+                            for (int w = 0; w < C::VW; ++w) vr[i][c].w[w] = 0;
+            }
+            bool odd = false;
+            if (partial && P.seg.causal) {
+                bool mine = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c) {
+                        uint32_t x[C::VE / 2];
+                        v_pairs<T, C>(vr[i][c], x);
+#pragma unroll
+                        for (int w = 0; w < C::VE / 2; ++w) mine |= odd_pair<T>(x[w]);
+                    }
+                odd = __any(mine);
+            }
+            const u32x4 pf = pack_weights<T>(p);
+            if (odd) {
+                add_values_by_row<T, C>(&R, pf, key0, limit, [&](int j, uint32_t z) {
+                    u32x4 f[2];
+                    value_pair(j / C::VE, j % C::VE / 2, z, &f[0], &f[1]);
+                    return f[j & 1];
+                });
+            } else {
+#pragma unroll
+                for (int j = 0; j < C::NJ; j += 2) {
+                    u32x4 f[2];
+                    value_pair(j / C::VE, j % C::VE / 2, 0, &f[0], &f[1]);
+                    R.o[j] = Mma<T>::run(f[0], pf, R.o[j]);
+                    R.o[j + 1] = Mma<T>::run(f[1], pf, R.o[j + 1]);
+                }
+            }
+            if (AHEAD && more) load_values(off_next);
+            off = off_next;
+            off_next = off_after;
+        }
+    }
+
+    // join the waves that shared a head's keys: the upper half of the parts
+    // hands over to the lower until one is left
+    for (int n = A.kp; n > 1;) {
+        const int half = (n + 1) / 2;
+        __syncthreads();
+        if (works && part >= half && part < n) {
+            float* b = lds + ((part - half) * A.hs + h) * (64 * (4 * C::NJ + 2));
+            b[lane] = R.m;
+            b[64 + lane] = R.l;
+#pragma unroll
+            for (int j = 0; j < C::NJ; ++j)
+                *reinterpret_cast<f32x4*>(b + 128 + (j * 64 + lane) * 4) = R.o[j];
+        }
+        __syncthreads();
+        if (works && part + half < n) {
+            const float* b = lds + (part * A.hs + h) * (64 * (4 * C::NJ + 2));
+            const float m2 = b[lane], l2 = b[64 + lane];
+            const float m = fmaxf(R.m, m2);
+            const float ref = m == -INFINITY ? 0.0f : m;
+            const float w1 = __builtin_amdgcn_exp2f(R.m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
+            R.m = m;
+            R.l = R.l * w1 + l2 * w2;
+#pragma unroll
+            for (int j = 0; j < C::NJ; ++j)
+                R.o[j] = R.o[j] * w1 + *reinterpret_cast<const f32x4*>(b + 128 + (j * 64 + lane) * 4) * w2;
+        }
+        n = half;
+    }
+    if (works && part == 0) store_rows<T, C>(A, to, R, h * kThinRows + a, token, head, live);
+    if (A.kp > 1) __syncthreads();
+}
+
+// ---------------------------------------------------------------- wide --
+
+// A wide tile's shapes: RT row tiles of 16 per wave, KT keys staged at a time.
+template <class C>
+struct Wide {
+    static constexpr int DP = C::KS * 32;
+    static constexpr int RT = DP <= 128 ? 2 : 1;
+    static constexpr int ROWS = kWaves * 16 * RT;
+    static constexpr int KT = DP <= 128 ? 128 : 64;
+    static constexpr int NB = KT / kKeys;               // steps of 32 keys
+    static constexpr int KF = (KT / 16) * C::KS;        // K fragments of 1 KiB
+    static constexpr int VF = NB * C::NJ;               // V fragments
+    static constexpr int BUF = (KF + VF) * 1024;
+    static constexpr int LDS = 2 * BUF + 2 * NB * 12;
+};
+
+template <class T, class C>
+__device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* lds) {
+    using W = Wide<C>;
+    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t kvh = P.set;
+    count_skipped(A, P, wave);
+
+    int32_t token[W::RT], head[W::RT], limit[W::RT];
+    bool live[W::RT];
+    u32x4 q[W::RT][C::KS];
+    Rows<C> R[W::RT];
+    const int32_t at = P.tile * A.wide_tokens, past = P.seg.keys - P.seg.ntok;
+    const int32_t first = at + wave * 16 * W::RT / A.G;     // this wave's first and last token
+    int32_t last = at + (wave * 16 * W::RT + 16 * W::RT - 1) / A.G;
+    if (last > P.seg.ntok - 1) last = P.seg.ntok - 1;
+    // keys that some row of this wave sees, and that every one does
+    int32_t most = P.key1, all_see = P.key1;
+    if (P.seg.causal) {
+        if (past + last + 1 < most) most = past + last + 1;
+        all_see = past + first + 1;
+    }
+    if (first >= P.seg.ntok) most = 0;                      // no rows
+#pragma unroll
+    for (int t = 0; t < W::RT; ++t) {
+        const int row = (wave * W::RT + t) * 16 + a;
+        const int32_t local = at + row / A.G;
+        live[t] = row < A.wide_tokens * A.G && local < P.seg.ntok;
+        token[t] = P.seg.tok0 + local;
+        head[t] = kvh * A.G + row % A.G;
+        limit[t] = P.key1;
+        if (live[t] && P.seg.causal && past + local + 1 < limit[t]) limit[t] = past + local + 1;
+        load_q<T, C>(A, q[t], token[t], head[t], live[t]);
+        clear(&R[t]);
+    }
+
+    const char* kh = A.k + kvh * A.head_stride;
+    const char* vhd = A.v + kvh * A.head_stride;
+    uint32_t* flags = reinterpret_cast<uint32_t*>(lds + 2 * W::BUF);   // [2][NB]: valid keys
+    uint32_t* odd_flags = flags + 2 * W::NB;                // [2][NB][2]: by staging wave
+
+    // Staging: waves 0-3 take K (KT / 4 keys each), waves 4-7 V (one step's
+    // keys, or half of its chunks, each).
+    constexpr int KPW = W::KT / 64;                       // K tiles per staging wave
+    constexpr int CPW = W::NB == 4 ? C::NC : 1;           // V chunks per staging wave
+    const bool stages_k = wave < 4;
+    const int vb = W::NB == 4 ? wave - 4 : (wave - 4) >> 1;
+    const int vc = W::NB == 4 ? 0 : (wave - 4) & 1;
+    constexpr int RAW_K = KPW * C::NK * 4, RAW_V = 8 * CPW * C::VW;
+    uint32_t raw[RAW_K > RAW_V ? RAW_K : RAW_V];          // of either kind of staging wave
+    auto offset_of = [&](int32_t tile0) -> int64_t {
+        const int32_t t = tile0 + (stages_k ? wave * (W::KT / 4) + (lane & (W::KT / 4 - 1))
+                                            : vb * kKeys + (lane & 31));
+        return t < P.key1 ? key_offset(A, P.lists, P.pg0, t) : -1;
+    };
+    auto load_tile = [&](int64_t off) {
+        const int64_t safe = off < 0 ? 0 : off;
+        if (stages_k) {
+#pragma unroll
+            for (int x = 0; x < KPW; ++x) {
+                KTile<C> kt;
+                load_k<C>(&kt, kh + __shfl(safe, x * 16 + a), g, A.D);
+#pragma unroll
+                for (int y = 0; y < C::NK; ++y)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) raw[(x * C::NK + y) * 4 + z] = kt.raw[y][z];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const char* row = vhd + __shfl(safe, (i >> 2) * 16 + 4 * g + (i & 3));
+#pragma unroll
+                for (int c = 0; c < CPW; ++c) {
+                    const int d = ((vc + c) * 16 + a) * C::VE;
+                    const Words<C::VW> w = load_words<C::VW>(row + (d < A.D ? d * C::EB : 0));
+#pragma unroll
+                    for (int z = 0; z < C::VW; ++z) raw[(i * CPW + c) * C::VW + z] = w.w[z];
+                }
+            }
+        }
+    };
+    auto stage_tile = [&](int64_t off, int buf) {
+        char* kb = lds + buf * W::BUF;
+        char* vbuf = kb + W::KF * 1024;
+        if (stages_k) {
+#pragma unroll
+            for (int x = 0; x < KPW; ++x) {
+                KTile<C> kt;
+#pragma unroll
+                for (int y = 0; y < C::NK; ++y)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) kt.raw[y][z] = raw[(x * C::NK + y) * 4 + z];
+#pragma unroll
+                for (int ks = 0; ks < C::KS; ++ks)
+                    *reinterpret_cast<u32x4*>(kb + (((wave * KPW + x) * C::KS + ks) * 64 + lane) * 16) =
+                        k_frag<T, C>(kt, ks, g, A.D);
+            }
+        } else {
+            const uint32_t valid = static_cast<uint32_t>(__ballot(off >= 0));
+            bool mine = false;
+#pragma unroll
+            for (int c = 0; c < CPW; ++c) {
+                uint32_t x[8][C::VE / 2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    Words<C::VW> w;
+#pragma unroll
+                    for (int z = 0; z < C::VW; ++z) w.w[z] = raw[(i * CPW + c) * C::VW + z];
+                    v_pairs<T, C>(w, x[i]);
+                }
+                if (valid != 0xffffffffu) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (!((valid >> ((i >> 2) * 16 + 4 * g + (i & 3))) & 1))
+#pragma unroll
+                            for (int w = 0; w < C::VE / 2; ++w) x[i][w] = 0;
+                }
+                if (P.seg.causal) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int w = 0; w < C::VE / 2; ++w) mine |= odd_pair<T>(x[i][w]);
+                }
+#pragma unroll
+                for (int w = 0; w < C::VE / 2; ++w) {
+                    const uint32_t y[8] = {x[0][w], x[1][w], x[2][w], x[3][w],
+                                           x[4][w], x[5][w], x[6][w], x[7][w]};
+                    u32x4 even, oddv;
+                    v_transpose(y, &even, &oddv);
+                    char* to = vbuf + ((vb * C::NJ + (vc + c) * C::VE + 2 * w) * 64 + lane) * 16;
+                    *reinterpret_cast<u32x4*>(to) = even;
+                    *reinterpret_cast<u32x4*>(to + 1024) = oddv;
+                }
+            }
+            const bool odd = __any(mine);
+            if (lane == 0) {
+                if (vc == 0) flags[buf * W::NB + vb] = valid;
+                odd_flags[(buf * W::NB + vb) * 2 + vc] = odd ? 1u : 0u;
+            }
+        }
+    };
+
+    int64_t off = offset_of(P.key0);
+    load_tile(off);
+    int64_t off_next = offset_of(P.key0 + W::KT);
+    stage_tile(off, 0);
+    __syncthreads();
+    int buf = 0;
+    for (int32_t tile0 = P.key0; tile0 < P.key1; tile0 += W::KT, buf ^= 1) {
+        const bool more = tile0 + W::KT < P.key1;
+        int64_t off_after = -1;
+        if (more) {
+            load_tile(off_next);
+            off_after = offset_of(tile0 + 2 * W::KT);
+        }
+        const char* kb = lds + buf * W::BUF;
+        const char* vbuf = kb + W::KF * 1024;
+#pragma unroll 1
+        for (int b = 0; b < W::NB; ++b) {
+            const int32_t key0 = tile0 + b * kKeys;
+            if (key0 >= most) break;
+            const uint32_t valid = __builtin_amdgcn_readfirstlane(flags[buf * W::NB + b]);
+            const bool partial = all_see < key0 + kKeys;
+            f32x4 s[W::RT][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int t = 0; t < W::RT; ++t) s[t][x] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int ks = 0; ks < C::KS; ++ks) {
+                    const u32x4 f = *reinterpret_cast<const u32x4*>(
+                        kb + (((b * 2 + x) * C::KS + ks) * 64 + lane) * 16);
+#pragma unroll
+                    for (int t = 0; t < W::RT; ++t) s[t][x] = Mma<T>::run(f, q[t][ks], s[t][x]);
+                }
+            }
+            u32x4 pf[W::RT];
+#pragma unroll
+            for (int t = 0; t < W::RT; ++t) {
+                if (valid != 0xffffffffu || partial) mask_scores(s[t], key0, limit[t], valid);
+                float p[8];
+                weigh<C>(&R[t], s[t], A.scale, p);
+                pf[t] = pack_weights<T>(p);
+            }
+            const uint32_t* of = odd_flags + (buf * W::NB + b) * 2;
+            if (partial && P.seg.causal &&
+                __builtin_amdgcn_readfirstlane(of[0] | (W::NB == 4 ? 0u : of[1])) != 0) {
+#pragma unroll
+                for (int t = 0; t < W::RT; ++t)
+                    add_values_by_row<T, C>(&R[t], pf[t], key0, limit[t], [&](int j, uint32_t z) {
+                        return *reinterpret_cast<const u32x4*>(
+                            vbuf + ((b * C::NJ + j) * 64 + lane) * 16 + z);
+                    });
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < C::NJ; ++j) {
+                const u32x4 f = *reinterpret_cast<const u32x4*>(
+                    vbuf + ((b * C::NJ + j) * 64 + lane) * 16);
+#pragma unroll
+                for (int t = 0; t < W::RT; ++t) R[t].o[j] = Mma<T>::run(f, pf[t], R[t].o[j]);
+            }
+        }
+        if (more) stage_tile(off_next, buf ^ 1);
+        off_next = off_after;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int t = 0; t < W::RT; ++t)
+        store_rows<T, C>(A, to, R[t], (wave * W::RT + t) * 16 + a, token[t], head[t], live[t]);
+}
+
+// -------------------------------------------------------------- kernel --
+
+__device__ inline int64_t wave_scan(int64_t x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
+struct Plan {
+    int64_t sums[kWaves][2];    // per-wave totals of a chunk
+    int64_t at[2];              // {segment, its start} of this workgroup's first key
+};
+
+// The workgroup's line (0 thin, 1 wide), its piece of it and the segment the
+// piece begins in.  Every workgroup scans all segments (512 at a time); the
+// first one also leaves their starts and the cut for k_attend_join.
+struct Mine {
+    int line;
+    int64_t w, lo, hi;
+    int64_t wgs;
+    int64_t n;
+    int64_t slot0;              // the line's first slot
+    int32_t seg;
+    int64_t seg_start;
+};
+
+__device__ inline int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+    return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+__device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_t grid) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int32_t nseg = A.num_groups + A.num_reqs;
+    int64_t total[2] = {0, 0};
+    int64_t start = 0, cost = 0;            // of this thread's segment in the last chunk
+    bool wide = false;
+    for (int32_t c0 = 0; c0 < nseg; c0 += kThreads) {
+        const int32_t s = c0 + static_cast<int32_t>(threadIdx.x);
+        cost = 0;
+        wide = false;
+        if (s < nseg) {
+            const Seg g = segment(A, s);
+            cost = set_keys(g) * g.sets;
+            wide = g.wide;
+        }
+        const int64_t x = wave_scan(wide ? 0 : cost), y = wave_scan(wide ? cost : 0);
+        if (lane == 63) {
+            L->sums[wave][0] = x;
+            L->sums[wave][1] = y;
+        }
+        __syncthreads();
+        int64_t before[2] = {total[0], total[1]};
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            const int64_t sx = L->sums[v][0], sy = L->sums[v][1];
+            if (v < wave) { before[0] += sx; before[1] += sy; }
+            total[0] += sx;
+            total[1] += sy;
+        }
+        start = wide ? before[1] + y - cost : before[0] + x - cost;
+        if (block == 0 && s < nseg) A.starts[s] = start;
+        __syncthreads();
+    }
+
+    // workgroups per line: by the lines' times, in eights (one per XCD), and
+    // no more than keep a piece at its least length
+    Mine M;
+    int64_t wgs[2];
+    const int64_t least[2] = {A.thin_min, A.wide_min};
+    int64_t share = 0;                      // workgroups of the wide line
+    if (total[1] > 0) {
+        share = grid;
+        if (total[0] > 0) {
+            const float tw = static_cast<float>(total[1]) * A.wide_weight;
+            const float tt = static_cast<float>(total[0]);
+            share = static_cast<int64_t>(grid * (tw / (tw + tt)) / 8.0f + 0.5f) * 8;
+            share = clamp_to(share, 8, static_cast<int64_t>(grid) - 8);
+        }
+    }
+    wgs[0] = grid - share;
+    wgs[1] = share;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t want = ((total[i] + least[i] - 1) / least[i] + 7) / 8 * 8;
+        if (wgs[i] > want) wgs[i] = want;
+    }
+    if (block == 0 && threadIdx.x == 0) {
+        A.plan[0] = total[0];
+        A.plan[1] = wgs[0];
+        A.plan[2] = total[1];
+        A.plan[3] = wgs[1];
+    }
+    // consecutive pieces on one XCD (workgroups are dealt to the eight in turn)
+    const int64_t xcd = block % 8, j = block / 8;
+    M.line = j < wgs[1] / 8 ? 1 : 0;
+    M.wgs = wgs[M.line];
+    M.n = total[M.line];
+    M.slot0 = M.line ? 0 : 2 * wgs[1];
+    const int64_t jj = M.line ? j : j - wgs[1] / 8;
+    M.w = xcd * (M.wgs / 8) + jj;
+    if (jj >= M.wgs / 8) {
+        M.lo = M.hi = 0;
+        return M;
+    }
+    M.lo = piece_start(M.n, M.wgs, M.w);
+    M.hi = piece_start(M.n, M.wgs, M.w + 1);
+    if (M.lo >= M.hi) return M;
+    // the segment that key lo lies in
+    if (nseg > kThreads) {
+        int64_t run = 0;
+        for (int32_t c0 = 0; c0 < nseg; c0 += kThreads) {
+            const int32_t s = c0 + static_cast<int32_t>(threadIdx.x);
+            int64_t cc = 0;
+            if (s < nseg) {
+                const Seg g = segment(A, s);
+                if (g.wide == (M.line == 1)) cc = set_keys(g) * g.sets;
+            }
+            const int64_t x = wave_scan(cc);
+            if (lane == 63) L->sums[wave][0] = x;
+            __syncthreads();
+            int64_t before = run;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) {
+                if (v < wave) before += L->sums[v][0];
+                run += L->sums[v][0];
+            }
+            const int64_t b = before + x - cc;
+            if (cc > 0 && b <= M.lo && M.lo < b + cc) {
+                L->at[0] = s;
+                L->at[1] = b;
+            }
+            __syncthreads();
+            if (run > M.lo) break;
+        }
+    } else {
+        if (cost > 0 && wide == (M.line == 1) && start <= M.lo && M.lo < start + cost) {
+            L->at[0] = threadIdx.x;
+            L->at[1] = start;
+        }
+        __syncthreads();
+    }
+    M.seg = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(L->at[0]));
+    M.seg_start = uniform(L->at[1]);
+    M.lo = uniform(M.lo);
+    M.hi = uniform(M.hi);
+    return M;
+}
+
+// LINES: 1 thin only, 2 wide only, 3 both.
+template <class T, bool FP8, int DP, int LINES>
+constexpr int lds_bytes() {
+    using C = Cfg<T, FP8, DP>;
+    const int thin = (kWaves / 2) * 64 * (4 * C::NJ + 2) * 4;
+    const int wide = Wide<C>::LDS;
+    return LINES == 1 ? thin : (LINES == 2 ? wide : (thin > wide ? thin : wide));
+}
+
+template <class T, bool FP8, int DP, int LINES>
+__global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
+    using C = Cfg<T, FP8, DP>;
+    __shared__ Plan plan;
+    __shared__ __attribute__((aligned(16))) char lds[lds_bytes<T, FP8, DP, LINES>()];
+    const Mine M = plan_work(A, &plan, blockIdx.x, gridDim.x);
+    if (M.lo >= M.hi) return;
+    const bool wide_line = LINES == 2 || (LINES == 3 && M.line == 1);
+    const int32_t nseg = A.num_groups + A.num_reqs;
+    const int64_t round = wide_line ? Wide<C>::KT : kKeys;
+
+    Piece P;
+    int64_t pos = M.lo;                     // on the line
+    int32_t s = M.seg;
+    int64_t seg_start = M.seg_start;
+    while (pos < M.hi && s < nseg) {
+        P.seg = segment(A, s);
+        const int64_t per_set = set_keys(P.seg);
+        const int64_t cost = per_set * P.seg.sets;
+        if (cost == 0 || P.seg.wide != (M.line == 1)) { ++s; continue; }
+        const bool pre = s < A.num_groups;
+        P.lists = pre ? A.pre : A.own;
+        P.pg0 = P.lists.pg_off[pre ? s : s - A.num_groups];
+        while (pos < M.hi && pos < seg_start + cost) {
+            const int64_t x = pos - seg_start;
+            P.set = static_cast<int32_t>(x / per_set);
+            const int64_t y = x - P.set * per_set;
+            // the tile that key y of the head set lies in
+            int32_t lo = 0, hi = P.seg.tiles - 1;
+            if (!P.seg.causal) {
+                lo = static_cast<int32_t>(y / P.seg.base);
+            } else {
+                while (lo < hi) {
+                    const int32_t mid = lo + (hi - lo + 1) / 2;
+                    if (tile_start(P.seg, mid) <= y) lo = mid; else hi = mid - 1;
+                }
+            }
+            P.tile = lo;
+            const int64_t len = tile_keys(P.seg, lo);
+            const int64_t item = seg_start + P.set * per_set + tile_start(P.seg, lo);
+            const int64_t end = M.hi < item + len ? M.hi : item + len;
+            const bool from_start = pos == item, to_end = end == item + len;
+            // cuts inside an item fall on whole steps, both sides alike
+            const int64_t key1 = to_end ? len : (end - item) / round * round;
+            P.key0 = static_cast<int32_t>((pos - item) / round * round);
+            P.key1 = key1 < P.seg.keys ? static_cast<int32_t>(key1) : P.seg.keys;
+            P.counts = P.set == 0 && P.tile == P.seg.tiles - 1;
+            Dest to;
+            if (from_start && to_end) {
+                to.kind = A.num_groups > 0 ? kRowBuffer : kFinal;
+            } else {
+                to.kind = kSlot;
+            }
+            to.part = pre ? 1 : 0;
+            to.slot = static_cast<int32_t>(M.slot0 + 2 * M.w + (from_start ? 1 : 0));
+            if constexpr (LINES != 1)
+                if (wide_line) run_wide<T, C>(A, P, to, lds);
+            if constexpr (LINES != 2)
+                if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(lds));
+            pos = end;
+        }
+        seg_start += cost;
+        ++s;
+    }
+}
+
+// ---------------------------------------------------------------- join --
+
+// The list entry r with off[r] <= x < off[r + 1] (off non-decreasing, n lists),
+// by a 64-way search of the wave.
+__device__ inline int32_t find_list(const int64_t* off, int32_t n, int64_t x) {
+    const int lane = threadIdx.x & 63;
+    int32_t lo = 0, len = n;                // the answer is in [lo, lo + len)
+    while (len > 1) {
+        const int32_t step = (len + 63) / 64;
+        const int32_t at = lo + lane * step;
+        const uint64_t below = __ballot(lane * step < len && off[at < n ? at : n] <= x);
+        const int32_t k = below == 0 ? 0 : 63 - __clzll(below);
+        const int32_t rest = len - k * step;
+        lo += k * step;
+        len = rest < step ? rest : step;
+    }
+    return lo;
+}
+
+// What one part (prefix or own) of a row left, and where.
+struct PartOf {
+    int64_t w0, w1;             // workgroups that have pieces of its item; w0 > w1: none
+    int64_t n, wgs;             // its line
+    int64_t slot0;
+    int32_t slot_row;
+};
+
+__device__ inline PartOf part_of(const Args& A, int32_t s, int32_t token, int32_t head) {
+    PartOf p;
+    p.w0 = 0;
+    p.w1 = -1;
+    const Seg g = segment(A, s);
+    const int line = g.wide ? 1 : 0;
+    p.n = A.plan[2 * line];
+    p.wgs = A.plan[2 * line + 1];
+    p.slot0 = line ? 0 : 2 * A.plan[3];
+    p.slot_row = 0;
+    const int32_t local = token - g.tok0;
+    if (g.tiles == 0 || local < 0 || local >= g.ntok) return p;
+    const int32_t kvh = head / A.G, hin = head % A.G;
+    const int32_t tile = local / g.tp;
+    const int32_t in_tile = local - tile * g.tp;
+    int32_t set;
+    if (g.wide) {
+        set = kvh;
+        p.slot_row = in_tile * A.G + hin;
+    } else {
+        const int32_t sub = hin / A.gv, vh = kvh * A.parts + sub;
+        set = vh / A.hs;
+        p.slot_row = (vh % A.hs) * kThinRows + in_tile * A.gv + hin % A.gv;
+    }
+    const int64_t item = A.starts[s] + set * set_keys(g) + tile_start(g, tile);
+    p.w0 = piece_of(p.n, p.wgs, item);
+    p.w1 = piece_of(p.n, p.wgs, item + tile_keys(g, tile) - 1);
+    return p;
+}
+
+// One wave joins the rows of 256 / DP neighbouring heads of one token: lane
+// holds 4 dims of one of them.  Bound by the partial sums' bytes, which are
+// few beside the keys'; what it costs is its launch and three dependent loads.
+template <class T, int DP>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
+    constexpr int LPR = DP / 4, RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63;
+    const int32_t hq = A.H * A.G;
+    const int32_t per_token = (hq + RPW - 1) / RPW;
+    const int64_t wave = static_cast<int64_t>(blockIdx.x) * kJoinWaves +
+                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave / per_token >= A.T) return;
+    const int32_t token = static_cast<int32_t>(wave / per_token);
+    const int32_t head = static_cast<int32_t>(wave % per_token) * RPW + lane / LPR;
+    const int32_t r = find_list(A.tok_off, A.num_reqs, token);
+    const int32_t gr = A.num_groups > 0 ? find_list(A.grp_off, A.num_groups, r) : 0;
+    const int d = lane % LPR * 4;
+    if (head >= hq) return;
+    const bool has_dims = d < A.D;
+    const int64_t row = static_cast<int64_t>(token) * hq + head;
+
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    auto add = [&](float m2, float l2, const float* src) {
+        if (l2 == 0.0f) return;
+        const f32x4 x = has_dims ? *reinterpret_cast<const f32x4*>(src + d) : f32x4{0, 0, 0, 0};
+        const float top = fmaxf(m, m2);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        const float w1 = __builtin_amdgcn_exp2f(m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
+        m = top;
+        l = l * w1 + l2 * w2;
+        o = o * w1 + x * w2;
+    };
+    const int parts = A.num_groups > 0 ? 2 : 1;
+    for (int k = 0; k < parts; ++k) {
+        const PartOf p = part_of(A, k ? gr : A.num_groups + r, token, head);
+        if (p.w0 > p.w1) continue;
+        if (p.w0 == p.w1) {
+            if (parts == 1) return;             // written by the workgroup that had it all
+            const int64_t at = static_cast<int64_t>(k) * A.T * hq + row;
+            const float2 ml = *reinterpret_cast<const float2*>(A.row_ml + at * 2);
+            add(ml.x, ml.y, A.row_o + at * A.D);
+            continue;
+        }
+#pragma unroll 4
+        for (int64_t w = p.w0; w <= p.w1; ++w) {
+            if (piece_start(p.n, p.wgs, w) >= piece_start(p.n, p.wgs, w + 1)) continue;
+            const int64_t at = (p.slot0 + 2 * w + (w == p.w0 ? 1 : 0)) * A.slot_rows + p.slot_row;
+            const float2 ml = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);
+            add(ml.x, ml.y, A.slot_o + at * A.D);
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : A.v_scale / l;
+    if (has_dims)
+        *reinterpret_cast<u32x2*>(A.out + static_cast<int64_t>(token) * A.out_stride +
+                                  (static_cast<int64_t>(head) * A.D + d) * 2) =
+            u32x2{Mma<T>::pack(o[0] * inv, o[1] * inv), Mma<T>::pack(o[2] * inv, o[3] * inv)};
+    if (d == 0 && A.lse != nullptr)
+        A.lse[row] = l == 0.0f ? -INFINITY
+                               : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+}
+
+}  // namespace attend
+}  // namespace kvx
