@@ -68,6 +68,16 @@ constexpr int kJoinWaves = 4;
 // accumulators are rescaled: weights stay below 2^8, exact in every type here.
 constexpr float kLag = 8.0f;
 
+// The lane, as a value that the compiler does not carry around loops: what is
+// computed from it stays where it is used.  Held over the loops of a piece,
+// lane-dependent addresses and predicates of every path filled the registers
+// and the loops' own values went to scratch memory.
+__device__ inline int here_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 struct Lists {                          // where a kind of segment's keys live
     const int64_t* pg_off;
     const int32_t* ids;
@@ -127,6 +137,16 @@ struct Args {
     int32_t slot_rows;
 };
 
+// A value that is the same in every lane, in a scalar register: what is loaded
+// from memory that the kernel might write comes in vector registers otherwise,
+// and so does all that is computed from it.
+__device__ inline int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ inline int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+    return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
 // ------------------------------------------------------------- segments --
 
 struct Seg {
@@ -168,6 +188,20 @@ __device__ inline Seg segment(const Args& A, int32_t s) {
     g.sets = g.wide ? A.H : A.sets;
     g.tiles = g.keys > 0 ? (g.ntok + g.tp - 1) / g.tp : 0;
     return g;
+}
+
+__device__ inline Seg uniform(const Seg& g) {
+    Seg u;
+    u.tok0 = uniform(g.tok0);
+    u.ntok = uniform(g.ntok);
+    u.keys = uniform(g.keys);
+    u.base = uniform(g.base);
+    u.tiles = uniform(g.tiles);
+    u.tp = uniform(g.tp);
+    u.sets = uniform(g.sets);
+    u.wide = uniform(static_cast<int32_t>(g.wide)) != 0;
+    u.causal = uniform(static_cast<int32_t>(g.causal)) != 0;
+    return u;
 }
 
 // Keys before tile i of a head set, and the keys of tile i (one more row tile
@@ -248,11 +282,11 @@ struct Mma<_Float16> {
     static constexpr uint32_t kExp = 0x7c007c00u;
 };
 
-// Whether either half of w is an infinity or a NaN.
+// w with halves that are an infinity or a NaN cleared.
 template <class T>
-__device__ inline bool odd_pair(uint32_t w) {
-    const uint32_t e = w & Mma<T>::kExp;
-    return (e & 0xffffu) == (Mma<T>::kExp & 0xffffu) || (e >> 16) == (Mma<T>::kExp >> 16);
+__device__ inline uint32_t finite_pair(uint32_t w) {
+    constexpr uint32_t lo = Mma<T>::kExp & 0xffffu, hi = Mma<T>::kExp & 0xffff0000u;
+    return ((w & lo) == lo ? 0u : w & 0xffffu) | ((w & hi) == hi ? 0u : w & 0xffff0000u);
 }
 
 // Shapes of one (query type, pool element, padded head dim) combination.
@@ -357,7 +391,8 @@ template <class C>
 struct Rows {
     float m;                    // reference maximum (log2), the same in a row's four lanes
     float l;                    // this lane's share of the sum
-    f32x4 o[C::NJ];             // o[c * VE + j][r]: dim 16 VE c + (4 g + r) VE + j
+    f32x4 o[C::NJ];             // thin o[c * VE + j][r]: dim 16 VE c + (4 g + r) VE + j
+                                // wide o[j][r]: dim 16 j + 4 g + r
 };
 
 template <class C>
@@ -368,12 +403,15 @@ __device__ inline void clear(Rows<C>* R) {
     for (int j = 0; j < C::NJ; ++j) R->o[j] = f32x4{0, 0, 0, 0};
 }
 
-// Scores s of 32 keys to weights p, with the row's maximum moved and the
-// accumulators rescaled when a score passes it by more than kLag.
-template <class C>
-__device__ inline void weigh(Rows<C>* R, const f32x4 (&s)[2], float scale, float (&p)[8]) {
-    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * scale;
+// Scores s of 32 U keys to weights in the query's type, with the row's maximum
+// moved and the accumulators rescaled when a score passes it by more than kLag.
+template <class T, class C, int U>
+__device__ inline void weigh(Rows<C>* R, const f32x4 (&s)[2 * U], float scale, u32x4 (&pf)[U]) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < 2 * U; ++x)
+        top = fmaxf(fmaxf(fmaxf(top, s[x][0]), s[x][1]), fmaxf(s[x][2], s[x][3]));
+    top *= scale;
     if (__any(top > R->m + kLag)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -387,43 +425,56 @@ __device__ inline void weigh(Rows<C>* R, const f32x4 (&s)[2], float scale, float
     const float m = R->m == -INFINITY ? 0.0f : R->m;
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], scale, -m));
-        sum += p[i];
+    for (int u = 0; u < U; ++u) {
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * u + (i >> 2)][i & 3], scale, -m));
+            sum += p[i];
+        }
+        pf[u] = u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]), Mma<T>::pack(p[4], p[5]),
+                      Mma<T>::pack(p[6], p[7])};
     }
     R->l += sum;
 }
 
-template <class T>
-__device__ inline u32x4 pack_weights(const float (&p)[8]) {
-    return u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]), Mma<T>::pack(p[4], p[5]),
-                 Mma<T>::pack(p[6], p[7])};
-}
-
-// The second product for a step in which some rows do not see a key whose
-// value row holds an infinity or a NaN: in one matrix product 0 times it would
-// reach them.  Row by row, with the keys that the row does not see cleared
-// from the operand, and only the row's own column kept.  `vf(j, z)` is operand
-// j; z is 0, but not known to be: it keeps the operands from being formed
-// ahead of the loop, whose registers the usual path would pay for.
-template <class T, class C, class VF>
-__device__ inline void add_values_by_row(Rows<C>* R, u32x4 pf, int32_t key0, int32_t limit, VF vf) {
-    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+// In a matrix product a weight of 0 times an infinity or a NaN is a NaN, so in
+// steps in which some row does not see some key, values that are not finite
+// are left out of the product.  What they make of the rows that do see them,
+// whose weights are positive, is added here: the value itself.  Rare, and a V
+// row at a time from memory.  Keys [from, to); `limit` is the lane's row's.
+template <class T, class C, bool WIDE>
+__device__ inline void add_not_finite(const Args& A, const Lists& L, int64_t pg0, const char* vhead,
+                                      int32_t from, int32_t to, int32_t limit, Rows<C>* R) {
+    const int g = here_lane() >> 4;
 #pragma unroll 1
-    for (int row = 0; row < 16; ++row) {
-        const int32_t lim = __shfl(limit, row) - key0;
-        uint32_t z = 0;
-        u32x4 keep;
+    for (int32_t t = from; t < to; ++t) {
+        const int64_t off = key_offset(A, L, pg0, t);
+        if (off < 0) continue;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int key = (p >> 1) * 16 + 4 * g + (p & 1) * 2;
-            keep[p] = (key < lim ? 0xffffu : 0u) | (key + 1 < lim ? 0xffff0000u : 0u);
-        }
+        for (int x = 0; x < C::NJ; ++x) {
+            // four dims in a run, as store_rows has them
+            constexpr int Q = C::VE / 4;
+            const int c = x / (4 * Q), r = x / Q % 4, j = c * C::VE + x % Q * 4;
+            const int d = WIDE ? x * 16 + 4 * g : c * 16 * C::VE + (4 * g + r) * C::VE + x % Q * 4;
+            if (d >= A.D || t >= limit) continue;
+            uint32_t w[2];
+            if constexpr (C::EB == 2) {
+                const u32x2 y = *reinterpret_cast<const u32x2*>(vhead + off + d * 2);
+                w[0] = y.x;
+                w[1] = y.y;
+            } else {
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(vhead + off + d);
+                w[0] = Mma<T>::template from_fp8<false>(y);
+                w[1] = Mma<T>::template from_fp8<true>(y);
+            }
 #pragma unroll
-        for (int j = 0; j < C::NJ; ++j) {
-            asm volatile("" : "+v"(z) : "v"(R->o[j > 0 ? j - 1 : 0][0]));
-            const f32x4 d = Mma<T>::run(vf(j, z) & keep, pf, f32x4{0, 0, 0, 0});
-            if (a == row) R->o[j] += d;
+            for (int i = 0; i < 4; ++i) {
+                const float v = i & 1 ? Mma<T>::hi(w[i >> 1]) : Mma<T>::lo(w[i >> 1]);
+                float* o = WIDE ? &reinterpret_cast<float*>(&R->o[x])[i]
+                                : &reinterpret_cast<float*>(&R->o[j + i])[r];
+                if (!__builtin_isfinite(v)) *o += v;
+            }
         }
     }
 }
@@ -439,63 +490,56 @@ struct Dest {
     int part;                   // kRowBuffer: 0 own, 1 prefix
 };
 
-template <class T, class C>
+template <class T, class C, bool WIDE>
 __device__ inline void store_rows(const Args& A, const Dest& to, const Rows<C>& R, int slot_row,
                                   int32_t token, int32_t head, bool live) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const int lane = here_lane(), g = lane >> 4;
     float l = R.l;
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     if (!live) return;
-    const int64_t hq = static_cast<int64_t>(A.H) * A.G;
+    // runs of 4 dims: f(dim, values)
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int x = 0; x < C::NJ; ++x) {
+            if constexpr (WIDE) {
+                f(x * 16 + 4 * g, R.o[x]);
+            } else {
+                constexpr int Q = C::VE / 4;                // runs of a row r of a chunk
+                const int c = x / (4 * Q), r = x / Q % 4, j = c * C::VE + x % Q * 4;
+                f(c * 16 * C::VE + (4 * g + r) * C::VE + x % Q * 4,
+                  f32x4{R.o[j][r], R.o[j + 1][r], R.o[j + 2][r], R.o[j + 3][r]});
+            }
+        }
+    };
+    const int64_t out_row = static_cast<int64_t>(token) * A.H * A.G + head;
     if (to.kind == kFinal) {
         const float inv = l == 0.0f ? 0.0f : A.v_scale / l;
         char* row = A.out + static_cast<int64_t>(token) * A.out_stride + static_cast<int64_t>(head) * A.D * 2;
-#pragma unroll
-        for (int c = 0; c < C::NC; ++c)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = c * 16 * C::VE + (4 * g + r) * C::VE;
-                if (d >= A.D) continue;
-                uint32_t w[C::VE / 2];
-#pragma unroll
-                for (int j = 0; j < C::VE; j += 2)
-                    w[j / 2] = Mma<T>::pack(R.o[c * C::VE + j][r] * inv,
-                                            R.o[c * C::VE + j + 1][r] * inv);
-                if constexpr (C::VE == 8)
-                    *reinterpret_cast<u32x4*>(row + d * 2) = u32x4{w[0], w[1], w[2], w[3]};
-                else
-                    *reinterpret_cast<u32x2*>(row + d * 2) = u32x2{w[0], w[1]};
-            }
+        each([&](int d, const f32x4& x) {
+            if (d < A.D)
+                *reinterpret_cast<u32x2*>(row + d * 2) =
+                    u32x2{Mma<T>::pack(x[0] * inv, x[1] * inv), Mma<T>::pack(x[2] * inv, x[3] * inv)};
+        });
         if (g == 0 && A.lse != nullptr)
-            A.lse[static_cast<int64_t>(token) * hq + head] =
+            A.lse[out_row] =
                 l == 0.0f ? -INFINITY : (R.m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
         return;
     }
-    int64_t row;
     float *o, *ml;
     if (to.kind == kSlot) {
-        row = static_cast<int64_t>(to.slot) * A.slot_rows + slot_row;
+        const int64_t row = static_cast<int64_t>(to.slot) * A.slot_rows + slot_row;
         o = A.slot_o + row * A.D;
         ml = A.slot_ml + row * 2;
     } else {
-        row = (static_cast<int64_t>(to.part) * A.T + token) * hq + head;
+        const int64_t row = static_cast<int64_t>(to.part) * A.T * A.H * A.G + out_row;
         o = A.row_o + row * A.D;
         ml = A.row_ml + row * 2;
     }
     if (g == 0) *reinterpret_cast<float2*>(ml) = make_float2(R.m, l);
-#pragma unroll
-    for (int c = 0; c < C::NC; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = c * 16 * C::VE + (4 * g + r) * C::VE;
-            if (d >= A.D) continue;
-#pragma unroll
-            for (int j = 0; j < C::VE; j += 4)
-                *reinterpret_cast<f32x4*>(o + d + j) =
-                    f32x4{R.o[c * C::VE + j][r], R.o[c * C::VE + j + 1][r],
-                          R.o[c * C::VE + j + 2][r], R.o[c * C::VE + j + 3][r]};
-        }
+    each([&](int d, const f32x4& x) {
+        if (d < A.D) *reinterpret_cast<f32x4*>(o + d) = x;
+    });
 }
 
 // --------------------------------------------------------------- thin --
@@ -528,7 +572,7 @@ __device__ inline void count_skipped(const Args& A, const Piece& P, int wave) {
 template <class T, class C>
 __device__ inline void load_q(const Args& A, u32x4 (&q)[C::KS], int32_t token, int32_t head,
                               bool live) {
-    const int g = (threadIdx.x & 63) >> 4;
+    const int g = here_lane() >> 4;
     const char* row = A.q + static_cast<int64_t>(token) * A.q_stride + static_cast<int64_t>(head) * A.D * 2;
 #pragma unroll
     for (int ks = 0; ks < C::KS; ++ks) {
@@ -552,18 +596,19 @@ __device__ inline void scores(const u32x4 (&q)[C::KS], f32x4 (&s)[2], KF kf) {
 
 // Keys this lane's row does not see get -inf: key index key0 + ..., seen below
 // `limit` and where `valid` has its bit.
-__device__ inline void mask_scores(f32x4 (&s)[2], int32_t key0, int32_t limit, uint32_t valid) {
-    const int g = (threadIdx.x & 63) >> 4;
+__device__ inline void mask_scores(f32x4* s, int32_t key0, int32_t limit, uint32_t valid) {
+    const int g = here_lane() >> 4;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int key = (i >> 2) * 16 + 4 * g + (i & 3);
-        if (key0 + key >= limit || !((valid >> key) & 1)) s[i >> 2][i & 3] = -INFINITY;
+        const bool seen = (key0 + key < limit) & (((valid >> key) & 1) != 0);
+        s[i >> 2][i & 3] = seen ? s[i >> 2][i & 3] : -INFINITY;
     }
 }
 
 template <class T, class C>
 __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* lds) {
-    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = wave % A.hs, part = wave / A.hs;
     const int32_t vh = P.set * A.hs + h;                  // thin head
@@ -621,17 +666,19 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             }
         };
         // operands of products 2 w and 2 w + 1 of chunk c
-        auto value_pair = [&](int c, int w, uint32_t z, u32x4* even, u32x4* odd) {
+        auto value_pair = [&](int c, int w, u32x4* even, u32x4* odd) {
             uint32_t y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t x[C::VE / 2];
                 v_pairs<T, C>(vr[i][c], x);
-                y[i] = x[w] ^ z;
+                y[i] = x[w];
             }
             v_transpose(y, even, odd);
         };
 
+        bool odd = false;               // a value left out of a product
+        int32_t first_edge = -1;        // this wave's first step that not all rows see whole
         int32_t key0 = P.key0 + part * kKeys;
         int64_t off = key0 < P.key1 ? offset_of(key0) : -1;
         if (AHEAD && key0 < P.key1) {
@@ -650,8 +697,8 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             const int64_t off_after = key0 + 2 * step < P.key1 ? offset_of(key0 + 2 * step) : -1;
             const bool partial = all_see < key0 + kKeys;
             if (valid != 0xffffffffu || partial) mask_scores(s, key0, limit, valid);
-            float p[8];
-            weigh<C>(&R, s, A.scale, p);
+            u32x4 pf[1];
+            weigh<T, C, 1>(&R, s, A.scale, pf);
             if (valid != 0xffffffffu) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -661,39 +708,41 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
 #pragma unroll
                             for (int w = 0; w < C::VW; ++w) vr[i][c].w[w] = 0;
             }
-            bool odd = false;
             if (partial && P.seg.causal) {
-                bool mine = false;
+                if (first_edge < 0) first_edge = key0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int c = 0; c < C::NC; ++c) {
-                        uint32_t x[C::VE / 2];
-                        v_pairs<T, C>(vr[i][c], x);
-#pragma unroll
-                        for (int w = 0; w < C::VE / 2; ++w) mine |= odd_pair<T>(x[w]);
-                    }
-                odd = __any(mine);
-            }
-            const u32x4 pf = pack_weights<T>(p);
-            if (odd) {
-                add_values_by_row<T, C>(&R, pf, key0, limit, [&](int j, uint32_t z) {
+                for (int j = 0; j < C::NJ; j += 2) {
                     u32x4 f[2];
-                    value_pair(j / C::VE, j % C::VE / 2, z, &f[0], &f[1]);
-                    return f[j & 1];
-                });
+                    value_pair(j / C::VE, j % C::VE / 2, &f[0], &f[1]);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t w = finite_pair<T>(f[z][y]);
+                            odd = odd || w != f[z][y];
+                            f[z][y] = w;
+                        }
+                    R.o[j] = Mma<T>::run(f[0], pf[0], R.o[j]);
+                    R.o[j + 1] = Mma<T>::run(f[1], pf[0], R.o[j + 1]);
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < C::NJ; j += 2) {
                     u32x4 f[2];
-                    value_pair(j / C::VE, j % C::VE / 2, 0, &f[0], &f[1]);
-                    R.o[j] = Mma<T>::run(f[0], pf, R.o[j]);
-                    R.o[j + 1] = Mma<T>::run(f[1], pf, R.o[j + 1]);
+                    value_pair(j / C::VE, j % C::VE / 2, &f[0], &f[1]);
+                    R.o[j] = Mma<T>::run(f[0], pf[0], R.o[j]);
+                    R.o[j + 1] = Mma<T>::run(f[1], pf[0], R.o[j + 1]);
                 }
             }
             if (AHEAD && more) load_values(off_next);
             off = off_next;
             off_next = off_after;
+        }
+        if (__any(odd)) {
+            // the wave's own steps only: `step` apart
+            for (int32_t t = first_edge; t < P.key1; t += step)
+                add_not_finite<T, C, false>(A, P.lists, P.pg0, vhd, t,
+                                            t + kKeys < P.key1 ? t + kKeys : P.key1, limit, &R);
         }
     }
 
@@ -725,236 +774,365 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
         }
         n = half;
     }
-    if (works && part == 0) store_rows<T, C>(A, to, R, h * kThinRows + a, token, head, live);
+    if (works && part == 0) store_rows<T, C, false>(A, to, R, h * kThinRows + a, token, head, live);
     if (A.kp > 1) __syncthreads();
 }
 
 // ---------------------------------------------------------------- wide --
 
-// A wide tile's shapes: RT row tiles of 16 per wave, KT keys staged at a time.
+// A wide tile's shapes: RT row tiles of 16 per wave, KT keys staged at a time
+// in one of two buffers, U steps of 32 keys computed together.
 template <class C>
 struct Wide {
     static constexpr int DP = C::KS * 32;
     static constexpr int RT = DP <= 128 ? 2 : 1;
     static constexpr int ROWS = kWaves * 16 * RT;
     static constexpr int KT = DP <= 128 ? 128 : 64;
+    static constexpr int U = DP <= 128 ? 2 : 1;
     static constexpr int NB = KT / kKeys;               // steps of 32 keys
+    static constexpr int KW = KT / 4;                   // keys that a wave stages
     static constexpr int KF = (KT / 16) * C::KS;        // K fragments of 1 KiB
-    static constexpr int VF = NB * C::NJ;               // V fragments
-    static constexpr int BUF = (KF + VF) * 1024;
-    static constexpr int LDS = 2 * BUF + 2 * NB * 12;
+    static constexpr int RB = DP * 2;                   // bytes of a V row
+    static constexpr int BUF = KF * 1024 + KT * RB;
+};
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+// 16 bytes per lane from memory to base + 16 * lane of shared memory.
+__device__ inline void load_to_lds(const char* src, char* base) {
+    __builtin_amdgcn_global_load_lds(
+        (const __attribute__((address_space(1))) uint32_t*)src,
+        (__attribute__((address_space(3))) uint32_t*)base, 16, 0, 0);
+}
+
+// V stands in shared memory row by row, its 32-byte pairs of 16-byte chunks
+// permuted by row so that the 4 rows x 32 bytes that 16 lanes read together,
+// and those of the next 16, lie in different banks.
+template <class C>
+__device__ inline int v_swizzle(int row) {
+    return (C::KS == 2 ? (row >> 1) & 3 : row & 7) << 1;
+}
+
+// Operand of the second product for 32 keys from row0 and dims 16 j .. 16 j +
+// 15: two transposing reads, each of 4 keys (rows 4 g + 0..3 of a 16-key tile)
+// for the lane's dim.
+// `at` is v_base's offset; chunk pair j differs from it in the bits of 32 j.
+template <class C>
+__device__ inline int v_base() {
+    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
+    const int row = 4 * g + (a >> 2);
+    return row * (C::KS * 64) + ((((a >> 1) & 1) ^ v_swizzle<C>(row)) * 16) + (a & 1) * 8;
+}
+
+template <class C>
+__device__ inline u32x4 v_frag(const char* v, int at, int step, int j) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    constexpr int RB = C::KS * 64;
+    const char* p = v + (at ^ (j << 5)) + step * 32 * RB;
+    const u32x2 lo = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+    const u32x2 hi = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * RB)));
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// Keys [tile0, tile0 + KT) of a piece on their way to a buffer: waves 0-3
+// stage K, 4-7 V, KT / 4 keys each.  16-bit values go from memory to shared
+// memory directly; fp8 ones through registers, where they are converted.
+template <class T, class C>
+struct Stage {
+    using W = Wide<C>;
+    static constexpr int N = C::EB == 2 ? 1 : W::KW * W::DP / 1024;   // 16-byte loads per lane
+    int64_t off;                        // the row offset of key kw * KW + lane % KW, or -1
+    u32x4 raw[N];
 };
 
 template <class T, class C>
-__device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* lds) {
+__device__ inline int64_t stage_offset(const Args& A, const Piece& P, int32_t tile0, int wave) {
     using W = Wide<C>;
-    const int lane = threadIdx.x & 63, a = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63;
+    const int32_t t = tile0 + (wave & 3) * W::KW + (lane & (W::KW - 1));
+    return t < P.key1 ? key_offset(A, P.lists, P.pg0, t) : -1;
+}
+
+template <class T, class C>
+__device__ inline void stage_load(const Args& A, Stage<T, C>* S, const char* kh, const char* vhd,
+                                  int wave, char* buf, uint32_t* flags) {
+    using W = Wide<C>;
+    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
+    const int kw = wave & 3;
+    const uint64_t seen = __ballot(S->off >= 0);
+    const bool whole = seen == ~0ull && A.D == W::DP;       // every lane loads
+    if (wave < 4) {
+        // flag kw * KW / 32: which of a step's keys are there (half a word each for KW = 16)
+        if (lane == 0) {
+            if constexpr (W::KW == 32) flags[kw] = static_cast<uint32_t>(seen);
+            else reinterpret_cast<uint16_t*>(flags)[kw] = static_cast<uint16_t>(seen);
+        }
+        if constexpr (C::EB == 2) {
+#pragma unroll
+            for (int x = 0; x < W::KW / 16; ++x) {
+                const int64_t off = __shfl(S->off, x * 16 + a);
+                const char* src = kh + off + g * 16;
+                char* to = buf + (kw * (W::KW / 16) + x) * C::KS * 1024;
+                if (whole) {
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks) load_to_lds(src + ks * 64, to + ks * 1024);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks) {
+                        if (off >= 0 && ks * 32 + g * 8 < A.D)
+                            load_to_lds(src + ks * 64, to + ks * 1024);
+                        else
+                            *reinterpret_cast<u32x4*>(to + ks * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < W::KW / 16; ++x) {
+                const int64_t off = __shfl(S->off, x * 16 + a);
+#pragma unroll
+                for (int y = 0; y < C::NK; ++y) {
+                    const int b = y * 64 + g * 16;
+                    S->raw[x * C::NK + y] = u32x4{0, 0, 0, 0};
+                    if (off >= 0 && b < A.D)
+                        S->raw[x * C::NK + y] = *reinterpret_cast<const u32x4*>(kh + off + b);
+                }
+            }
+        }
+    } else {
+        char* v = buf + W::KF * 1024 + kw * W::KW * W::RB;
+        if constexpr (C::EB == 2) {
+            constexpr int LPR = W::RB / 16, RPP = 64 / LPR;  // lanes per row, rows per load
+#pragma unroll
+            for (int i = 0; i < W::KW / RPP; ++i) {
+                const int row = i * RPP + lane / LPR;
+                const int64_t off = __shfl(S->off, row);
+                const int chunk = (lane % LPR) ^ v_swizzle<C>(row);
+                const char* src = vhd + off + chunk * 16;
+                char* to = v + i * 1024;
+                if (whole) {
+                    load_to_lds(src, to);
+                } else {
+                    if (off >= 0 && chunk * 8 < A.D)
+                        load_to_lds(src, to);
+                    else
+                        *reinterpret_cast<u32x4*>(to + lane * 16) = u32x4{0, 0, 0, 0};
+                }
+            }
+        } else {
+            constexpr int LPR = W::DP / 16, RPP = 64 / LPR;
+#pragma unroll
+            for (int i = 0; i < W::KW / RPP; ++i) {
+                const int64_t off = __shfl(S->off, i * RPP + lane / LPR);
+                const int b = lane % LPR * 16;
+                S->raw[i] = u32x4{0, 0, 0, 0};
+                if (off >= 0 && b < A.D) S->raw[i] = *reinterpret_cast<const u32x4*>(vhd + off + b);
+            }
+        }
+    }
+}
+
+// 8 fp8 values as 8 of the query's type.
+template <class T>
+__device__ inline u32x4 widen(uint32_t lo, uint32_t hi) {
+    return u32x4{Mma<T>::template from_fp8<false>(lo), Mma<T>::template from_fp8<true>(lo),
+                 Mma<T>::template from_fp8<false>(hi), Mma<T>::template from_fp8<true>(hi)};
+}
+
+template <class T, class C>
+__device__ inline void stage_store(const Stage<T, C>& S, int wave, char* buf) {
+    if constexpr (C::EB == 1) {
+        using W = Wide<C>;
+        const int lane = here_lane();
+        const int kw = wave & 3;
+        if (wave < 4) {
+            char* to = buf + kw * (W::KW / 16) * C::KS * 1024 + lane * 16;
+#pragma unroll
+            for (int x = 0; x < W::KW / 16 * C::NK; ++x) {
+                *reinterpret_cast<u32x4*>(to + 2 * x * 1024) = widen<T>(S.raw[x].x, S.raw[x].y);
+                *reinterpret_cast<u32x4*>(to + (2 * x + 1) * 1024) = widen<T>(S.raw[x].z, S.raw[x].w);
+            }
+        } else {
+            constexpr int LPR = W::DP / 16, RPP = 64 / LPR;
+            char* v = buf + W::KF * 1024 + kw * W::KW * W::RB;
+#pragma unroll
+            for (int i = 0; i < W::KW / RPP; ++i) {
+                const int row = i * RPP + lane / LPR;
+                char* to = v + row * W::RB;
+                const int c = 2 * (lane % LPR), sw = v_swizzle<C>(row);
+                *reinterpret_cast<u32x4*>(to + ((c ^ sw) * 16)) = widen<T>(S.raw[i].x, S.raw[i].y);
+                *reinterpret_cast<u32x4*>(to + (((c + 1) ^ sw) * 16)) = widen<T>(S.raw[i].z, S.raw[i].w);
+            }
+        }
+    }
+}
+
+template <class T, class C>
+struct WideState {
+    using W = Wide<C>;
+    int32_t limit[W::RT];
+    u32x4 q[W::RT][C::KS];
+    Rows<C> R[W::RT];
+    int32_t most, all_see;
+    int32_t first_edge;                 // first step that not all rows see whole, or -1
+    bool odd;                           // a value left out of a product
+};
+
+// The keys of one buffer against the wave's rows.
+template <class T, class C>
+__device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>* S, int32_t tile0,
+                                 const char* buf, const uint32_t* flags) {
+    using W = Wide<C>;
+    const int lane = threadIdx.x & 63;
+    const char* v = buf + W::KF * 1024;
+#pragma unroll 1
+    for (int b = 0; b < W::NB; b += W::U) {
+        const int32_t key0 = tile0 + b * kKeys;
+        if (key0 >= S->most) break;
+        const bool edge = S->all_see < key0 + W::U * kKeys;     // some row does not see some key
+        bool masked = edge;
+        uint32_t valid[W::U];
+#pragma unroll
+        for (int u = 0; u < W::U; ++u) {
+            valid[u] = __builtin_amdgcn_readfirstlane(flags[b + u]);
+            masked = masked || valid[u] != 0xffffffffu;
+        }
+        f32x4 s[W::RT][2 * W::U];
+#pragma unroll
+        for (int x = 0; x < 2 * W::U; ++x) {
+#pragma unroll
+            for (int t = 0; t < W::RT; ++t) s[t][x] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int ks = 0; ks < C::KS; ++ks) {
+                const u32x4 f = *reinterpret_cast<const u32x4*>(
+                    buf + (((b * 2 + x) * C::KS + ks) * 64 + lane) * 16);
+#pragma unroll
+                for (int t = 0; t < W::RT; ++t) s[t][x] = Mma<T>::run(f, S->q[t][ks], s[t][x]);
+            }
+        }
+        u32x4 pf[W::RT][W::U];
+#pragma unroll
+        for (int t = 0; t < W::RT; ++t) {
+            if (masked) {
+#pragma unroll
+                for (int u = 0; u < W::U; ++u)
+                    mask_scores(&s[t][2 * u], key0 + u * kKeys, S->limit[t], valid[u]);
+            }
+            weigh<T, C, W::U>(&S->R[t], s[t], A.scale, pf[t]);
+        }
+        const int vb = v_base<C>();
+        if (edge && P.seg.causal) {
+            if (S->first_edge < 0) S->first_edge = key0;
+#pragma unroll
+            for (int u = 0; u < W::U; ++u)
+#pragma unroll
+                for (int j = 0; j < C::NJ; ++j) {
+                    u32x4 f = v_frag<C>(v, vb, b + u, j);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t w = finite_pair<T>(f[y]);
+                        S->odd = S->odd || w != f[y];
+                        f[y] = w;
+                    }
+#pragma unroll
+                    for (int t = 0; t < W::RT; ++t)
+                        S->R[t].o[j] = Mma<T>::run(f, pf[t][u], S->R[t].o[j]);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < W::U; ++u)
+#pragma unroll
+                for (int j = 0; j < C::NJ; ++j) {
+                    const u32x4 f = v_frag<C>(v, vb, b + u, j);
+#pragma unroll
+                    for (int t = 0; t < W::RT; ++t)
+                        S->R[t].o[j] = Mma<T>::run(f, pf[t][u], S->R[t].o[j]);
+                }
+        }
+    }
+}
+
+// flags: [2][NB] words, a bit per key that is there.
+template <class T, class C>
+__device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* buf0, char* buf1,
+                         uint32_t* flags) {
+    using W = Wide<C>;
+    const int lane = here_lane(), a = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t kvh = P.set;
     count_skipped(A, P, wave);
 
-    int32_t token[W::RT], head[W::RT], limit[W::RT];
-    bool live[W::RT];
-    u32x4 q[W::RT][C::KS];
-    Rows<C> R[W::RT];
+    const char* kh = A.k + kvh * A.head_stride;
+    const char* vhd = A.v + kvh * A.head_stride;
+    Stage<T, C> next;
+    next.off = stage_offset<T, C>(A, P, P.key0, wave);
+    stage_load<T, C>(A, &next, kh, vhd, wave, buf0, flags);
+
+    WideState<T, C> S;
     const int32_t at = P.tile * A.wide_tokens, past = P.seg.keys - P.seg.ntok;
     const int32_t first = at + wave * 16 * W::RT / A.G;     // this wave's first and last token
     int32_t last = at + (wave * 16 * W::RT + 16 * W::RT - 1) / A.G;
     if (last > P.seg.ntok - 1) last = P.seg.ntok - 1;
     // keys that some row of this wave sees, and that every one does
-    int32_t most = P.key1, all_see = P.key1;
+    S.most = S.all_see = P.key1;
+    S.first_edge = -1;
+    S.odd = false;
     if (P.seg.causal) {
-        if (past + last + 1 < most) most = past + last + 1;
-        all_see = past + first + 1;
+        if (past + last + 1 < S.most) S.most = past + last + 1;
+        S.all_see = past + first + 1;
     }
-    if (first >= P.seg.ntok) most = 0;                      // no rows
+    if (first >= P.seg.ntok) S.most = 0;                    // no rows
+    auto row_of = [&](int t, int32_t* local, int32_t* head) {
+        const int row = (wave * W::RT + t) * 16 + a;
+        *local = at + row / A.G;
+        *head = kvh * A.G + row % A.G;
+        return row < A.wide_tokens * A.G && *local < P.seg.ntok;
+    };
 #pragma unroll
     for (int t = 0; t < W::RT; ++t) {
-        const int row = (wave * W::RT + t) * 16 + a;
-        const int32_t local = at + row / A.G;
-        live[t] = row < A.wide_tokens * A.G && local < P.seg.ntok;
-        token[t] = P.seg.tok0 + local;
-        head[t] = kvh * A.G + row % A.G;
-        limit[t] = P.key1;
-        if (live[t] && P.seg.causal && past + local + 1 < limit[t]) limit[t] = past + local + 1;
-        load_q<T, C>(A, q[t], token[t], head[t], live[t]);
-        clear(&R[t]);
+        int32_t local, head;
+        const bool live = row_of(t, &local, &head);
+        S.limit[t] = P.key1;
+        if (live && P.seg.causal && past + local + 1 < S.limit[t]) S.limit[t] = past + local + 1;
+        load_q<T, C>(A, S.q[t], P.seg.tok0 + local, head, live);
+        clear(&S.R[t]);
     }
 
-    const char* kh = A.k + kvh * A.head_stride;
-    const char* vhd = A.v + kvh * A.head_stride;
-    uint32_t* flags = reinterpret_cast<uint32_t*>(lds + 2 * W::BUF);   // [2][NB]: valid keys
-    uint32_t* odd_flags = flags + 2 * W::NB;                // [2][NB][2]: by staging wave
-
-    // Staging: waves 0-3 take K (KT / 4 keys each), waves 4-7 V (one step's
-    // keys, or half of its chunks, each).
-    constexpr int KPW = W::KT / 64;                       // K tiles per staging wave
-    constexpr int CPW = W::NB == 4 ? C::NC : 1;           // V chunks per staging wave
-    const bool stages_k = wave < 4;
-    const int vb = W::NB == 4 ? wave - 4 : (wave - 4) >> 1;
-    const int vc = W::NB == 4 ? 0 : (wave - 4) & 1;
-    constexpr int RAW_K = KPW * C::NK * 4, RAW_V = 8 * CPW * C::VW;
-    uint32_t raw[RAW_K > RAW_V ? RAW_K : RAW_V];          // of either kind of staging wave
-    auto offset_of = [&](int32_t tile0) -> int64_t {
-        const int32_t t = tile0 + (stages_k ? wave * (W::KT / 4) + (lane & (W::KT / 4 - 1))
-                                            : vb * kKeys + (lane & 31));
-        return t < P.key1 ? key_offset(A, P.lists, P.pg0, t) : -1;
-    };
-    auto load_tile = [&](int64_t off) {
-        const int64_t safe = off < 0 ? 0 : off;
-        if (stages_k) {
-#pragma unroll
-            for (int x = 0; x < KPW; ++x) {
-                KTile<C> kt;
-                load_k<C>(&kt, kh + __shfl(safe, x * 16 + a), g, A.D);
-#pragma unroll
-                for (int y = 0; y < C::NK; ++y)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) raw[(x * C::NK + y) * 4 + z] = kt.raw[y][z];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const char* row = vhd + __shfl(safe, (i >> 2) * 16 + 4 * g + (i & 3));
-#pragma unroll
-                for (int c = 0; c < CPW; ++c) {
-                    const int d = ((vc + c) * 16 + a) * C::VE;
-                    const Words<C::VW> w = load_words<C::VW>(row + (d < A.D ? d * C::EB : 0));
-#pragma unroll
-                    for (int z = 0; z < C::VW; ++z) raw[(i * CPW + c) * C::VW + z] = w.w[z];
-                }
-            }
-        }
-    };
-    auto stage_tile = [&](int64_t off, int buf) {
-        char* kb = lds + buf * W::BUF;
-        char* vbuf = kb + W::KF * 1024;
-        if (stages_k) {
-#pragma unroll
-            for (int x = 0; x < KPW; ++x) {
-                KTile<C> kt;
-#pragma unroll
-                for (int y = 0; y < C::NK; ++y)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) kt.raw[y][z] = raw[(x * C::NK + y) * 4 + z];
-#pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks)
-                    *reinterpret_cast<u32x4*>(kb + (((wave * KPW + x) * C::KS + ks) * 64 + lane) * 16) =
-                        k_frag<T, C>(kt, ks, g, A.D);
-            }
-        } else {
-            const uint32_t valid = static_cast<uint32_t>(__ballot(off >= 0));
-            bool mine = false;
-#pragma unroll
-            for (int c = 0; c < CPW; ++c) {
-                uint32_t x[8][C::VE / 2];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    Words<C::VW> w;
-#pragma unroll
-                    for (int z = 0; z < C::VW; ++z) w.w[z] = raw[(i * CPW + c) * C::VW + z];
-                    v_pairs<T, C>(w, x[i]);
-                }
-                if (valid != 0xffffffffu) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (!((valid >> ((i >> 2) * 16 + 4 * g + (i & 3))) & 1))
-#pragma unroll
-                            for (int w = 0; w < C::VE / 2; ++w) x[i][w] = 0;
-                }
-                if (P.seg.causal) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int w = 0; w < C::VE / 2; ++w) mine |= odd_pair<T>(x[i][w]);
-                }
-#pragma unroll
-                for (int w = 0; w < C::VE / 2; ++w) {
-                    const uint32_t y[8] = {x[0][w], x[1][w], x[2][w], x[3][w],
-                                           x[4][w], x[5][w], x[6][w], x[7][w]};
-                    u32x4 even, oddv;
-                    v_transpose(y, &even, &oddv);
-                    char* to = vbuf + ((vb * C::NJ + (vc + c) * C::VE + 2 * w) * 64 + lane) * 16;
-                    *reinterpret_cast<u32x4*>(to) = even;
-                    *reinterpret_cast<u32x4*>(to + 1024) = oddv;
-                }
-            }
-            const bool odd = __any(mine);
-            if (lane == 0) {
-                if (vc == 0) flags[buf * W::NB + vb] = valid;
-                odd_flags[(buf * W::NB + vb) * 2 + vc] = odd ? 1u : 0u;
-            }
-        }
-    };
-
-    int64_t off = offset_of(P.key0);
-    load_tile(off);
-    int64_t off_next = offset_of(P.key0 + W::KT);
-    stage_tile(off, 0);
+    stage_store<T, C>(next, wave, buf0);
+    next.off = stage_offset<T, C>(A, P, P.key0 + W::KT, wave);
     __syncthreads();
-    int buf = 0;
-    for (int32_t tile0 = P.key0; tile0 < P.key1; tile0 += W::KT, buf ^= 1) {
+    // one tile: the next one is on its way to the other buffer meanwhile
+    auto turn = [&](int32_t tile0, char* here, char* there, uint32_t* fh, uint32_t* ft) {
         const bool more = tile0 + W::KT < P.key1;
-        int64_t off_after = -1;
+        int64_t after = -1;
         if (more) {
-            load_tile(off_next);
-            off_after = offset_of(tile0 + 2 * W::KT);
+            stage_load<T, C>(A, &next, kh, vhd, wave, there, ft);
+            after = stage_offset<T, C>(A, P, tile0 + 2 * W::KT, wave);
         }
-        const char* kb = lds + buf * W::BUF;
-        const char* vbuf = kb + W::KF * 1024;
-#pragma unroll 1
-        for (int b = 0; b < W::NB; ++b) {
-            const int32_t key0 = tile0 + b * kKeys;
-            if (key0 >= most) break;
-            const uint32_t valid = __builtin_amdgcn_readfirstlane(flags[buf * W::NB + b]);
-            const bool partial = all_see < key0 + kKeys;
-            f32x4 s[W::RT][2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                for (int t = 0; t < W::RT; ++t) s[t][x] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks) {
-                    const u32x4 f = *reinterpret_cast<const u32x4*>(
-                        kb + (((b * 2 + x) * C::KS + ks) * 64 + lane) * 16);
-#pragma unroll
-                    for (int t = 0; t < W::RT; ++t) s[t][x] = Mma<T>::run(f, q[t][ks], s[t][x]);
-                }
-            }
-            u32x4 pf[W::RT];
-#pragma unroll
-            for (int t = 0; t < W::RT; ++t) {
-                if (valid != 0xffffffffu || partial) mask_scores(s[t], key0, limit[t], valid);
-                float p[8];
-                weigh<C>(&R[t], s[t], A.scale, p);
-                pf[t] = pack_weights<T>(p);
-            }
-            const uint32_t* of = odd_flags + (buf * W::NB + b) * 2;
-            if (partial && P.seg.causal &&
-                __builtin_amdgcn_readfirstlane(of[0] | (W::NB == 4 ? 0u : of[1])) != 0) {
-#pragma unroll
-                for (int t = 0; t < W::RT; ++t)
-                    add_values_by_row<T, C>(&R[t], pf[t], key0, limit[t], [&](int j, uint32_t z) {
-                        return *reinterpret_cast<const u32x4*>(
-                            vbuf + ((b * C::NJ + j) * 64 + lane) * 16 + z);
-                    });
-                continue;
-            }
-#pragma unroll
-            for (int j = 0; j < C::NJ; ++j) {
-                const u32x4 f = *reinterpret_cast<const u32x4*>(
-                    vbuf + ((b * C::NJ + j) * 64 + lane) * 16);
-#pragma unroll
-                for (int t = 0; t < W::RT; ++t) R[t].o[j] = Mma<T>::run(f, pf[t], R[t].o[j]);
-            }
-        }
-        if (more) stage_tile(off_next, buf ^ 1);
-        off_next = off_after;
+        wide_tile<T, C>(A, P, &S, tile0, here, fh);
+        if (more) stage_store<T, C>(next, wave, there);
+        next.off = after;
         __syncthreads();
+    };
+    for (int32_t tile0 = P.key0; tile0 < P.key1; tile0 += 2 * W::KT) {
+        turn(tile0, buf0, buf1, flags, flags + W::NB);
+        if (tile0 + W::KT < P.key1) turn(tile0 + W::KT, buf1, buf0, flags + W::NB, flags);
+    }
+    if (__any(S.odd)) {
+#pragma unroll
+        for (int t = 0; t < W::RT; ++t)
+            add_not_finite<T, C, true>(A, P.lists, P.pg0, vhd, S.first_edge, S.most, S.limit[t], &S.R[t]);
     }
 #pragma unroll
-    for (int t = 0; t < W::RT; ++t)
-        store_rows<T, C>(A, to, R[t], (wave * W::RT + t) * 16 + a, token[t], head[t], live[t]);
+    for (int t = 0; t < W::RT; ++t) {
+        int32_t local, head;
+        const bool live = row_of(t, &local, &head);
+        store_rows<T, C, true>(A, to, S.R[t], (wave * W::RT + t) * 16 + a, P.seg.tok0 + local, head,
+                               live);
+    }
 }
 
 // -------------------------------------------------------------- kernel --
@@ -986,12 +1164,6 @@ struct Mine {
     int32_t seg;
     int64_t seg_start;
 };
-
-__device__ inline int64_t uniform(int64_t x) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
-    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
-    return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
-}
 
 __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_t grid) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -1027,6 +1199,8 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
         __syncthreads();
     }
 
+    total[0] = uniform(total[0]);
+    total[1] = uniform(total[1]);
     // workgroups per line: by the lines' times, in eights (one per XCD), and
     // no more than keep a piece at its least length
     Mine M;
@@ -1058,8 +1232,8 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     // consecutive pieces on one XCD (workgroups are dealt to the eight in turn)
     const int64_t xcd = block % 8, j = block / 8;
     M.line = j < wgs[1] / 8 ? 1 : 0;
-    M.wgs = wgs[M.line];
-    M.n = total[M.line];
+    M.wgs = uniform(wgs[M.line]);
+    M.n = uniform(total[M.line]);
     M.slot0 = M.line ? 0 : 2 * wgs[1];
     const int64_t jj = M.line ? j : j - wgs[1] / 8;
     M.w = xcd * (M.wgs / 8) + jj;
@@ -1111,23 +1285,27 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     return M;
 }
 
-// LINES: 1 thin only, 2 wide only, 3 both.
+// LINES: 1 thin only, 3 thin and wide.
 template <class T, bool FP8, int DP, int LINES>
-constexpr int lds_bytes() {
+struct Shared {
     using C = Cfg<T, FP8, DP>;
-    const int thin = (kWaves / 2) * 64 * (4 * C::NJ + 2) * 4;
-    const int wide = Wide<C>::LDS;
-    return LINES == 1 ? thin : (LINES == 2 ? wide : (thin > wide ? thin : wide));
-}
+    static constexpr int THIN = (kWaves / 2) * 64 * (4 * C::NJ + 2) * 4;
+    static constexpr int BUF = LINES == 1 ? 16 : Wide<C>::BUF;
+    static constexpr int BUF0 = BUF > THIN ? BUF : THIN;
+};
 
 template <class T, bool FP8, int DP, int LINES>
 __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
     using C = Cfg<T, FP8, DP>;
+    using S = Shared<T, FP8, DP, LINES>;
     __shared__ Plan plan;
-    __shared__ __attribute__((aligned(16))) char lds[lds_bytes<T, FP8, DP, LINES>()];
+    // separate arrays: reads of one need not wait for loads on their way to the other
+    __shared__ __attribute__((aligned(16))) char buf0[S::BUF0];
+    __shared__ __attribute__((aligned(16))) char buf1[S::BUF];
+    __shared__ uint32_t flags[2 * Wide<C>::NB];
     const Mine M = plan_work(A, &plan, blockIdx.x, gridDim.x);
     if (M.lo >= M.hi) return;
-    const bool wide_line = LINES == 2 || (LINES == 3 && M.line == 1);
+    const bool wide_line = LINES == 3 && M.line == 1;
     const int32_t nseg = A.num_groups + A.num_reqs;
     const int64_t round = wide_line ? Wide<C>::KT : kKeys;
 
@@ -1136,13 +1314,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
     int32_t s = M.seg;
     int64_t seg_start = M.seg_start;
     while (pos < M.hi && s < nseg) {
-        P.seg = segment(A, s);
+        P.seg = uniform(segment(A, s));
         const int64_t per_set = set_keys(P.seg);
         const int64_t cost = per_set * P.seg.sets;
         if (cost == 0 || P.seg.wide != (M.line == 1)) { ++s; continue; }
         const bool pre = s < A.num_groups;
         P.lists = pre ? A.pre : A.own;
-        P.pg0 = P.lists.pg_off[pre ? s : s - A.num_groups];
+        P.pg0 = uniform(P.lists.pg_off[pre ? s : s - A.num_groups]);
         while (pos < M.hi && pos < seg_start + cost) {
             const int64_t x = pos - seg_start;
             P.set = static_cast<int32_t>(x / per_set);
@@ -1175,10 +1353,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
             }
             to.part = pre ? 1 : 0;
             to.slot = static_cast<int32_t>(M.slot0 + 2 * M.w + (from_start ? 1 : 0));
-            if constexpr (LINES != 1)
-                if (wide_line) run_wide<T, C>(A, P, to, lds);
-            if constexpr (LINES != 2)
-                if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(lds));
+            if constexpr (LINES == 3) {
+                if (wide_line) run_wide<T, C>(A, P, to, buf0, buf1, flags);
+            }
+            if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(buf0));
             pos = end;
         }
         seg_start += cost;
