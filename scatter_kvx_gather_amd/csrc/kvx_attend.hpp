@@ -15,8 +15,9 @@
 //
 // Work.  A segment is a group's prefix or a request's own context; an item is
 // (segment, head set, tile of query rows), and its length is the number of
-// keys its last row sees.  All items laid end to end make one line of keys
-// that the workgroups cut into equal pieces, whatever the lengths are: they
+// keys its last row sees, and some units more that stand for its fixed time.
+// All items laid end to end make one line that the workgroups cut into equal
+// pieces, whatever the lengths are: they
 // stand in device memory, so each workgroup finds its piece itself from a
 // scan over the segments, and the host needs to know none of them.  A piece
 // that is not a whole item leaves (m, l, o) in the workgroup's two slots of
@@ -64,9 +65,12 @@ constexpr int kKeys = 32;               // keys of one step of a wave
 constexpr int kThinRows = 16;
 constexpr int kJoinWaves = 4;
 
-// A running maximum may lag the true one by this much (in log2) before the
-// accumulators are rescaled: weights stay below 2^8, exact in every type here.
-constexpr float kLag = 8.0f;
+// A row's reference maximum may lag the true one while a lane's weights of one
+// step sum to no more than this: they stay exact in every type here.
+constexpr float kMostWeight = 256.0f;
+// The reference of a row that has seen no key: any score's weight against it
+// is infinite, and -inf's is 0.
+constexpr float kNoKey = -3.0e38f;
 
 // The lane, as a value that the compiler does not carry around loops: what is
 // computed from it stays where it is used.  Held over the loops of a piece,
@@ -124,12 +128,14 @@ struct Args {
     int32_t wide_tokens;                // tokens per wide tile
     int32_t pre_wide;                   // prefixes run in wide tiles
     int32_t own_wide;                   // own contexts run in wide tiles
-    int32_t thin_min;                   // fewest keys of a piece
-    int32_t wide_min;
+    int32_t thin_min_log2;              // fewest units of a piece
+    int32_t wide_min_log2;
+    int32_t thin_item;                  // units that an item's fixed time counts for
+    int32_t wide_item;
     float wide_weight;                  // time of a wide key over a thin key's
     // workspace
     int64_t* starts;                    // [num_groups + num_reqs]: segment starts on its line
-    int64_t* plan;                      // [4]: keys and workgroups of the thin and the wide line
+    int64_t* plan;                      // [4]: units and workgroups of the thin and the wide line
     float* slot_o;                      // [2 * grid][slot rows][D]
     float* slot_ml;                     // [2 * grid][slot rows][2]
     float* row_o;                       // [2][T][Hq][D]: own, prefix (only with prefixes)
@@ -157,6 +163,7 @@ struct Seg {
     int32_t tiles;
     int32_t tp;                         // tokens per tile
     int32_t sets;                       // head sets
+    int32_t extra;                      // units of a tile's fixed time
     bool wide;
     bool causal;
 };
@@ -186,6 +193,7 @@ __device__ inline Seg segment(const Args& A, int32_t s) {
     g.wide = (pre ? A.pre_wide : A.own_wide) != 0;
     g.tp = g.wide ? A.wide_tokens : A.thin_tokens;
     g.sets = g.wide ? A.H : A.sets;
+    g.extra = g.wide ? A.wide_item : A.thin_item;
     g.tiles = g.keys > 0 ? (g.ntok + g.tp - 1) / g.tp : 0;
     return g;
 }
@@ -199,31 +207,44 @@ __device__ inline Seg uniform(const Seg& g) {
     u.tiles = uniform(g.tiles);
     u.tp = uniform(g.tp);
     u.sets = uniform(g.sets);
+    u.extra = uniform(g.extra);
     u.wide = uniform(static_cast<int32_t>(g.wide)) != 0;
     u.causal = uniform(static_cast<int32_t>(g.causal)) != 0;
     return u;
 }
 
-// Keys before tile i of a head set, and the keys of tile i (one more row tile
-// of a causal segment sees up to tp more keys).
+// Units before tile i of a head set, the keys of tile i (one more row tile of a
+// causal segment sees up to tp more keys), and the units of a head set.
 __device__ inline int64_t tile_start(const Seg& g, int32_t i) {
     const int64_t n = i;
-    return n * g.base + (g.causal ? g.tp * (n * (n + 1) / 2) : 0);
+    return n * (static_cast<int64_t>(g.base) + g.extra) + (g.causal ? g.tp * (n * (n + 1) / 2) : 0);
 }
 __device__ inline int64_t tile_keys(const Seg& g, int32_t i) {
     if (!g.causal) return g.base;
     const int64_t last = (static_cast<int64_t>(i) + 1) * g.tp;
     return g.base + (last < g.ntok ? last : g.ntok);
 }
-__device__ inline int64_t set_keys(const Seg& g) {
-    return g.tiles > 0 ? tile_start(g, g.tiles - 1) + tile_keys(g, g.tiles - 1) : 0;
+__device__ inline int64_t set_units(const Seg& g) {
+    return g.tiles > 0 ? tile_start(g, g.tiles - 1) + tile_keys(g, g.tiles - 1) + g.extra : 0;
+}
+// The key that a cut x units into an item falls on: a whole step of 2^log2 keys.
+__device__ inline int32_t cut_key(const Seg& g, int64_t x, int step_log2) {
+    return x <= g.extra ? 0 : static_cast<int32_t>((x - g.extra) >> step_log2 << step_log2);
 }
 
-// First key of workgroup w's piece of a line of n keys cut in `wgs` pieces, and the piece that key x is in.
-__device__ inline int64_t piece_start(int64_t n, int64_t wgs, int64_t w) { return n * w / wgs; }
-__device__ inline int64_t piece_of(int64_t n, int64_t wgs, int64_t x) {
-    return ((x + 1) * wgs - 1) / n;
-}
+// A line of n units cut into `wgs` pieces whose lengths differ by one at most.
+struct Cuts {
+    int64_t q, r;               // r pieces of q + 1 units, then pieces of q
+    __device__ inline Cuts(int64_t n, int64_t wgs) {
+        q = wgs > 0 ? n / wgs : 0;
+        r = n - q * wgs;
+    }
+    __device__ inline int64_t start(int64_t w) const { return q * w + (w < r ? w : r); }
+    __device__ inline int64_t piece_of(int64_t x) const {
+        const int64_t big = (q + 1) * r;
+        return x < big ? x / (q + 1) : r + (x - big) / q;
+    }
+};
 
 // Byte offset of key t's row (of head 0), or -1 when its page is out of range.
 __device__ inline int64_t key_offset(const Args& A, const Lists& L, int64_t pg0, int32_t t) {
@@ -390,6 +411,7 @@ __device__ inline void v_transpose(const uint32_t (&x)[8], u32x4* even, u32x4* o
 template <class C>
 struct Rows {
     float m;                    // reference maximum (log2), the same in a row's four lanes
+    float ref;                  // m, or kNoKey while it is -inf
     float l;                    // this lane's share of the sum
     f32x4 o[C::NJ];             // thin o[c * VE + j][r]: dim 16 VE c + (4 g + r) VE + j
                                 // wide o[j][r]: dim 16 j + 4 g + r
@@ -398,42 +420,52 @@ struct Rows {
 template <class C>
 __device__ inline void clear(Rows<C>* R) {
     R->m = -INFINITY;
+    R->ref = kNoKey;
     R->l = 0.0f;
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) R->o[j] = f32x4{0, 0, 0, 0};
 }
 
-// Scores s of 32 U keys to weights in the query's type, with the row's maximum
-// moved and the accumulators rescaled when a score passes it by more than kLag.
+// Scores s of 32 U keys to weights in the query's type.  The weights are taken
+// against the row's reference maximum as it stands, and only when a lane's sum
+// of them passes 2^kLag (or is a NaN) is the maximum looked for, the
+// accumulators rescaled and the weights taken anew: looking for it every time
+// cost as many instructions as the rest.
 template <class T, class C, int U>
 __device__ inline void weigh(Rows<C>* R, const f32x4 (&s)[2 * U], float scale, u32x4 (&pf)[U]) {
-    float top = -INFINITY;
+    float sum;
+    auto take = [&](float m) {
+        float part[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int x = 0; x < 2 * U; ++x)
-        top = fmaxf(fmaxf(fmaxf(top, s[x][0]), s[x][1]), fmaxf(s[x][2], s[x][3]));
-    top *= scale;
-    if (__any(top > R->m + kLag)) {
+        for (int u = 0; u < U; ++u) {
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * u + (i >> 2)][i & 3], scale, -m));
+                part[i & 1] += p[i];
+            }
+            pf[u] = u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]),
+                          Mma<T>::pack(p[4], p[5]), Mma<T>::pack(p[6], p[7])};
+        }
+        sum = part[0] + part[1];
+    };
+    take(R->ref);
+    if (__any(!(sum <= kMostWeight))) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 2 * U; ++x)
+            top = fmaxf(fmaxf(fmaxf(top, s[x][0]), s[x][1]), fmaxf(s[x][2], s[x][3]));
+        top *= scale;
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float m = fmaxf(R->m, top);
         const float a = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(R->m - m);
         R->m = m;
+        R->ref = m == -INFINITY ? kNoKey : m;
         R->l *= a;
 #pragma unroll
         for (int j = 0; j < C::NJ; ++j) R->o[j] *= a;
-    }
-    const float m = R->m == -INFINITY ? 0.0f : R->m;
-    float sum = 0.0f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float p[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * u + (i >> 2)][i & 3], scale, -m));
-            sum += p[i];
-        }
-        pf[u] = u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]), Mma<T>::pack(p[4], p[5]),
-                      Mma<T>::pack(p[6], p[7])};
+        take(R->ref);
     }
     R->l += sum;
 }
@@ -1147,24 +1179,29 @@ __device__ inline int64_t wave_scan(int64_t x) {
     return x;
 }
 
+constexpr int kWindow = 64;     // segments whose values are held in shared memory
+
 struct Plan {
     int64_t sums[kWaves][2];    // per-wave totals of a chunk
-    int64_t at[2];              // {segment, its start} of this workgroup's first key
+    int64_t at[2];              // {segment, its start} of this workgroup's first unit
+    Seg seg[kWindow];           // a window of segments
+    int64_t pg0[kWindow];
+    int64_t units[kWindow];     // of a head set
 };
 
-// The workgroup's line (0 thin, 1 wide), its piece of it and the segment the
-// piece begins in.  Every workgroup scans all segments (512 at a time); the
-// first one also leaves their starts and the cut for k_attend_join.
+// The workgroup's line (0 thin, 1 wide), its piece [lo, hi) of it and the
+// segment that the piece begins in.  Every workgroup scans all segments (512
+// at a time); the first one also leaves their starts and the lines' lengths
+// for k_attend_join.
 struct Mine {
     int line;
     int64_t w, lo, hi;
-    int64_t wgs;
-    int64_t n;
     int64_t slot0;              // the line's first slot
     int32_t seg;
     int64_t seg_start;
 };
 
+template <int LINES>
 __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_t grid) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int32_t nseg = A.num_groups + A.num_reqs;
@@ -1177,10 +1214,10 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
         wide = false;
         if (s < nseg) {
             const Seg g = segment(A, s);
-            cost = set_keys(g) * g.sets;
-            wide = g.wide;
+            cost = set_units(g) * g.sets;
+            wide = LINES == 3 && g.wide;
         }
-        const int64_t x = wave_scan(wide ? 0 : cost), y = wave_scan(wide ? cost : 0);
+        const int64_t x = wave_scan(wide ? 0 : cost), y = LINES == 3 ? wave_scan(wide ? cost : 0) : 0;
         if (lane == 63) {
             L->sums[wave][0] = x;
             L->sums[wave][1] = y;
@@ -1196,16 +1233,13 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
         }
         start = wide ? before[1] + y - cost : before[0] + x - cost;
         if (block == 0 && s < nseg) A.starts[s] = start;
-        __syncthreads();
+        if (c0 + kThreads < nseg) __syncthreads();
     }
-
     total[0] = uniform(total[0]);
     total[1] = uniform(total[1]);
+
     // workgroups per line: by the lines' times, in eights (one per XCD), and
     // no more than keep a piece at its least length
-    Mine M;
-    int64_t wgs[2];
-    const int64_t least[2] = {A.thin_min, A.wide_min};
     int64_t share = 0;                      // workgroups of the wide line
     if (total[1] > 0) {
         share = grid;
@@ -1216,12 +1250,12 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
             share = clamp_to(share, 8, static_cast<int64_t>(grid) - 8);
         }
     }
-    wgs[0] = grid - share;
-    wgs[1] = share;
+    int64_t wgs[2] = {static_cast<int64_t>(grid) - share, share};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int64_t want = ((total[i] + least[i] - 1) / least[i] + 7) / 8 * 8;
-        if (wgs[i] > want) wgs[i] = want;
+        const int log2 = i ? A.wide_min_log2 : A.thin_min_log2;
+        const int64_t want = (((total[i] + (int64_t(1) << log2) - 1) >> log2) + 7) / 8 * 8;
+        wgs[i] = uniform(wgs[i] > want ? want : wgs[i]);
     }
     if (block == 0 && threadIdx.x == 0) {
         A.plan[0] = total[0];
@@ -1230,29 +1264,29 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
         A.plan[3] = wgs[1];
     }
     // consecutive pieces on one XCD (workgroups are dealt to the eight in turn)
+    Mine M;
     const int64_t xcd = block % 8, j = block / 8;
     M.line = j < wgs[1] / 8 ? 1 : 0;
-    M.wgs = uniform(wgs[M.line]);
-    M.n = uniform(total[M.line]);
     M.slot0 = M.line ? 0 : 2 * wgs[1];
+    const int64_t mine = M.line ? wgs[1] : wgs[0];
     const int64_t jj = M.line ? j : j - wgs[1] / 8;
-    M.w = xcd * (M.wgs / 8) + jj;
-    if (jj >= M.wgs / 8) {
-        M.lo = M.hi = 0;
-        return M;
-    }
-    M.lo = piece_start(M.n, M.wgs, M.w);
-    M.hi = piece_start(M.n, M.wgs, M.w + 1);
+    M.w = xcd * (mine / 8) + jj;
+    M.lo = M.hi = 0;
+    if (jj >= mine / 8) return M;
+    const Cuts cuts(M.line ? total[1] : total[0], mine);
+    M.lo = uniform(cuts.start(M.w));
+    M.hi = uniform(cuts.start(M.w + 1));
     if (M.lo >= M.hi) return M;
-    // the segment that key lo lies in
+    // the segment that unit lo lies in
     if (nseg > kThreads) {
+        __syncthreads();
         int64_t run = 0;
         for (int32_t c0 = 0; c0 < nseg; c0 += kThreads) {
             const int32_t s = c0 + static_cast<int32_t>(threadIdx.x);
             int64_t cc = 0;
             if (s < nseg) {
                 const Seg g = segment(A, s);
-                if (g.wide == (M.line == 1)) cc = set_keys(g) * g.sets;
+                if (g.wide == (M.line == 1)) cc = set_units(g) * g.sets;
             }
             const int64_t x = wave_scan(cc);
             if (lane == 63) L->sums[wave][0] = x;
@@ -1269,7 +1303,7 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
                 L->at[1] = b;
             }
             __syncthreads();
-            if (run > M.lo) break;
+            if (uniform(run) > M.lo) break;
         }
     } else {
         if (cost > 0 && wide == (M.line == 1) && start <= M.lo && M.lo < start + cost) {
@@ -1278,10 +1312,8 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
         }
         __syncthreads();
     }
-    M.seg = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(L->at[0]));
+    M.seg = uniform(static_cast<int32_t>(L->at[0]));
     M.seg_start = uniform(L->at[1]);
-    M.lo = uniform(M.lo);
-    M.hi = uniform(M.hi);
     return M;
 }
 
@@ -1303,47 +1335,61 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
     __shared__ __attribute__((aligned(16))) char buf0[S::BUF0];
     __shared__ __attribute__((aligned(16))) char buf1[S::BUF];
     __shared__ uint32_t flags[2 * Wide<C>::NB];
-    const Mine M = plan_work(A, &plan, blockIdx.x, gridDim.x);
+    const Mine M = plan_work<LINES>(A, &plan, blockIdx.x, gridDim.x);
     if (M.lo >= M.hi) return;
     const bool wide_line = LINES == 3 && M.line == 1;
     const int32_t nseg = A.num_groups + A.num_reqs;
-    const int64_t round = wide_line ? Wide<C>::KT : kKeys;
+    const int step_log2 = wide_line ? (Wide<C>::KT == 128 ? 7 : 6) : 5;
 
     Piece P;
     int64_t pos = M.lo;                     // on the line
-    int32_t s = M.seg;
+    int32_t s = M.seg, first = M.seg - kWindow;
     int64_t seg_start = M.seg_start;
     while (pos < M.hi && s < nseg) {
-        P.seg = uniform(segment(A, s));
-        const int64_t per_set = set_keys(P.seg);
+        if (s >= first + kWindow) {
+            first = s;
+            __syncthreads();
+            const int32_t t = first + static_cast<int32_t>(threadIdx.x);
+            if (threadIdx.x < kWindow && t < nseg) {
+                const Seg g = segment(A, t);
+                plan.seg[threadIdx.x] = g;
+                plan.units[threadIdx.x] = set_units(g);
+                plan.pg0[threadIdx.x] = t < A.num_groups ? A.pre.pg_off[t] : A.own.pg_off[t - A.num_groups];
+            }
+            __syncthreads();
+        }
+        P.seg = uniform(plan.seg[s - first]);
+        const int64_t per_set = uniform(plan.units[s - first]);
         const int64_t cost = per_set * P.seg.sets;
         if (cost == 0 || P.seg.wide != (M.line == 1)) { ++s; continue; }
         const bool pre = s < A.num_groups;
         P.lists = pre ? A.pre : A.own;
-        P.pg0 = uniform(P.lists.pg_off[pre ? s : s - A.num_groups]);
+        P.pg0 = uniform(plan.pg0[s - first]);
         while (pos < M.hi && pos < seg_start + cost) {
             const int64_t x = pos - seg_start;
-            P.set = static_cast<int32_t>(x / per_set);
+            P.set = P.seg.sets == 1 ? 0 : static_cast<int32_t>(x / per_set);
             const int64_t y = x - P.set * per_set;
-            // the tile that key y of the head set lies in
+            // the tile that unit y of the head set lies in
             int32_t lo = 0, hi = P.seg.tiles - 1;
-            if (!P.seg.causal) {
-                lo = static_cast<int32_t>(y / P.seg.base);
-            } else {
-                while (lo < hi) {
-                    const int32_t mid = lo + (hi - lo + 1) / 2;
-                    if (tile_start(P.seg, mid) <= y) lo = mid; else hi = mid - 1;
+            if (hi > 0) {
+                if (!P.seg.causal) {
+                    lo = static_cast<int32_t>(y / (static_cast<int64_t>(P.seg.base) + P.seg.extra));
+                } else {
+                    while (lo < hi) {
+                        const int32_t mid = lo + (hi - lo + 1) / 2;
+                        if (tile_start(P.seg, mid) <= y) lo = mid; else hi = mid - 1;
+                    }
                 }
             }
             P.tile = lo;
-            const int64_t len = tile_keys(P.seg, lo);
+            const int64_t keys = tile_keys(P.seg, lo), len = keys + P.seg.extra;
             const int64_t item = seg_start + P.set * per_set + tile_start(P.seg, lo);
             const int64_t end = M.hi < item + len ? M.hi : item + len;
             const bool from_start = pos == item, to_end = end == item + len;
             // cuts inside an item fall on whole steps, both sides alike
-            const int64_t key1 = to_end ? len : (end - item) / round * round;
-            P.key0 = static_cast<int32_t>((pos - item) / round * round);
-            P.key1 = key1 < P.seg.keys ? static_cast<int32_t>(key1) : P.seg.keys;
+            P.key0 = cut_key(P.seg, pos - item, step_log2);
+            P.key1 = to_end ? static_cast<int32_t>(keys < P.seg.keys ? keys : P.seg.keys)
+                            : cut_key(P.seg, end - item, step_log2);
             P.counts = P.set == 0 && P.tile == P.seg.tiles - 1;
             Dest to;
             if (from_start && to_end) {
@@ -1353,11 +1399,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
             }
             to.part = pre ? 1 : 0;
             to.slot = static_cast<int32_t>(M.slot0 + 2 * M.w + (from_start ? 1 : 0));
+            pos = end;
+            // a piece without a step of its own leaves nothing (k_attend_join sees it the same way)
+            if (to.kind == kSlot && P.key0 >= P.key1) continue;
             if constexpr (LINES == 3) {
                 if (wide_line) run_wide<T, C>(A, P, to, buf0, buf1, flags);
             }
             if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(buf0));
-            pos = end;
         }
         seg_start += cost;
         ++s;
@@ -1385,25 +1433,23 @@ __device__ inline int32_t find_list(const int64_t* off, int32_t n, int64_t x) {
 
 // What one part (prefix or own) of a row left, and where.
 struct PartOf {
-    int64_t w0, w1;             // workgroups that have pieces of its item; w0 > w1: none
-    int64_t n, wgs;             // its line
-    int64_t slot0;
+    int32_t w0, w1;             // workgroups that have pieces of its item; w0 > w1: none
+    int32_t slot0;
     int32_t slot_row;
+    int64_t item;               // the item's first unit
 };
 
-__device__ inline PartOf part_of(const Args& A, int32_t s, int32_t token, int32_t head) {
+__device__ inline PartOf part_of(const Args& A, const Seg& g, const Cuts& cuts, int64_t start,
+                                 int32_t wide_wgs, int32_t token, int32_t head) {
     PartOf p;
     p.w0 = 0;
     p.w1 = -1;
-    const Seg g = segment(A, s);
-    const int line = g.wide ? 1 : 0;
-    p.n = A.plan[2 * line];
-    p.wgs = A.plan[2 * line + 1];
-    p.slot0 = line ? 0 : 2 * A.plan[3];
+    p.slot0 = g.wide ? 0 : 2 * wide_wgs;
     p.slot_row = 0;
+    p.item = 0;
     const int32_t local = token - g.tok0;
     if (g.tiles == 0 || local < 0 || local >= g.ntok) return p;
-    const int32_t kvh = head / A.G, hin = head % A.G;
+    const int32_t kvh = head / A.G, hin = head - kvh * A.G;
     const int32_t tile = local / g.tp;
     const int32_t in_tile = local - tile * g.tp;
     int32_t set;
@@ -1413,30 +1459,51 @@ __device__ inline PartOf part_of(const Args& A, int32_t s, int32_t token, int32_
     } else {
         const int32_t sub = hin / A.gv, vh = kvh * A.parts + sub;
         set = vh / A.hs;
-        p.slot_row = (vh % A.hs) * kThinRows + in_tile * A.gv + hin % A.gv;
+        p.slot_row = (vh - set * A.hs) * kThinRows + in_tile * A.gv + hin - sub * A.gv;
     }
-    const int64_t item = A.starts[s] + set * set_keys(g) + tile_start(g, tile);
-    p.w0 = piece_of(p.n, p.wgs, item);
-    p.w1 = piece_of(p.n, p.wgs, item + tile_keys(g, tile) - 1);
+    p.item = start + set * set_units(g) + tile_start(g, tile);
+    p.w0 = static_cast<int32_t>(cuts.piece_of(p.item));
+    p.w1 = static_cast<int32_t>(cuts.piece_of(p.item + tile_keys(g, tile) + g.extra - 1));
     return p;
 }
 
 // One wave joins the rows of 256 / DP neighbouring heads of one token: lane
-// holds 4 dims of one of them.  Bound by the partial sums' bytes, which are
-// few beside the keys'; what it costs is its launch and three dependent loads.
+// holds 4 dims of one of them.  Bound by its launch and its dependent loads:
+// the lists that the token is in (guessed for one token per request, and
+// searched for otherwise), the partial sums' maxima and sums, and their rows.
 template <class T, int DP>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
     constexpr int LPR = DP / 4, RPW = 64 / LPR;
     const int lane = threadIdx.x & 63;
     const int32_t hq = A.H * A.G;
-    const int32_t per_token = (hq + RPW - 1) / RPW;
+    const uint32_t per_token = (hq + RPW - 1) / RPW;
     const int64_t wave = static_cast<int64_t>(blockIdx.x) * kJoinWaves +
                          __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wave / per_token >= A.T) return;
-    const int32_t token = static_cast<int32_t>(wave / per_token);
-    const int32_t head = static_cast<int32_t>(wave % per_token) * RPW + lane / LPR;
-    const int32_t r = find_list(A.tok_off, A.num_reqs, token);
-    const int32_t gr = A.num_groups > 0 ? find_list(A.grp_off, A.num_groups, r) : 0;
+    const int64_t tok = (wave >> 32) == 0 ? static_cast<uint32_t>(wave) / per_token : wave / per_token;
+    if (tok >= A.T) return;
+    const int32_t token = static_cast<int32_t>(tok);
+    const int32_t head = static_cast<int32_t>(wave - tok * per_token) * RPW + lane / LPR;
+
+    int32_t r = token < A.num_reqs ? token : A.num_reqs - 1;
+    Seg own = uniform(segment(A, A.num_groups + r));
+    int64_t own_start = A.starts[A.num_groups + r];
+    const int64_t n0 = uniform(A.plan[0]), n1 = uniform(A.plan[2]);
+    const int32_t wgs0 = uniform(static_cast<int32_t>(A.plan[1]));
+    const int32_t wgs1 = uniform(static_cast<int32_t>(A.plan[3]));
+    if (token < own.tok0 || token >= own.tok0 + own.ntok) {
+        r = uniform(find_list(A.tok_off, A.num_reqs, token));
+        own = uniform(segment(A, A.num_groups + r));
+        own_start = A.starts[A.num_groups + r];
+    }
+    const int parts = A.num_groups > 0 ? 2 : 1;
+    Seg pre = own;
+    int64_t pre_start = 0;
+    if (parts == 2) {
+        const int32_t g = A.num_groups == 1 ? 0 : uniform(find_list(A.grp_off, A.num_groups, r));
+        pre = uniform(segment(A, g));
+        pre_start = A.starts[g];
+    }
+    const Cuts thin(n0, wgs0), wide(n1, wgs1);
     const int d = lane % LPR * 4;
     if (head >= hq) return;
     const bool has_dims = d < A.D;
@@ -1444,33 +1511,51 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
 
     float m = -INFINITY, l = 0.0f;
     f32x4 o = {0, 0, 0, 0};
-    auto add = [&](float m2, float l2, const float* src) {
-        if (l2 == 0.0f) return;
-        const f32x4 x = has_dims ? *reinterpret_cast<const f32x4*>(src + d) : f32x4{0, 0, 0, 0};
-        const float top = fmaxf(m, m2);
+    auto add = [&](float2 ml, f32x4 x) {
+        if (ml.y == 0.0f) return;
+        const float top = fmaxf(m, ml.x);
         const float ref = top == -INFINITY ? 0.0f : top;
-        const float w1 = __builtin_amdgcn_exp2f(m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
+        const float w1 = __builtin_amdgcn_exp2f(m - ref), w2 = __builtin_amdgcn_exp2f(ml.x - ref);
         m = top;
-        l = l * w1 + l2 * w2;
+        l = l * w1 + ml.y * w2;
         o = o * w1 + x * w2;
     };
-    const int parts = A.num_groups > 0 ? 2 : 1;
     for (int k = 0; k < parts; ++k) {
-        const PartOf p = part_of(A, k ? gr : A.num_groups + r, token, head);
+        const Seg& g = k ? pre : own;
+        const Cuts& cuts = g.wide ? wide : thin;
+        const PartOf p = part_of(A, g, cuts, k ? pre_start : own_start, wgs1, token, head);
         if (p.w0 > p.w1) continue;
         if (p.w0 == p.w1) {
             if (parts == 1) return;             // written by the workgroup that had it all
             const int64_t at = static_cast<int64_t>(k) * A.T * hq + row;
             const float2 ml = *reinterpret_cast<const float2*>(A.row_ml + at * 2);
-            add(ml.x, ml.y, A.row_o + at * A.D);
+            add(ml, has_dims ? *reinterpret_cast<const f32x4*>(A.row_o + at * A.D + d) : f32x4{0, 0, 0, 0});
             continue;
         }
-#pragma unroll 4
-        for (int64_t w = p.w0; w <= p.w1; ++w) {
-            if (piece_start(p.n, p.wgs, w) >= piece_start(p.n, p.wgs, w + 1)) continue;
-            const int64_t at = (p.slot0 + 2 * w + (w == p.w0 ? 1 : 0)) * A.slot_rows + p.slot_row;
-            const float2 ml = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);
-            add(ml.x, ml.y, A.slot_o + at * A.D);
+        const int step_log2 = !g.wide ? 5 : (DP <= 128 ? 7 : 6);
+        // a workgroup has left its slot if its piece has a step of keys
+        const int32_t local = token - g.tok0;
+        const int64_t keys64 = tile_keys(g, local / g.tp);
+        const int32_t keys = static_cast<int32_t>(keys64 < g.keys ? keys64 : g.keys);
+        constexpr int B = 4;                    // slots under way at once
+        for (int32_t w0 = p.w0; w0 <= p.w1; w0 += B) {
+            float2 ml[B];
+            f32x4 x[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const int32_t w = w0 + i;
+                ml[i] = make_float2(0.0f, 0.0f);
+                x[i] = f32x4{0, 0, 0, 0};
+                if (w > p.w1) continue;
+                const int32_t k0 = w == p.w0 ? 0 : cut_key(g, cuts.start(w) - p.item, step_log2);
+                const int32_t k1 = w == p.w1 ? keys : cut_key(g, cuts.start(w + 1) - p.item, step_log2);
+                if (k0 >= k1) continue;
+                const int64_t at = static_cast<int64_t>(p.slot0 + 2 * w + (w == p.w0 ? 1 : 0)) * A.slot_rows + p.slot_row;
+                ml[i] = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);
+                if (has_dims) x[i] = *reinterpret_cast<const f32x4*>(A.slot_o + at * A.D + d);
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i) add(ml[i], x[i]);
         }
     }
     const float inv = l == 0.0f ? 0.0f : A.v_scale / l;

@@ -440,12 +440,14 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.wide_tokens = s.wide_rows / s.G;
     a.pre_wide = s.pre_wide;
     a.own_wide = s.own_wide;
-    a.thin_min = 64 * a.kp;
-    a.wide_min = 256;
-    // a compute unit's time for a wide key (its products at half the matrix
-    // peak) over that for a thin key (its bytes at the memory's rate)
-    const double wide_ns = 4.0 * s.wide_rows * s.DP / 4000.0;
-    const double thin_ns = 2.0 * a.hs * g.Db / a.parts / 19.5;
+    a.thin_min_log2 = 6;
+    a.wide_min_log2 = 8;
+    a.thin_item = 64;
+    a.wide_item = 320;
+    // a compute unit's time for a wide key (its products) over that for a thin
+    // key (its bytes)
+    const double wide_ns = 4.0 * s.wide_rows * s.DP / 2000.0;
+    const double thin_ns = 2.0 * a.hs * g.Db / a.parts / 26.0;
     a.wide_weight = static_cast<float>(wide_ns / thin_ns);
     char* ws = static_cast<char*>(x.workspace);
     a.starts = reinterpret_cast<int64_t*>(ws + s.starts);
