@@ -246,16 +246,35 @@ struct Cuts {
     }
 };
 
-// Byte offset of key t's row (of head 0), or -1 when its page is out of range.
-__device__ inline int64_t key_offset(const Args& A, const Lists& L, int64_t pg0, int32_t t) {
+// Page id of key t (any id when the list has no such entry), and the byte
+// offset of the key's row (of head 0) from it, or -1 when entry or page are out
+// of range.  Two steps, because loops load the ids of a later step first and
+// ask for the offsets a step later: loads return in order, so an id asked for
+// at once would wait for the rows under way before it.  The load has no
+// condition, which would do the same.
+__device__ inline int32_t key_page(const Args& A, const Lists& L, int64_t pg0, int32_t t) {
     const uint32_t tu = static_cast<uint32_t>(t);
-    const uint32_t kp = A.page_shift >= 0 ? tu >> A.page_shift : tu / static_cast<uint32_t>(A.page_size);
-    const uint32_t row = tu - kp * static_cast<uint32_t>(A.page_size);
+    const int64_t kp = A.page_shift >= 0 ? tu >> A.page_shift : tu / static_cast<uint32_t>(A.page_size);
+    int64_t i = 0;
+    if (pg0 >= -kp && pg0 < L.num_ids - kp) i = pg0 + kp;
+    // an empty list's entry is read from an array that is never empty
+    const int32_t* ids = L.num_ids > 0 ? L.ids : reinterpret_cast<const int32_t*>(A.tok_off);
+    return ids[i];
+}
+__device__ inline int64_t page_offset(const Args& A, const Lists& L, int64_t pg0, int32_t page,
+                                      int32_t t, int32_t end) {
+    const uint32_t tu = static_cast<uint32_t>(t), b = static_cast<uint32_t>(A.page_size);
+    const int64_t kp = A.page_shift >= 0 ? tu >> A.page_shift : tu / b;
+    const uint32_t row = A.page_shift >= 0 ? tu & (b - 1) : tu - static_cast<uint32_t>(kp) * b;
     // the index is range-checked before the sum is formed: no pg_off value makes it wrap
-    if (pg0 < -static_cast<int64_t>(kp) || pg0 >= L.num_ids - static_cast<int64_t>(kp)) return -1;
-    const int64_t page = L.ids[pg0 + kp];
-    if (page < 0 || page >= A.num_pages) return -1;
-    return page * A.page_stride + row * A.row_stride;
+    const bool ok = (t < end) & (pg0 >= -kp) & (pg0 < L.num_ids - kp) & (page >= 0) &
+                    (page < A.num_pages);
+    const int64_t off = static_cast<uint32_t>(page) * A.page_stride + row * A.row_stride;
+    return ok ? off : -1;
+}
+__device__ inline int64_t key_offset(const Args& A, const Lists& L, int64_t pg0, int32_t t,
+                                     int32_t end) {
+    return page_offset(A, L, pg0, key_page(A, L, pg0, t), t, end);
 }
 
 // ------------------------------------------------------------ elements --
@@ -481,7 +500,7 @@ __device__ inline void add_not_finite(const Args& A, const Lists& L, int64_t pg0
     const int g = here_lane() >> 4;
 #pragma unroll 1
     for (int32_t t = from; t < to; ++t) {
-        const int64_t off = key_offset(A, L, pg0, t);
+        const int64_t off = key_offset(A, L, pg0, t, to);
         if (off < 0) continue;
 #pragma unroll
         for (int x = 0; x < C::NJ; ++x) {
@@ -595,7 +614,8 @@ __device__ inline void count_skipped(const Args& A, const Piece& P, int wave) {
     const int lane = threadIdx.x & 63;
     unsigned long long n = 0;
     for (int64_t t = static_cast<int64_t>(P.key0) + wave * 64; t < P.key1; t += kThreads) {
-        const bool bad = t + lane < P.key1 && key_offset(A, P.lists, P.pg0, static_cast<int32_t>(t) + lane) < 0;
+        const int32_t k = static_cast<int32_t>(t) + lane;
+        const bool bad = k < P.key1 && key_offset(A, P.lists, P.pg0, k, P.key1) < 0;
         n += __popcll(__ballot(bad));
     }
     if (lane == 0 && n != 0) atomicAdd(A.skipped, n);
@@ -676,9 +696,12 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
         constexpr bool AHEAD = C::NC == 1;
         KTile<C> kt[2];
         Words<C::VW> vr[8][C::NC];
-        auto offset_of = [&](int32_t key0) -> int64_t {
-            const int32_t t = key0 + (lane & 31);
-            return t < P.key1 ? key_offset(A, P.lists, P.pg0, t) : -1;
+        // page ids of a step's keys, one per lane, and their offsets
+        auto page_of = [&](int32_t key0) -> int32_t {
+            return key_page(A, P.lists, P.pg0, key0 + (lane & 31));
+        };
+        auto offset_of = [&](int32_t key0, int32_t page) -> int64_t {
+            return page_offset(A, P.lists, P.pg0, page, key0 + (lane & 31), P.key1);
         };
         auto load_keys = [&](int64_t off) {
             const int64_t safe = off < 0 ? 0 : off;
@@ -712,12 +735,16 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
         bool odd = false;               // a value left out of a product
         int32_t first_edge = -1;        // this wave's first step that not all rows see whole
         int32_t key0 = P.key0 + part * kKeys;
-        int64_t off = key0 < P.key1 ? offset_of(key0) : -1;
-        if (AHEAD && key0 < P.key1) {
-            load_keys(off);
-            load_values(off);
+        int32_t page = -1;
+        int64_t off = -1;
+        if (key0 < P.key1) {
+            off = offset_of(key0, page_of(key0));
+            page = page_of(key0 + step);
+            if (AHEAD) {
+                load_keys(off);
+                load_values(off);
+            }
         }
-        int64_t off_next = key0 + step < P.key1 ? offset_of(key0 + step) : -1;
         for (; key0 < P.key1; key0 += step) {
             const uint32_t valid = static_cast<uint32_t>(__ballot(off >= 0));
             const bool more = key0 + step < P.key1;
@@ -725,8 +752,9 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             f32x4 s[2];
             scores<T, C>(q, s, [&](int x, int ks) { return k_frag<T, C>(kt[x], ks, g, A.D); });
             if (!AHEAD) load_values(off);
+            const int64_t off_next = offset_of(key0 + step, page);
+            page = page_of(key0 + 2 * step);
             if (AHEAD && more) load_keys(off_next);
-            const int64_t off_after = key0 + 2 * step < P.key1 ? offset_of(key0 + 2 * step) : -1;
             const bool partial = all_see < key0 + kKeys;
             if (valid != 0xffffffffu || partial) mask_scores(s, key0, limit, valid);
             u32x4 pf[1];
@@ -768,7 +796,6 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             }
             if (AHEAD && more) load_values(off_next);
             off = off_next;
-            off_next = off_after;
         }
         if (__any(odd)) {
             // the wave's own steps only: `step` apart
@@ -880,12 +907,15 @@ struct Stage {
     u32x4 raw[N];
 };
 
-template <class T, class C>
-__device__ inline int64_t stage_offset(const Args& A, const Piece& P, int32_t tile0, int wave) {
-    using W = Wide<C>;
-    const int lane = threadIdx.x & 63;
-    const int32_t t = tile0 + (wave & 3) * W::KW + (lane & (W::KW - 1));
-    return t < P.key1 ? key_offset(A, P.lists, P.pg0, t) : -1;
+// The key whose offset this lane holds, and its page id.
+template <class C>
+__device__ inline int32_t stage_key(int32_t tile0, int wave) {
+    constexpr int KW = Wide<C>::KW;
+    return tile0 + (wave & 3) * KW + (here_lane() & (KW - 1));
+}
+template <class C>
+__device__ inline int32_t stage_page(const Args& A, const Piece& P, int32_t tile0, int wave) {
+    return key_page(A, P.lists, P.pg0, stage_key<C>(tile0, wave));
 }
 
 template <class T, class C>
@@ -903,23 +933,28 @@ __device__ inline void stage_load(const Args& A, Stage<T, C>* S, const char* kh,
             else reinterpret_cast<uint16_t*>(flags)[kw] = static_cast<uint16_t>(seen);
         }
         if constexpr (C::EB == 2) {
+            constexpr int N = W::KW / 16;
+            int64_t off[N];
 #pragma unroll
-            for (int x = 0; x < W::KW / 16; ++x) {
-                const int64_t off = __shfl(S->off, x * 16 + a);
-                const char* src = kh + off + g * 16;
-                char* to = buf + (kw * (W::KW / 16) + x) * C::KS * 1024;
-                if (whole) {
+            for (int x = 0; x < N; ++x) off[x] = __shfl(S->off, x * 16 + a);
+            char* to = buf + kw * N * C::KS * 1024;
+            if (whole) {
 #pragma unroll
-                    for (int ks = 0; ks < C::KS; ++ks) load_to_lds(src + ks * 64, to + ks * 1024);
-                } else {
+                for (int x = 0; x < N; ++x)
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks)
+                        load_to_lds(kh + off[x] + g * 16 + ks * 64, to + (x * C::KS + ks) * 1024);
+            } else {
+#pragma unroll
+                for (int x = 0; x < N; ++x)
 #pragma unroll
                     for (int ks = 0; ks < C::KS; ++ks) {
-                        if (off >= 0 && ks * 32 + g * 8 < A.D)
-                            load_to_lds(src + ks * 64, to + ks * 1024);
+                        char* t = to + (x * C::KS + ks) * 1024;
+                        if (off[x] >= 0 && ks * 32 + g * 8 < A.D)
+                            load_to_lds(kh + off[x] + g * 16 + ks * 64, t);
                         else
-                            *reinterpret_cast<u32x4*>(to + ks * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+                            *reinterpret_cast<u32x4*>(t + lane * 16) = u32x4{0, 0, 0, 0};
                     }
-                }
             }
         } else {
 #pragma unroll
@@ -938,20 +973,23 @@ __device__ inline void stage_load(const Args& A, Stage<T, C>* S, const char* kh,
         char* v = buf + W::KF * 1024 + kw * W::KW * W::RB;
         if constexpr (C::EB == 2) {
             constexpr int LPR = W::RB / 16, RPP = 64 / LPR;  // lanes per row, rows per load
+            constexpr int N = W::KW / RPP;
+            int64_t off[N];
 #pragma unroll
-            for (int i = 0; i < W::KW / RPP; ++i) {
-                const int row = i * RPP + lane / LPR;
-                const int64_t off = __shfl(S->off, row);
-                const int chunk = (lane % LPR) ^ v_swizzle<C>(row);
-                const char* src = vhd + off + chunk * 16;
-                char* to = v + i * 1024;
-                if (whole) {
-                    load_to_lds(src, to);
-                } else {
-                    if (off >= 0 && chunk * 8 < A.D)
-                        load_to_lds(src, to);
+            for (int i = 0; i < N; ++i) off[i] = __shfl(S->off, i * RPP + lane / LPR);
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    load_to_lds(vhd + off[i] + ((lane % LPR) ^ v_swizzle<C>(i * RPP + lane / LPR)) * 16,
+                                v + i * 1024);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int chunk = (lane % LPR) ^ v_swizzle<C>(i * RPP + lane / LPR);
+                    if (off[i] >= 0 && chunk * 8 < A.D)
+                        load_to_lds(vhd + off[i] + chunk * 16, v + i * 1024);
                     else
-                        *reinterpret_cast<u32x4*>(to + lane * 16) = u32x4{0, 0, 0, 0};
+                        *reinterpret_cast<u32x4*>(v + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
                 }
             }
         } else {
@@ -1100,7 +1138,9 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
     const char* kh = A.k + kvh * A.head_stride;
     const char* vhd = A.v + kvh * A.head_stride;
     Stage<T, C> next;
-    next.off = stage_offset<T, C>(A, P, P.key0, wave);
+    int32_t page = stage_page<C>(A, P, P.key0, wave);
+    next.off = page_offset(A, P.lists, P.pg0, page, stage_key<C>(P.key0, wave), P.key1);
+    page = stage_page<C>(A, P, P.key0 + W::KT, wave);
     stage_load<T, C>(A, &next, kh, vhd, wave, buf0, flags);
 
     WideState<T, C> S;
@@ -1134,19 +1174,17 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
     }
 
     stage_store<T, C>(next, wave, buf0);
-    next.off = stage_offset<T, C>(A, P, P.key0 + W::KT, wave);
     __syncthreads();
     // one tile: the next one is on its way to the other buffer meanwhile
     auto turn = [&](int32_t tile0, char* here, char* there, uint32_t* fh, uint32_t* ft) {
         const bool more = tile0 + W::KT < P.key1;
-        int64_t after = -1;
         if (more) {
+            next.off = page_offset(A, P.lists, P.pg0, page, stage_key<C>(tile0 + W::KT, wave), P.key1);
+            page = stage_page<C>(A, P, tile0 + 2 * W::KT, wave);
             stage_load<T, C>(A, &next, kh, vhd, wave, there, ft);
-            after = stage_offset<T, C>(A, P, tile0 + 2 * W::KT, wave);
         }
         wide_tile<T, C>(A, P, &S, tile0, here, fh);
         if (more) stage_store<T, C>(next, wave, there);
-        next.off = after;
         __syncthreads();
     };
     for (int32_t tile0 = P.key0; tile0 < P.key1; tile0 += 2 * W::KT) {
