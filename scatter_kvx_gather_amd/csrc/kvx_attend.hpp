@@ -849,7 +849,9 @@ struct Wide {
     static constexpr int KT = DP <= 128 ? 128 : 64;
     static constexpr int U = DP <= 128 ? 2 : 1;
     static constexpr int NB = KT / kKeys;               // steps of 32 keys
-    static constexpr int KW = KT / 4;                   // keys that a wave stages
+    static constexpr int WPG = 128 / KT;                // waves that stage one group of 16 keys
+    static constexpr int VR = 16 / WPG;                 // V rows that a wave stages
+    static constexpr int KSW = C::KS / WPG;             // k-steps of a K tile that a wave stages
     static constexpr int KF = (KT / 16) * C::KS;        // K fragments of 1 KiB
     static constexpr int RB = DP * 2;                   // bytes of a V row
     static constexpr int BUF = KF * 1024 + KT * RB;
@@ -896,22 +898,24 @@ __device__ inline u32x4 v_frag(const char* v, int at, int step, int j) {
     return u32x4{lo.x, lo.y, hi.x, hi.y};
 }
 
-// Keys [tile0, tile0 + KT) of a piece on their way to a buffer: waves 0-3
-// stage K, 4-7 V, KT / 4 keys each.  16-bit values go from memory to shared
-// memory directly; fp8 ones through registers, where they are converted.
+// Keys [tile0, tile0 + KT) of a piece on their way to a buffer: each wave
+// stages K and V of a group of 16 keys, or half of each.  16-bit values go
+// from memory to shared memory directly; fp8 ones through registers, where
+// they are converted.
 template <class T, class C>
 struct Stage {
     using W = Wide<C>;
-    static constexpr int N = C::EB == 2 ? 1 : W::KW * W::DP / 1024;   // 16-byte loads per lane
-    int64_t off;                        // the row offset of key kw * KW + lane % KW, or -1
-    u32x4 raw[N];
+    static constexpr int NK = C::EB == 2 ? 1 : C::NK / W::WPG;            // 16-byte loads per lane
+    static constexpr int NV = C::EB == 2 ? 1 : W::VR * W::DP / 1024;
+    int64_t off;                        // the row offset of key lane % 16 of the group, or -1
+    u32x4 k[NK];
+    u32x4 v[NV];
 };
 
 // The key whose offset this lane holds, and its page id.
 template <class C>
 __device__ inline int32_t stage_key(int32_t tile0, int wave) {
-    constexpr int KW = Wide<C>::KW;
-    return tile0 + (wave & 3) * KW + (here_lane() & (KW - 1));
+    return tile0 + wave / Wide<C>::WPG * 16 + (here_lane() & 15);
 }
 template <class C>
 __device__ inline int32_t stage_page(const Args& A, const Piece& P, int32_t tile0, int wave) {
@@ -923,84 +927,60 @@ __device__ inline void stage_load(const Args& A, Stage<T, C>* S, const char* kh,
                                   int wave, char* buf, uint32_t* flags) {
     using W = Wide<C>;
     const int lane = here_lane(), a = lane & 15, g = lane >> 4;
-    const int kw = wave & 3;
+    const int grp = wave / W::WPG, sub = wave % W::WPG;
     const uint64_t seen = __ballot(S->off >= 0);
     const bool whole = seen == ~0ull && A.D == W::DP;       // every lane loads
-    if (wave < 4) {
-        // flag kw * KW / 32: which of a step's keys are there (half a word each for KW = 16)
-        if (lane == 0) {
-            if constexpr (W::KW == 32) flags[kw] = static_cast<uint32_t>(seen);
-            else reinterpret_cast<uint16_t*>(flags)[kw] = static_cast<uint16_t>(seen);
-        }
-        if constexpr (C::EB == 2) {
-            constexpr int N = W::KW / 16;
-            int64_t off[N];
+    if (lane == 0 && sub == 0) reinterpret_cast<uint16_t*>(flags)[grp] = static_cast<uint16_t>(seen);
+    const int64_t koff = S->off;                            // of key a, in every lane group
+    if constexpr (C::EB == 2) {
+        constexpr int LPR = W::RB / 16, RPP = 64 / LPR;     // lanes per V row, rows per load
+        constexpr int N = W::VR / RPP;
+        int64_t off[N];
 #pragma unroll
-            for (int x = 0; x < N; ++x) off[x] = __shfl(S->off, x * 16 + a);
-            char* to = buf + kw * N * C::KS * 1024;
-            if (whole) {
+        for (int i = 0; i < N; ++i) off[i] = __shfl(S->off, sub * W::VR + i * RPP + lane / LPR);
+        char* kb = buf + (grp * C::KS + sub * W::KSW) * 1024;
+        char* vb = buf + W::KF * 1024 + (grp * 16 + sub * W::VR) * W::RB;
+        const char* ksrc = kh + koff + g * 16 + sub * W::KSW * 64;
+        if (whole) {
 #pragma unroll
-                for (int x = 0; x < N; ++x)
+            for (int ks = 0; ks < W::KSW; ++ks) load_to_lds(ksrc + ks * 64, kb + ks * 1024);
 #pragma unroll
-                    for (int ks = 0; ks < C::KS; ++ks)
-                        load_to_lds(kh + off[x] + g * 16 + ks * 64, to + (x * C::KS + ks) * 1024);
-            } else {
-#pragma unroll
-                for (int x = 0; x < N; ++x)
-#pragma unroll
-                    for (int ks = 0; ks < C::KS; ++ks) {
-                        char* t = to + (x * C::KS + ks) * 1024;
-                        if (off[x] >= 0 && ks * 32 + g * 8 < A.D)
-                            load_to_lds(kh + off[x] + g * 16 + ks * 64, t);
-                        else
-                            *reinterpret_cast<u32x4*>(t + lane * 16) = u32x4{0, 0, 0, 0};
-                    }
+            for (int i = 0; i < N; ++i) {
+                const int row = sub * W::VR + i * RPP + lane / LPR;
+                load_to_lds(vhd + off[i] + ((lane % LPR) ^ v_swizzle<C>(row)) * 16, vb + i * 1024);
             }
         } else {
 #pragma unroll
-            for (int x = 0; x < W::KW / 16; ++x) {
-                const int64_t off = __shfl(S->off, x * 16 + a);
+            for (int ks = 0; ks < W::KSW; ++ks) {
+                if (koff >= 0 && (sub * W::KSW + ks) * 32 + g * 8 < A.D)
+                    load_to_lds(ksrc + ks * 64, kb + ks * 1024);
+                else
+                    *reinterpret_cast<u32x4*>(kb + ks * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+            }
 #pragma unroll
-                for (int y = 0; y < C::NK; ++y) {
-                    const int b = y * 64 + g * 16;
-                    S->raw[x * C::NK + y] = u32x4{0, 0, 0, 0};
-                    if (off >= 0 && b < A.D)
-                        S->raw[x * C::NK + y] = *reinterpret_cast<const u32x4*>(kh + off + b);
-                }
+            for (int i = 0; i < N; ++i) {
+                const int chunk = (lane % LPR) ^ v_swizzle<C>(sub * W::VR + i * RPP + lane / LPR);
+                if (off[i] >= 0 && chunk * 8 < A.D)
+                    load_to_lds(vhd + off[i] + chunk * 16, vb + i * 1024);
+                else
+                    *reinterpret_cast<u32x4*>(vb + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
             }
         }
     } else {
-        char* v = buf + W::KF * 1024 + kw * W::KW * W::RB;
-        if constexpr (C::EB == 2) {
-            constexpr int LPR = W::RB / 16, RPP = 64 / LPR;  // lanes per row, rows per load
-            constexpr int N = W::KW / RPP;
-            int64_t off[N];
+        using St = Stage<T, C>;
+        constexpr int LPR = W::DP / 16, RPP = 64 / LPR;
 #pragma unroll
-            for (int i = 0; i < N; ++i) off[i] = __shfl(S->off, i * RPP + lane / LPR);
-            if (whole) {
+        for (int y = 0; y < St::NK; ++y) {
+            const int b = (sub * St::NK + y) * 64 + g * 16;
+            S->k[y] = u32x4{0, 0, 0, 0};
+            if (koff >= 0 && b < A.D) S->k[y] = *reinterpret_cast<const u32x4*>(kh + koff + b);
+        }
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    load_to_lds(vhd + off[i] + ((lane % LPR) ^ v_swizzle<C>(i * RPP + lane / LPR)) * 16,
-                                v + i * 1024);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int chunk = (lane % LPR) ^ v_swizzle<C>(i * RPP + lane / LPR);
-                    if (off[i] >= 0 && chunk * 8 < A.D)
-                        load_to_lds(vhd + off[i] + chunk * 16, v + i * 1024);
-                    else
-                        *reinterpret_cast<u32x4*>(v + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
-                }
-            }
-        } else {
-            constexpr int LPR = W::DP / 16, RPP = 64 / LPR;
-#pragma unroll
-            for (int i = 0; i < W::KW / RPP; ++i) {
-                const int64_t off = __shfl(S->off, i * RPP + lane / LPR);
-                const int b = lane % LPR * 16;
-                S->raw[i] = u32x4{0, 0, 0, 0};
-                if (off >= 0 && b < A.D) S->raw[i] = *reinterpret_cast<const u32x4*>(vhd + off + b);
-            }
+        for (int i = 0; i < St::NV; ++i) {
+            const int64_t off = __shfl(S->off, sub * W::VR + i * RPP + lane / LPR);
+            const int b = lane % LPR * 16;
+            S->v[i] = u32x4{0, 0, 0, 0};
+            if (off >= 0 && b < A.D) S->v[i] = *reinterpret_cast<const u32x4*>(vhd + off + b);
         }
     }
 }
@@ -1016,26 +996,24 @@ template <class T, class C>
 __device__ inline void stage_store(const Stage<T, C>& S, int wave, char* buf) {
     if constexpr (C::EB == 1) {
         using W = Wide<C>;
+        using St = Stage<T, C>;
         const int lane = here_lane();
-        const int kw = wave & 3;
-        if (wave < 4) {
-            char* to = buf + kw * (W::KW / 16) * C::KS * 1024 + lane * 16;
+        const int grp = wave / W::WPG, sub = wave % W::WPG;
+        char* to = buf + (grp * C::KS + sub * W::KSW) * 1024 + lane * 16;
 #pragma unroll
-            for (int x = 0; x < W::KW / 16 * C::NK; ++x) {
-                *reinterpret_cast<u32x4*>(to + 2 * x * 1024) = widen<T>(S.raw[x].x, S.raw[x].y);
-                *reinterpret_cast<u32x4*>(to + (2 * x + 1) * 1024) = widen<T>(S.raw[x].z, S.raw[x].w);
-            }
-        } else {
-            constexpr int LPR = W::DP / 16, RPP = 64 / LPR;
-            char* v = buf + W::KF * 1024 + kw * W::KW * W::RB;
+        for (int x = 0; x < St::NK; ++x) {
+            *reinterpret_cast<u32x4*>(to + 2 * x * 1024) = widen<T>(S.k[x].x, S.k[x].y);
+            *reinterpret_cast<u32x4*>(to + (2 * x + 1) * 1024) = widen<T>(S.k[x].z, S.k[x].w);
+        }
+        constexpr int LPR = W::DP / 16, RPP = 64 / LPR;
+        char* v = buf + W::KF * 1024 + grp * 16 * W::RB;
 #pragma unroll
-            for (int i = 0; i < W::KW / RPP; ++i) {
-                const int row = i * RPP + lane / LPR;
-                char* to = v + row * W::RB;
-                const int c = 2 * (lane % LPR), sw = v_swizzle<C>(row);
-                *reinterpret_cast<u32x4*>(to + ((c ^ sw) * 16)) = widen<T>(S.raw[i].x, S.raw[i].y);
-                *reinterpret_cast<u32x4*>(to + (((c + 1) ^ sw) * 16)) = widen<T>(S.raw[i].z, S.raw[i].w);
-            }
+        for (int i = 0; i < St::NV; ++i) {
+            const int row = sub * W::VR + i * RPP + lane / LPR;
+            char* at = v + row * W::RB;
+            const int c = 2 * (lane % LPR), sw = v_swizzle<C>(row);
+            *reinterpret_cast<u32x4*>(at + ((c ^ sw) * 16)) = widen<T>(S.v[i].x, S.v[i].y);
+            *reinterpret_cast<u32x4*>(at + (((c + 1) ^ sw) * 16)) = widen<T>(S.v[i].z, S.v[i].w);
         }
     }
 }
