@@ -322,11 +322,16 @@ struct Mma<_Float16> {
     static constexpr uint32_t kExp = 0x7c007c00u;
 };
 
-// w with halves that are an infinity or a NaN cleared.
+// w with 16-bit halves that are an infinity or a NaN cleared; of a word of four
+// fp8 values, with NaN cleared.
 template <class T>
 __device__ inline uint32_t finite_pair(uint32_t w) {
     constexpr uint32_t lo = Mma<T>::kExp & 0xffffu, hi = Mma<T>::kExp & 0xffff0000u;
     return ((w & lo) == lo ? 0u : w & 0xffffu) | ((w & hi) == hi ? 0u : w & 0xffff0000u);
+}
+__device__ inline uint32_t finite_quad(uint32_t w) {
+    const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    return w & ~((nan >> 7) * 0xffu);
 }
 
 // Shapes of one (query type, pool element, padded head dim) combination.
@@ -445,48 +450,40 @@ __device__ inline void clear(Rows<C>* R) {
     for (int j = 0; j < C::NJ; ++j) R->o[j] = f32x4{0, 0, 0, 0};
 }
 
-// Scores s of 32 U keys to weights in the query's type.  The weights are taken
+// Scores s of 32 keys to weights in the query's type.  The weights are taken
 // against the row's reference maximum as it stands, and only when a lane's sum
-// of them passes 2^kLag (or is a NaN) is the maximum looked for, the
+// of them passes kMostWeight (or is a NaN) is the maximum looked for, the
 // accumulators rescaled and the weights taken anew: looking for it every time
 // cost as many instructions as the rest.
-template <class T, class C, int U>
-__device__ inline void weigh(Rows<C>* R, const f32x4 (&s)[2 * U], float scale, u32x4 (&pf)[U]) {
-    float sum;
-    auto take = [&](float m) {
-        float part[2] = {0.0f, 0.0f};
+template <class T, class C>
+__device__ inline float take_weights(const Rows<C>& R, const f32x4* s, float scale, u32x4* pf) {
+    float part[2] = {0.0f, 0.0f}, p[8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float p[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * u + (i >> 2)][i & 3], scale, -m));
-                part[i & 1] += p[i];
-            }
-            pf[u] = u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]),
-                          Mma<T>::pack(p[4], p[5]), Mma<T>::pack(p[6], p[7])};
-        }
-        sum = part[0] + part[1];
-    };
-    take(R->ref);
-    if (__any(!(sum <= kMostWeight))) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 2 * U; ++x)
-            top = fmaxf(fmaxf(fmaxf(top, s[x][0]), s[x][1]), fmaxf(s[x][2], s[x][3]));
-        top *= scale;
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m = fmaxf(R->m, top);
-        const float a = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(R->m - m);
-        R->m = m;
-        R->ref = m == -INFINITY ? kNoKey : m;
-        R->l *= a;
-#pragma unroll
-        for (int j = 0; j < C::NJ; ++j) R->o[j] *= a;
-        take(R->ref);
+    for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], scale, -R.ref));
+        part[i & 1] += p[i];
     }
-    R->l += sum;
+    *pf = u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]), Mma<T>::pack(p[4], p[5]),
+                Mma<T>::pack(p[6], p[7])};
+    return part[0] + part[1];
+}
+
+__device__ inline bool too_much(float sum) { return __any(!(sum <= kMostWeight)); }
+
+template <class T, class C>
+__device__ inline float move_maximum(Rows<C>* R, const f32x4* s, float scale, u32x4* pf) {
+    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * scale;
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m = fmaxf(R->m, top);
+    const float a = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(R->m - m);
+    R->m = m;
+    R->ref = m == -INFINITY ? kNoKey : m;
+    R->l *= a;
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) R->o[j] *= a;
+    return take_weights<T, C>(*R, s, scale, pf);
 }
 
 // In a matrix product a weight of 0 times an infinity or a NaN is a NaN, so in
@@ -732,8 +729,7 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             v_transpose(y, even, odd);
         };
 
-        bool odd = false;               // a value left out of a product
-        int32_t first_edge = -1;        // this wave's first step that not all rows see whole
+        int32_t first_odd = -1;         // this wave's first step whose product left values out
         int32_t key0 = P.key0 + part * kKeys;
         int32_t page = -1;
         int64_t off = -1;
@@ -758,7 +754,9 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             const bool partial = all_see < key0 + kKeys;
             if (valid != 0xffffffffu || partial) mask_scores(s, key0, limit, valid);
             u32x4 pf[1];
-            weigh<T, C, 1>(&R, s, A.scale, pf);
+            float sum = take_weights<T, C>(R, s, A.scale, pf);
+            if (too_much(sum)) sum = move_maximum<T, C>(&R, s, A.scale, pf);
+            R.l += sum;
             if (valid != 0xffffffffu) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -769,37 +767,33 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
                             for (int w = 0; w < C::VW; ++w) vr[i][c].w[w] = 0;
             }
             if (partial && P.seg.causal) {
-                if (first_edge < 0) first_edge = key0;
+                bool mine = false;
 #pragma unroll
-                for (int j = 0; j < C::NJ; j += 2) {
-                    u32x4 f[2];
-                    value_pair(j / C::VE, j % C::VE / 2, &f[0], &f[1]);
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int z = 0; z < 2; ++z)
+                    for (int c = 0; c < C::NC; ++c)
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const uint32_t w = finite_pair<T>(f[z][y]);
-                            odd = odd || w != f[z][y];
-                            f[z][y] = w;
+                        for (int w = 0; w < C::VW; ++w) {
+                            const uint32_t x = vr[i][c].w[w];
+                            const uint32_t y = C::EB == 2 ? finite_pair<T>(x) : finite_quad(x);
+                            mine = mine || x != y;
+                            vr[i][c].w[w] = y;
                         }
-                    R.o[j] = Mma<T>::run(f[0], pf[0], R.o[j]);
-                    R.o[j + 1] = Mma<T>::run(f[1], pf[0], R.o[j + 1]);
-                }
-            } else {
+                if (first_odd < 0 && __any(mine)) first_odd = key0;
+            }
 #pragma unroll
-                for (int j = 0; j < C::NJ; j += 2) {
-                    u32x4 f[2];
-                    value_pair(j / C::VE, j % C::VE / 2, &f[0], &f[1]);
-                    R.o[j] = Mma<T>::run(f[0], pf[0], R.o[j]);
-                    R.o[j + 1] = Mma<T>::run(f[1], pf[0], R.o[j + 1]);
-                }
+            for (int j = 0; j < C::NJ; j += 2) {
+                u32x4 f[2];
+                value_pair(j / C::VE, j % C::VE / 2, &f[0], &f[1]);
+                R.o[j] = Mma<T>::run(f[0], pf[0], R.o[j]);
+                R.o[j + 1] = Mma<T>::run(f[1], pf[0], R.o[j + 1]);
             }
             if (AHEAD && more) load_values(off_next);
             off = off_next;
         }
-        if (__any(odd)) {
+        if (first_odd >= 0) {
             // the wave's own steps only: `step` apart
-            for (int32_t t = first_edge; t < P.key1; t += step)
+            for (int32_t t = first_odd; t < P.key1; t += step)
                 add_not_finite<T, C, false>(A, P.lists, P.pg0, vhd, t,
                                             t + kKeys < P.key1 ? t + kKeys : P.key1, limit, &R);
         }
@@ -840,14 +834,13 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
 // ---------------------------------------------------------------- wide --
 
 // A wide tile's shapes: RT row tiles of 16 per wave, KT keys staged at a time
-// in one of two buffers, U steps of 32 keys computed together.
+// in one of two buffers.
 template <class C>
 struct Wide {
     static constexpr int DP = C::KS * 32;
     static constexpr int RT = DP <= 128 ? 2 : 1;
     static constexpr int ROWS = kWaves * 16 * RT;
     static constexpr int KT = DP <= 128 ? 128 : 64;
-    static constexpr int U = DP <= 128 ? 2 : 1;
     static constexpr int NB = KT / kKeys;               // steps of 32 keys
     static constexpr int WPG = 128 / KT;                // waves that stage one group of 16 keys
     static constexpr int VR = 16 / WPG;                 // V rows that a wave stages
@@ -1025,32 +1018,62 @@ struct WideState {
     u32x4 q[W::RT][C::KS];
     Rows<C> R[W::RT];
     int32_t most, all_see;
-    int32_t first_edge;                 // first step that not all rows see whole, or -1
-    bool odd;                           // a value left out of a product
+    int32_t first_odd;                  // first tile that values were taken out of, or -1
 };
 
-// The keys of one buffer against the wave's rows.
+// Clears the infinities and NaN in a wave's eighth of a buffer's V rows; whether there were any.
+template <class T, class C>
+__device__ inline bool take_out_not_finite(char* buf, int wave) {
+    using W = Wide<C>;
+    constexpr int N = W::KT * W::RB / kWaves / 1024;
+    char* v = buf + W::KF * 1024 + wave * (N * 1024) + here_lane() * 16;
+    bool mine = false;
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+        u32x4 x = *reinterpret_cast<const u32x4*>(v + i * 1024);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const uint32_t w = finite_pair<T>(x[y]);
+            mine = mine || w != x[y];
+            x[y] = w;
+        }
+        *reinterpret_cast<u32x4*>(v + i * 1024) = x;
+    }
+    return __any(mine);
+}
+
+// The order of a block of N operands, each read from shared memory and used in
+// RT products, beside the instructions that take the last step's weights:
+// operands are read AHEAD of their products (left to itself the compiler asks
+// for one and waits for it), and vector instructions stand between products.
+template <int N, int RT>
+__device__ inline void interleave() {
+    constexpr int AHEAD = N < 6 ? N : 6;
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);          // shared memory reads
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, RT, 0);         // products
+        if (i + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4 * RT, 0);     // vector
+        __builtin_amdgcn_sched_group_barrier(0x400, RT, 0);         // exponentials
+    }
+}
+
+// The keys of one buffer against the wave's rows: scores of a step of 32 keys
+// while the weights of the step before are taken, then that step's product
+// with V, so that matrix and vector unit work side by side.
 template <class T, class C>
 __device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>* S, int32_t tile0,
                                  const char* buf, const uint32_t* flags) {
     using W = Wide<C>;
-    const int lane = threadIdx.x & 63;
     const char* v = buf + W::KF * 1024;
-#pragma unroll 1
-    for (int b = 0; b < W::NB; b += W::U) {
-        const int32_t key0 = tile0 + b * kKeys;
-        if (key0 >= S->most) break;
-        const bool edge = S->all_see < key0 + W::U * kKeys;     // some row does not see some key
-        bool masked = edge;
-        uint32_t valid[W::U];
+    int32_t n = (S->most - tile0 + kKeys - 1) / kKeys;          // steps that some row sees
+    n = n < W::NB ? n : W::NB;
+    if (n <= 0) return;
+    const int lane = here_lane();
+    auto scores_of = [&](int b, f32x4 (&s)[W::RT][2]) {
 #pragma unroll
-        for (int u = 0; u < W::U; ++u) {
-            valid[u] = __builtin_amdgcn_readfirstlane(flags[b + u]);
-            masked = masked || valid[u] != 0xffffffffu;
-        }
-        f32x4 s[W::RT][2 * W::U];
-#pragma unroll
-        for (int x = 0; x < 2 * W::U; ++x) {
+        for (int x = 0; x < 2; ++x) {
 #pragma unroll
             for (int t = 0; t < W::RT; ++t) s[t][x] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -1061,54 +1084,58 @@ __device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>*
                 for (int t = 0; t < W::RT; ++t) s[t][x] = Mma<T>::run(f, S->q[t][ks], s[t][x]);
             }
         }
-        u32x4 pf[W::RT][W::U];
+    };
+    auto mask = [&](int b, f32x4 (&s)[W::RT][2]) {
+        const int32_t key0 = tile0 + b * kKeys;
+        const uint32_t valid = __builtin_amdgcn_readfirstlane(flags[b]);
+        if (valid != 0xffffffffu || S->all_see < key0 + kKeys) {
 #pragma unroll
-        for (int t = 0; t < W::RT; ++t) {
-            if (masked) {
-#pragma unroll
-                for (int u = 0; u < W::U; ++u)
-                    mask_scores(&s[t][2 * u], key0 + u * kKeys, S->limit[t], valid[u]);
-            }
-            weigh<T, C, W::U>(&S->R[t], s[t], A.scale, pf[t]);
+            for (int t = 0; t < W::RT; ++t) mask_scores(s[t], key0, S->limit[t], valid);
         }
-        const int vb = v_base<C>();
-        if (edge && P.seg.causal) {
-            if (S->first_edge < 0) S->first_edge = key0;
+    };
+    const int vb = v_base<C>();
+    auto step = [&](int b, f32x4 (&s)[W::RT][2], f32x4 (&next)[W::RT][2]) {
+        u32x4 pf[W::RT];
+        float sum[W::RT];
+        if (b + 1 < n) {
+            scores_of(b + 1, next);
 #pragma unroll
-            for (int u = 0; u < W::U; ++u)
-#pragma unroll
-                for (int j = 0; j < C::NJ; ++j) {
-                    u32x4 f = v_frag<C>(v, vb, b + u, j);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const uint32_t w = finite_pair<T>(f[y]);
-                        S->odd = S->odd || w != f[y];
-                        f[y] = w;
-                    }
-#pragma unroll
-                    for (int t = 0; t < W::RT; ++t)
-                        S->R[t].o[j] = Mma<T>::run(f, pf[t][u], S->R[t].o[j]);
-                }
+            for (int t = 0; t < W::RT; ++t) sum[t] = take_weights<T, C>(S->R[t], s[t], A.scale, &pf[t]);
+            interleave<2 * C::KS, W::RT>();
         } else {
 #pragma unroll
-            for (int u = 0; u < W::U; ++u)
-#pragma unroll
-                for (int j = 0; j < C::NJ; ++j) {
-                    const u32x4 f = v_frag<C>(v, vb, b + u, j);
-#pragma unroll
-                    for (int t = 0; t < W::RT; ++t)
-                        S->R[t].o[j] = Mma<T>::run(f, pf[t][u], S->R[t].o[j]);
-                }
+            for (int t = 0; t < W::RT; ++t) sum[t] = take_weights<T, C>(S->R[t], s[t], A.scale, &pf[t]);
         }
+#pragma unroll
+        for (int t = 0; t < W::RT; ++t) {
+            if (__builtin_expect(too_much(sum[t]), 0))
+                sum[t] = move_maximum<T, C>(&S->R[t], s[t], A.scale, &pf[t]);
+            S->R[t].l += sum[t];
+        }
+#pragma unroll
+        for (int j = 0; j < C::NJ; ++j) {
+            const u32x4 f = v_frag<C>(v, vb, b, j);
+#pragma unroll
+            for (int t = 0; t < W::RT; ++t) S->R[t].o[j] = Mma<T>::run(f, pf[t], S->R[t].o[j]);
+        }
+        if (b + 1 < n) mask(b + 1, next);
+    };
+    f32x4 s[2][W::RT][2];
+    scores_of(0, s[0]);
+    mask(0, s[0]);
+#pragma unroll 1
+    for (int b = 0; b < n; b += 2) {
+        step(b, s[0], s[1]);
+        if (b + 1 < n) step(b + 1, s[1], s[0]);
     }
 }
 
-// flags: [2][NB] words, a bit per key that is there.
+// flags: [2][NB] words, a bit per key that is there; odds: a word per wave.
 template <class T, class C>
 __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* buf0, char* buf1,
-                         uint32_t* flags) {
+                         uint32_t* flags, uint32_t* odds) {
     using W = Wide<C>;
-    const int lane = here_lane(), a = lane & 15;
+    const int a = here_lane() & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t kvh = P.set;
     count_skipped(A, P, wave);
@@ -1128,8 +1155,7 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
     if (last > P.seg.ntok - 1) last = P.seg.ntok - 1;
     // keys that some row of this wave sees, and that every one does
     S.most = S.all_see = P.key1;
-    S.first_edge = -1;
-    S.odd = false;
+    S.first_odd = -1;
     if (P.seg.causal) {
         if (past + last + 1 < S.most) S.most = past + last + 1;
         S.all_see = past + first + 1;
@@ -1161,6 +1187,18 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
             page = stage_page<C>(A, P, tile0 + 2 * W::KT, wave);
             stage_load<T, C>(A, &next, kh, vhd, wave, there, ft);
         }
+        // where some row of the workgroup does not see some key, values that are
+        // not finite leave the buffer (see add_not_finite); once some have, the
+        // piece's later ones are added whatever they are
+        if (P.seg.causal && tile0 + W::KT > past + at + 1) {
+            const bool mine = take_out_not_finite<T, C>(here, wave);
+            if ((threadIdx.x & 63) == 0) odds[wave] = mine ? 1u : 0u;
+            __syncthreads();
+            uint32_t any = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) any |= odds[w];
+            if (S.first_odd < 0 && __builtin_amdgcn_readfirstlane(any) != 0) S.first_odd = tile0;
+        }
         wide_tile<T, C>(A, P, &S, tile0, here, fh);
         if (more) stage_store<T, C>(next, wave, there);
         __syncthreads();
@@ -1169,10 +1207,10 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
         turn(tile0, buf0, buf1, flags, flags + W::NB);
         if (tile0 + W::KT < P.key1) turn(tile0 + W::KT, buf1, buf0, flags + W::NB, flags);
     }
-    if (__any(S.odd)) {
+    if (S.first_odd >= 0) {
 #pragma unroll
         for (int t = 0; t < W::RT; ++t)
-            add_not_finite<T, C, true>(A, P.lists, P.pg0, vhd, S.first_edge, S.most, S.limit[t], &S.R[t]);
+            add_not_finite<T, C, true>(A, P.lists, P.pg0, vhd, S.first_odd, S.most, S.limit[t], &S.R[t]);
     }
 #pragma unroll
     for (int t = 0; t < W::RT; ++t) {
@@ -1351,6 +1389,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
     __shared__ __attribute__((aligned(16))) char buf0[S::BUF0];
     __shared__ __attribute__((aligned(16))) char buf1[S::BUF];
     __shared__ uint32_t flags[2 * Wide<C>::NB];
+    __shared__ uint32_t odds[kWaves];
     const Mine M = plan_work<LINES>(A, &plan, blockIdx.x, gridDim.x);
     if (M.lo >= M.hi) return;
     const bool wide_line = LINES == 3 && M.line == 1;
@@ -1419,7 +1458,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
             // a piece without a step of its own leaves nothing (k_attend_join sees it the same way)
             if (to.kind == kSlot && P.key0 >= P.key1) continue;
             if constexpr (LINES == 3) {
-                if (wide_line) run_wide<T, C>(A, P, to, buf0, buf1, flags);
+                if (wide_line) run_wide<T, C>(A, P, to, buf0, buf1, flags, odds);
             }
             if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(buf0));
         }
