@@ -63,7 +63,8 @@ constexpr int kWaves = 8;               // waves of an attention workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kKeys = 32;               // keys of one step of a wave
 constexpr int kThinRows = 16;
-constexpr int kJoinWaves = 4;
+constexpr int kJoinWaves = 8;
+constexpr int kJoinParts = 4;
 
 // A row's reference maximum may lag the true one while a lane's weights of one
 // step sum to no more than this: they stay exact in every type here.
@@ -81,6 +82,19 @@ __device__ inline int here_lane() {
     asm volatile("" : "+v"(lane));
     return lane;
 }
+
+// The item that begins in a workgroup's piece and ends in a later one's, if there is one.
+struct Split {
+    int64_t item;                       // its first unit
+    int32_t last;                       // the piece that it ends in; -1: no such item
+    int32_t w, slot0;                   // this piece, the line's first slot
+    int32_t wide;
+    int32_t tok0, ntok;                 // of its segment
+    int32_t set, tile;
+    int32_t keys;                       // that its last row sees
+    int32_t extra;
+    int32_t pad[2];
+};
 
 struct Lists {                          // where a kind of segment's keys live
     const int64_t* pg_off;
@@ -134,8 +148,9 @@ struct Args {
     int32_t wide_item;
     float wide_weight;                  // time of a wide key over a thin key's
     // workspace
-    int64_t* starts;                    // [num_groups + num_reqs]: segment starts on its line
-    int64_t* plan;                      // [4]: units and workgroups of the thin and the wide line
+    struct Placed* placed;              // [num_groups + num_reqs]: segments on their lines
+    int64_t* plan;                      // [6]: Cuts of the thin and the wide line, workgroups of each
+    struct Split* splits;               // [grid]
     float* slot_o;                      // [2 * grid][slot rows][D]
     float* slot_ml;                     // [2 * grid][slot rows][2]
     float* row_o;                       // [2][T][Hq][D]: own, prefix (only with prefixes)
@@ -235,6 +250,7 @@ __device__ inline int32_t cut_key(const Seg& g, int64_t x, int step_log2) {
 // A line of n units cut into `wgs` pieces whose lengths differ by one at most.
 struct Cuts {
     int64_t q, r;               // r pieces of q + 1 units, then pieces of q
+    __device__ inline Cuts() {}
     __device__ inline Cuts(int64_t n, int64_t wgs) {
         q = wgs > 0 ? n / wgs : 0;
         r = n - q * wgs;
@@ -244,6 +260,13 @@ struct Cuts {
         const int64_t big = (q + 1) * r;
         return x < big ? x / (q + 1) : r + (x - big) / q;
     }
+};
+
+// A segment as k_attend leaves it for the join.
+struct Placed {
+    Seg g;
+    int64_t start;              // its first unit on its line
+    int64_t units;              // of a head set
 };
 
 // Page id of key t (any id when the list has no such entry), and the byte
@@ -1249,6 +1272,7 @@ struct Plan {
 // for k_attend_join.
 struct Mine {
     int line;
+    int64_t n, wgs;             // its units and workgroups
     int64_t w, lo, hi;
     int64_t slot0;              // the line's first slot
     int32_t seg;
@@ -1266,10 +1290,13 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
         const int32_t s = c0 + static_cast<int32_t>(threadIdx.x);
         cost = 0;
         wide = false;
+        Seg mine;
+        int64_t units = 0;
         if (s < nseg) {
-            const Seg g = segment(A, s);
-            cost = set_units(g) * g.sets;
-            wide = LINES == 3 && g.wide;
+            mine = segment(A, s);
+            units = set_units(mine);
+            cost = units * mine.sets;
+            wide = LINES == 3 && mine.wide;
         }
         const int64_t x = wave_scan(wide ? 0 : cost), y = LINES == 3 ? wave_scan(wide ? cost : 0) : 0;
         if (lane == 63) {
@@ -1286,7 +1313,7 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
             total[1] += sy;
         }
         start = wide ? before[1] + y - cost : before[0] + x - cost;
-        if (block == 0 && s < nseg) A.starts[s] = start;
+        if (block == 0 && s < nseg) A.placed[s] = Placed{mine, start, units};
         if (c0 + kThreads < nseg) __syncthreads();
     }
     total[0] = uniform(total[0]);
@@ -1312,10 +1339,13 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
         wgs[i] = uniform(wgs[i] > want ? want : wgs[i]);
     }
     if (block == 0 && threadIdx.x == 0) {
-        A.plan[0] = total[0];
-        A.plan[1] = wgs[0];
-        A.plan[2] = total[1];
-        A.plan[3] = wgs[1];
+        const Cuts thin(total[0], wgs[0]), wide_cuts(total[1], wgs[1]);
+        A.plan[0] = thin.q;
+        A.plan[1] = thin.r;
+        A.plan[2] = wide_cuts.q;
+        A.plan[3] = wide_cuts.r;
+        A.plan[4] = wgs[0];
+        A.plan[5] = wgs[1];
     }
     // consecutive pieces on one XCD (workgroups are dealt to the eight in turn)
     Mine M;
@@ -1327,7 +1357,9 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     M.w = xcd * (mine / 8) + jj;
     M.lo = M.hi = 0;
     if (jj >= mine / 8) return M;
-    const Cuts cuts(M.line ? total[1] : total[0], mine);
+    M.n = M.line ? total[1] : total[0];
+    M.wgs = mine;
+    const Cuts cuts(M.n, mine);
     M.lo = uniform(cuts.start(M.w));
     M.hi = uniform(cuts.start(M.w + 1));
     if (M.lo >= M.hi) return M;
@@ -1390,6 +1422,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
     __shared__ __attribute__((aligned(16))) char buf1[S::BUF];
     __shared__ uint32_t flags[2 * Wide<C>::NB];
     __shared__ uint32_t odds[kWaves];
+    if (threadIdx.x == 0) A.splits[blockIdx.x].last = -1;
     const Mine M = plan_work<LINES>(A, &plan, blockIdx.x, gridDim.x);
     if (M.lo >= M.hi) return;
     const bool wide_line = LINES == 3 && M.line == 1;
@@ -1455,6 +1488,21 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
             to.part = pre ? 1 : 0;
             to.slot = static_cast<int32_t>(M.slot0 + 2 * M.w + (from_start ? 1 : 0));
             pos = end;
+            if (from_start && !to_end && threadIdx.x == 0) {
+                Split x;
+                x.item = item;
+                x.last = static_cast<int32_t>(Cuts(M.n, M.wgs).piece_of(item + len - 1));
+                x.w = static_cast<int32_t>(M.w);
+                x.slot0 = static_cast<int32_t>(M.slot0);
+                x.wide = wide_line;
+                x.tok0 = P.seg.tok0;
+                x.ntok = P.seg.ntok;
+                x.set = P.set;
+                x.tile = P.tile;
+                x.keys = static_cast<int32_t>(keys < P.seg.keys ? keys : P.seg.keys);
+                x.extra = P.seg.extra;
+                A.splits[blockIdx.x] = x;
+            }
             // a piece without a step of its own leaves nothing (k_attend_join sees it the same way)
             if (to.kind == kSlot && P.key0 >= P.key1) continue;
             if constexpr (LINES == 3) {
@@ -1486,87 +1534,12 @@ __device__ inline int32_t find_list(const int64_t* off, int32_t n, int64_t x) {
     return lo;
 }
 
-// What one part (prefix or own) of a row left, and where.
-struct PartOf {
-    int32_t w0, w1;             // workgroups that have pieces of its item; w0 > w1: none
-    int32_t slot0;
-    int32_t slot_row;
-    int64_t item;               // the item's first unit
-};
-
-__device__ inline PartOf part_of(const Args& A, const Seg& g, const Cuts& cuts, int64_t start,
-                                 int32_t wide_wgs, int32_t token, int32_t head) {
-    PartOf p;
-    p.w0 = 0;
-    p.w1 = -1;
-    p.slot0 = g.wide ? 0 : 2 * wide_wgs;
-    p.slot_row = 0;
-    p.item = 0;
-    const int32_t local = token - g.tok0;
-    if (g.tiles == 0 || local < 0 || local >= g.ntok) return p;
-    const int32_t kvh = head / A.G, hin = head - kvh * A.G;
-    const int32_t tile = local / g.tp;
-    const int32_t in_tile = local - tile * g.tp;
-    int32_t set;
-    if (g.wide) {
-        set = kvh;
-        p.slot_row = in_tile * A.G + hin;
-    } else {
-        const int32_t sub = hin / A.gv, vh = kvh * A.parts + sub;
-        set = vh / A.hs;
-        p.slot_row = (vh - set * A.hs) * kThinRows + in_tile * A.gv + hin - sub * A.gv;
-    }
-    p.item = start + set * set_units(g) + tile_start(g, tile);
-    p.w0 = static_cast<int32_t>(cuts.piece_of(p.item));
-    p.w1 = static_cast<int32_t>(cuts.piece_of(p.item + tile_keys(g, tile) + g.extra - 1));
-    return p;
-}
-
-// One wave joins the rows of 256 / DP neighbouring heads of one token: lane
-// holds 4 dims of one of them.  Bound by its launch and its dependent loads:
-// the lists that the token is in (guessed for one token per request, and
-// searched for otherwise), the partial sums' maxima and sums, and their rows.
-template <class T, int DP>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
-    constexpr int LPR = DP / 4, RPW = 64 / LPR;
-    const int lane = threadIdx.x & 63;
-    const int32_t hq = A.H * A.G;
-    const uint32_t per_token = (hq + RPW - 1) / RPW;
-    const int64_t wave = static_cast<int64_t>(blockIdx.x) * kJoinWaves +
-                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tok = (wave >> 32) == 0 ? static_cast<uint32_t>(wave) / per_token : wave / per_token;
-    if (tok >= A.T) return;
-    const int32_t token = static_cast<int32_t>(tok);
-    const int32_t head = static_cast<int32_t>(wave - tok * per_token) * RPW + lane / LPR;
-
-    int32_t r = token < A.num_reqs ? token : A.num_reqs - 1;
-    Seg own = uniform(segment(A, A.num_groups + r));
-    int64_t own_start = A.starts[A.num_groups + r];
-    const int64_t n0 = uniform(A.plan[0]), n1 = uniform(A.plan[2]);
-    const int32_t wgs0 = uniform(static_cast<int32_t>(A.plan[1]));
-    const int32_t wgs1 = uniform(static_cast<int32_t>(A.plan[3]));
-    if (token < own.tok0 || token >= own.tok0 + own.ntok) {
-        r = uniform(find_list(A.tok_off, A.num_reqs, token));
-        own = uniform(segment(A, A.num_groups + r));
-        own_start = A.starts[A.num_groups + r];
-    }
-    const int parts = A.num_groups > 0 ? 2 : 1;
-    Seg pre = own;
-    int64_t pre_start = 0;
-    if (parts == 2) {
-        const int32_t g = A.num_groups == 1 ? 0 : uniform(find_list(A.grp_off, A.num_groups, r));
-        pre = uniform(segment(A, g));
-        pre_start = A.starts[g];
-    }
-    const Cuts thin(n0, wgs0), wide(n1, wgs1);
-    const int d = lane % LPR * 4;
-    if (head >= hq) return;
-    const bool has_dims = d < A.D;
-    const int64_t row = static_cast<int64_t>(token) * hq + head;
-
-    float m = -INFINITY, l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-    auto add = [&](float2 ml, f32x4 x) {
+// Partial sums of one row under way: lane holds 4 dims of it.
+struct Sum {
+    float m, l;
+    f32x4 o;
+    __device__ inline Sum() : m(-INFINITY), l(0.0f), o{0, 0, 0, 0} {}
+    __device__ inline void add(float2 ml, f32x4 x) {
         if (ml.y == 0.0f) return;
         const float top = fmaxf(m, ml.x);
         const float ref = top == -INFINITY ? 0.0f : top;
@@ -1574,53 +1547,171 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
         m = top;
         l = l * w1 + ml.y * w2;
         o = o * w1 + x * w2;
-    };
-    for (int k = 0; k < parts; ++k) {
-        const Seg& g = k ? pre : own;
-        const Cuts& cuts = g.wide ? wide : thin;
-        const PartOf p = part_of(A, g, cuts, k ? pre_start : own_start, wgs1, token, head);
-        if (p.w0 > p.w1) continue;
-        if (p.w0 == p.w1) {
-            if (parts == 1) return;             // written by the workgroup that had it all
-            const int64_t at = static_cast<int64_t>(k) * A.T * hq + row;
-            const float2 ml = *reinterpret_cast<const float2*>(A.row_ml + at * 2);
-            add(ml, has_dims ? *reinterpret_cast<const f32x4*>(A.row_o + at * A.D + d) : f32x4{0, 0, 0, 0});
-            continue;
-        }
-        const int step_log2 = !g.wide ? 5 : (DP <= 128 ? 7 : 6);
-        // a workgroup has left its slot if its piece has a step of keys
-        const int32_t local = token - g.tok0;
-        const int64_t keys64 = tile_keys(g, local / g.tp);
-        const int32_t keys = static_cast<int32_t>(keys64 < g.keys ? keys64 : g.keys);
-        constexpr int B = 4;                    // slots under way at once
-        for (int32_t w0 = p.w0; w0 <= p.w1; w0 += B) {
-            float2 ml[B];
-            f32x4 x[B];
-#pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const int32_t w = w0 + i;
-                ml[i] = make_float2(0.0f, 0.0f);
-                x[i] = f32x4{0, 0, 0, 0};
-                if (w > p.w1) continue;
-                const int32_t k0 = w == p.w0 ? 0 : cut_key(g, cuts.start(w) - p.item, step_log2);
-                const int32_t k1 = w == p.w1 ? keys : cut_key(g, cuts.start(w + 1) - p.item, step_log2);
-                if (k0 >= k1) continue;
-                const int64_t at = static_cast<int64_t>(p.slot0 + 2 * w + (w == p.w0 ? 1 : 0)) * A.slot_rows + p.slot_row;
-                ml[i] = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);
-                if (has_dims) x[i] = *reinterpret_cast<const f32x4*>(A.slot_o + at * A.D + d);
-            }
-#pragma unroll
-            for (int i = 0; i < B; ++i) add(ml[i], x[i]);
-        }
     }
-    const float inv = l == 0.0f ? 0.0f : A.v_scale / l;
-    if (has_dims)
-        *reinterpret_cast<u32x2*>(A.out + static_cast<int64_t>(token) * A.out_stride +
-                                  (static_cast<int64_t>(head) * A.D + d) * 2) =
-            u32x2{Mma<T>::pack(o[0] * inv, o[1] * inv), Mma<T>::pack(o[2] * inv, o[3] * inv)};
-    if (d == 0 && A.lse != nullptr)
-        A.lse[row] = l == 0.0f ? -INFINITY
-                               : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    template <class T>
+    __device__ inline void store(const Args& A, int32_t token, int32_t head, int d) const {
+        const float inv = l == 0.0f ? 0.0f : A.v_scale / l;
+        if (d < A.D)
+            *reinterpret_cast<u32x2*>(A.out + static_cast<int64_t>(token) * A.out_stride +
+                                      (static_cast<int64_t>(head) * A.D + d) * 2) =
+                u32x2{Mma<T>::pack(o[0] * inv, o[1] * inv), Mma<T>::pack(o[2] * inv, o[3] * inv)};
+        if (d == 0 && A.lse != nullptr)
+            A.lse[static_cast<int64_t>(token) * A.H * A.G + head] =
+                l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    }
+};
+
+// Adds row `slot_row` of the pieces w0 .. w1 of an item that begins at unit
+// `item`; a workgroup has left its slot if its piece has a step of keys.
+__device__ inline void add_slots(const Args& A, Sum* sum, const Seg& g, const Cuts& cuts, int64_t item,
+                                 int32_t keys, int32_t w0, int32_t w1, int32_t slot0, int slot_row,
+                                 int d, int step_log2) {
+    constexpr int B = 4;                    // slots under way at once
+    for (int32_t w = w0; w <= w1; w += B) {
+        float2 ml[B];
+        f32x4 x[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            ml[i] = make_float2(0.0f, 0.0f);
+            x[i] = f32x4{0, 0, 0, 0};
+            const int32_t v = w + i;
+            if (v > w1) continue;
+            const int32_t k0 = v == w0 ? 0 : cut_key(g, cuts.start(v) - item, step_log2);
+            const int32_t k1 = v == w1 ? keys : cut_key(g, cuts.start(v + 1) - item, step_log2);
+            if (k0 >= k1) continue;
+            const int64_t at = static_cast<int64_t>(slot0 + 2 * v + (v == w0 ? 1 : 0)) * A.slot_rows + slot_row;
+            ml[i] = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);
+            if (d < A.D) x[i] = *reinterpret_cast<const f32x4*>(A.slot_o + at * A.D + d);
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) sum->add(ml[i], x[i]);
+    }
+}
+
+// Without prefixes: kJoinParts workgroups join the item that begins in a piece
+// and ends in a later one; workgroups behind those write the rows of requests
+// without keys, 64 requests a wave.
+template <class T, int DP>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Args A, int32_t pieces) {
+    constexpr int LPR = DP / 4, RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int d = lane % LPR * 4, sub_row = lane / LPR;
+    const int32_t hq = A.H * A.G;
+    const int32_t block = blockIdx.x;
+    if (block >= pieces * kJoinParts) {
+        const int32_t r0 = ((block - pieces * kJoinParts) * kJoinWaves + wave) * 64;
+        int32_t t0 = 0, n = 0;
+        if (r0 + lane < A.num_reqs && A.ctx[r0 + lane] <= 0) {
+            t0 = clamp_to(A.tok_off[r0 + lane], 0, A.T);
+            n = clamp_to(A.tok_off[r0 + lane + 1], t0, A.T) - t0;
+        }
+        for (uint64_t todo = __ballot(n > 0); todo != 0; todo &= todo - 1) {
+            const int who = __ffsll(static_cast<unsigned long long>(todo)) - 1;
+            const int64_t rows = static_cast<int64_t>(__shfl(n, who)) * hq;
+            const int32_t first = __shfl(t0, who);
+            for (int64_t x = sub_row; x < rows; x += RPW)
+                Sum().store<T>(A, first + static_cast<int32_t>(x / hq), static_cast<int32_t>(x % hq), d);
+        }
+        return;
+    }
+    const Split S = A.splits[block / kJoinParts];
+    if (S.last < 0) return;
+    Cuts cuts;
+    cuts.q = A.plan[S.wide ? 2 : 0];
+    cuts.r = A.plan[S.wide ? 3 : 1];
+    Seg g;
+    g.extra = S.extra;
+    const int step_log2 = S.wide ? (DP <= 128 ? 7 : 6) : 5;
+    const int rows = S.wide ? A.wide_tokens * A.G : A.hs * kThinRows;
+    for (int row = (block % kJoinParts * kJoinWaves + wave) * RPW + sub_row; row < rows;
+         row += kJoinParts * kJoinWaves * RPW) {
+        int32_t local, head;
+        bool live = true;
+        if (S.wide) {
+            local = S.tile * A.wide_tokens + row / A.G;
+            head = S.set * A.G + row % A.G;
+        } else {
+            const int a = row % kThinRows;
+            const int32_t vh = S.set * A.hs + row / kThinRows;
+            const int32_t kvh = vh / A.parts, hin = vh % A.parts * A.gv + a % A.gv;
+            local = S.tile * A.thin_tokens + a / A.gv;
+            head = kvh * A.G + hin;
+            live = a < A.thin_tokens * A.gv && kvh < A.H && hin < A.G;
+        }
+        if (!live || local >= S.ntok) continue;
+        Sum sum;
+        add_slots(A, &sum, g, cuts, S.item, S.keys, S.w, S.last, S.slot0, row, d, step_log2);
+        sum.store<T>(A, S.tok0 + local, head, d);
+    }
+}
+
+// With prefixes: the workgroups (x, .) join the rows of token x, each from its
+// two parts, a thin head's query heads (256 / DP of them) by a wave.
+// Bound by its launch and its dependent loads: the lists that the token is in
+// (guessed for one token per request, searched for otherwise), then the parts.
+template <class T, int DP>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
+    constexpr int LPR = DP / 4, RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t token = blockIdx.x;
+    const int d = lane % LPR * 4;
+
+    int32_t r = token < A.num_reqs ? token : A.num_reqs - 1;
+    Placed part[2] = {A.placed[A.num_groups + r], A.placed[0]};
+    Cuts thin, wide;
+    thin.q = uniform(A.plan[0]);
+    thin.r = uniform(A.plan[1]);
+    wide.q = uniform(A.plan[2]);
+    wide.r = uniform(A.plan[3]);
+    const int32_t wgs1 = uniform(static_cast<int32_t>(A.plan[5]));
+    if (uniform(static_cast<int32_t>(token < part[0].g.tok0 || token >= part[0].g.tok0 + part[0].g.ntok))) {
+        r = uniform(find_list(A.tok_off, A.num_reqs, token));
+        part[0] = A.placed[A.num_groups + r];
+    }
+    if (A.num_groups > 1) part[1] = A.placed[uniform(find_list(A.grp_off, A.num_groups, r))];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        part[k].g = uniform(part[k].g);
+        part[k].start = uniform(part[k].start);
+        part[k].units = uniform(part[k].units);
+    }
+
+    const int32_t per = (A.gv + RPW - 1) / RPW, units = A.H * A.parts * per;
+    {
+        const int32_t u = blockIdx.y * kJoinWaves + wave;
+        if (u >= units) return;
+        const int32_t vh = u / per, kvh = vh / A.parts, sub = vh - kvh * A.parts;
+        const int32_t in = (u - vh * per) * RPW + lane / LPR, hin = sub * A.gv + in;
+        const bool live = in < A.gv && hin < A.G;
+        const int32_t head = kvh * A.G + (live ? hin : 0);
+        const int64_t row = static_cast<int64_t>(token) * A.H * A.G + head;
+        Sum sum;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Seg& g = part[k].g;
+            const int32_t local = token - g.tok0;
+            if (g.tiles == 0 || local < 0 || local >= g.ntok) continue;
+            const Cuts& cuts = g.wide ? wide : thin;
+            const int32_t tile = local / g.tp, in_tile = local - tile * g.tp;
+            const int32_t set = g.wide ? kvh : vh / A.hs;
+            const int64_t item = part[k].start + set * part[k].units + tile_start(g, tile);
+            const int64_t keys = tile_keys(g, tile);
+            const int32_t w0 = static_cast<int32_t>(cuts.piece_of(item));
+            if (item + keys + g.extra <= cuts.start(w0 + 1)) {     // one workgroup had it all
+                const int64_t at = static_cast<int64_t>(k) * A.T * A.H * A.G + row;
+                const float2 ml = *reinterpret_cast<const float2*>(A.row_ml + at * 2);
+                sum.add(ml, d < A.D ? *reinterpret_cast<const f32x4*>(A.row_o + at * A.D + d) : f32x4{0, 0, 0, 0});
+            } else {
+                const int32_t w1 = static_cast<int32_t>(cuts.piece_of(item + keys + g.extra - 1));
+                const int slot_row = g.wide ? in_tile * A.G + (live ? hin : 0)
+                                            : (vh - set * A.hs) * kThinRows + in_tile * A.gv + (live ? in : 0);
+                add_slots(A, &sum, g, cuts, item, static_cast<int32_t>(keys < g.keys ? keys : g.keys), w0,
+                          w1, g.wide ? 0 : 2 * wgs1, slot_row, d, !g.wide ? 5 : (DP <= 128 ? 7 : 6));
+            }
+        }
+        if (live) sum.store<T>(A, token, head, d);
+    }
 }
 
 }  // namespace attend

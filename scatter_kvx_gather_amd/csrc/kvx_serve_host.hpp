@@ -132,7 +132,7 @@ struct AttendShape {
     bool pre_wide, own_wide;
     int32_t wide_rows;
     int32_t slot_rows;
-    int64_t starts, plan, slot_ml, slot_o, row_ml, row_o, bytes;    // offsets into the workspace
+    int64_t placed, plan, splits, slot_ml, slot_o, row_ml, row_o, bytes;    // offsets into the workspace
 };
 
 kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_reqs,
@@ -162,8 +162,9 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
         end += (b + 255) / 256 * 256;
         return at0;
     };
-    s->starts = take(static_cast<int64_t>(num_reqs) + num_groups, 8);
-    s->plan = take(4, 8);
+    s->placed = take(static_cast<int64_t>(num_reqs) + num_groups, sizeof(at::Placed));
+    s->plan = take(6, 8);
+    s->splits = take(kAttendGrid, sizeof(at::Split));
     s->slot_ml = take(2 * kAttendGrid * s->slot_rows, 8);
     s->slot_o = take(2 * kAttendGrid * s->slot_rows, 4 * static_cast<int64_t>(D));
     int64_t out_rows = 0;
@@ -176,18 +177,23 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     return KVX_OK;
 }
 
+struct AttendKernels {
+    const void *main, *join, *join_items;
+};
+
 template <class T, bool FP8, int DP>
-void attend_kernels(int lines, const void** main, const void** join) {
-    *main = lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 1>)
-                       : reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 3>);
-    *join = reinterpret_cast<const void*>(&at::k_attend_join<T, DP>);
+AttendKernels attend_kernels(int lines) {
+    return {lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 1>)
+                       : reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 3>),
+            reinterpret_cast<const void*>(&at::k_attend_join<T, DP>),
+            reinterpret_cast<const void*>(&at::k_attend_join_items<T, DP>)};
 }
 
 template <class T, bool FP8>
-void attend_kernels(int DP, int lines, const void** main, const void** join) {
-    if (DP == 64) attend_kernels<T, FP8, 64>(lines, main, join);
-    else if (DP == 128) attend_kernels<T, FP8, 128>(lines, main, join);
-    else attend_kernels<T, FP8, 256>(lines, main, join);
+AttendKernels attend_kernels(int DP, int lines) {
+    return DP == 64    ? attend_kernels<T, FP8, 64>(lines)
+           : DP == 128 ? attend_kernels<T, FP8, 128>(lines)
+                       : attend_kernels<T, FP8, 256>(lines);
 }
 
 kvx_status validate_attend(const kvx_reqs* reqs, const int32_t* ctx, const kvx_prefix* prefix,
@@ -450,8 +456,9 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     const double thin_ns = 2.0 * a.hs * g.Db / a.parts / 26.0;
     a.wide_weight = static_cast<float>(wide_ns / thin_ns);
     char* ws = static_cast<char*>(x.workspace);
-    a.starts = reinterpret_cast<int64_t*>(ws + s.starts);
+    a.placed = reinterpret_cast<at::Placed*>(ws + s.placed);
     a.plan = reinterpret_cast<int64_t*>(ws + s.plan);
+    a.splits = reinterpret_cast<at::Split*>(ws + s.splits);
     a.slot_ml = reinterpret_cast<float*>(ws + s.slot_ml);
     a.slot_o = reinterpret_cast<float*>(ws + s.slot_o);
     a.row_ml = reinterpret_cast<float*>(ws + s.row_ml);
@@ -459,26 +466,35 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.slot_rows = s.slot_rows;
 
     const int lines = s.own_wide || s.pre_wide ? 3 : 1;
-    const void *main = nullptr, *join = nullptr;
     const bool fp8 = layout->dtype == KVX_FP8;
-    if (x.dtype == KVX_BF16) {
-        if (fp8) attend_kernels<__bf16, true>(s.DP, lines, &main, &join);
-        else attend_kernels<__bf16, false>(s.DP, lines, &main, &join);
-    } else {
-        if (fp8) attend_kernels<_Float16, true>(s.DP, lines, &main, &join);
-        else attend_kernels<_Float16, false>(s.DP, lines, &main, &join);
-    }
-    const int per_wave = 256 / s.DP;
-    const int64_t waves = static_cast<int64_t>(a.T) * ((x.q_heads + per_wave - 1) / per_wave);
-    const int64_t join_grid = (waves + at::kJoinWaves - 1) / at::kJoinWaves;
-    if (join_grid > INT32_MAX) return KVX_E_RANGE;
+    const AttendKernels k = x.dtype == KVX_BF16
+                                ? (fp8 ? attend_kernels<__bf16, true>(s.DP, lines)
+                                       : attend_kernels<__bf16, false>(s.DP, lines))
+                                : (fp8 ? attend_kernels<_Float16, true>(s.DP, lines)
+                                       : attend_kernels<_Float16, false>(s.DP, lines));
     if (log_enabled())
         std::fprintf(stderr,
                      "kvx: attend reqs=%d groups=%d tokens=%lld heads=%d/%d dim=%d prefix=%s own=%s\n",
                      a.num_reqs, ng, static_cast<long long>(a.T), x.q_heads, g.H, a.D,
                      ng == 0 ? "none" : (s.pre_wide ? "wide" : "thin"), s.own_wide ? "wide" : "thin");
-    KVX_TRY(launch_one(main, kAttendGrid, at::kThreads, a, stream));
-    return launch_one(join, join_grid, 64 * at::kJoinWaves, a, stream);
+    KVX_TRY(launch_one(k.main, kAttendGrid, at::kThreads, a, stream));
+    if (ng > 0) {
+        const int32_t per_head = (a.gv + 256 / s.DP - 1) / (256 / s.DP);
+        const int32_t units = heads * per_head;
+        void* join_params[] = {&a};
+        return hipLaunchKernel(k.join, dim3(static_cast<uint32_t>(a.T), (units + at::kJoinWaves - 1) / at::kJoinWaves),
+                               dim3(64 * at::kJoinWaves), join_params, 0, stream) == hipSuccess
+                   ? KVX_OK
+                   : KVX_E_HIP;
+    }
+    int32_t pieces = static_cast<int32_t>(kAttendGrid);
+    const int64_t grid = pieces * at::kJoinParts +
+                         (a.num_reqs + 64 * at::kJoinWaves - 1) / (64 * at::kJoinWaves);
+    void* params[] = {&a, &pieces};
+    return hipLaunchKernel(k.join_items, dim3(static_cast<uint32_t>(grid)), dim3(64 * at::kJoinWaves), params,
+                           0, stream) == hipSuccess
+               ? KVX_OK
+               : KVX_E_HIP;
 }
 
 }  // extern "C"
