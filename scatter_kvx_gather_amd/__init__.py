@@ -632,19 +632,19 @@ def _token_rows(what: str, t: torch.Tensor, heads: int, dim: int) -> int:
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{what} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
-    if (dim > 1 and stride[2] != 1) or (heads > 1 and stride[1] != dim):
+    if (stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1):
         raise ValueError(f"{what} must be dense in its last two dimensions (strides {stride})")
     return (stride[0] if shape[0] > 1 else heads * dim) * t.element_size()
 
 
-def _one_device(first: torch.Tensor, *others) -> torch.device:
-    """All tensors of a call on one GPU, which the launch goes to."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"kvx calls take device tensors; got a {dev} tensor")
+def _one_device(first: torch.Tensor, *others) -> int:
+    """Index of the GPU that all tensors of a call are on, which the launch goes to."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"kvx calls take device tensors; got a {first.device} tensor")
     for t in others:
-        if t is not None and not isinstance(t, int) and t.device != dev:
-            raise ValueError(f"tensors on {dev} and on {t.device} in one call")
+        if t is not None and t.__class__ is not int and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and on {t.device} in one call")
     return dev
 
 
@@ -655,12 +655,18 @@ def _pool_tensor(pool: "Pool") -> Optional[torch.Tensor]:
     return next((t for t in keep if isinstance(t, torch.Tensor)), None)
 
 
-def _on(dev: torch.device, stream, call) -> int:
-    """call(stream handle) with `dev` current; the default stream is dev's current one."""
-    if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
+# The current stream's handle without a Stream object around it (1 us of a call's 8).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _launch(dev: int, stream, fn, *args) -> int:
+    """fn(*args, stream handle) with GPU `dev` current; the default stream is
+    that GPU's current one."""
+    if dev == torch.cuda.current_device():
+        return fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
     with torch.cuda.device(dev):
-        return call(_stream(stream))
+        return fn(*args, _stream(stream))
 
 
 def _block_layout(name: str) -> int:
@@ -718,10 +724,8 @@ def build_tables(out: BatchTables, page_size: int, add_len: torch.Tensor, free_i
             raise ValueError("held is the output's own table: alternate two BatchTables")
         _one_device(out.ctx_len, have_len, held.pg_off, held.page_ids)
     dev = _one_device(out.ctx_len, add_len, free_ids)
-    lib = load_library()
-    _check(_on(dev, stream, lambda st: lib.kvx_build_tables(
-        n, page_size, have, add, held._c if have else None, free, free_ids.numel(), out._c, st)),
-        "kvx_build_tables")
+    _check(_launch(dev, stream, (_lib or load_library()).kvx_build_tables, n, page_size, have, add,
+                   held._c if have else None, free, free_ids.numel(), out._c), "kvx_build_tables")
 
 
 def append(layout: Layout, layer: int, pool: Pool, slots: torch.Tensor, k: torch.Tensor,
@@ -742,9 +746,8 @@ def append(layout: Layout, layer: int, pool: Pool, slots: torch.Tensor, k: torch
     _counter(skipped)
     dev = _one_device(k, v, slots, _pool_tensor(pool), skipped)
     rows = _CRows(k.data_ptr(), v.data_ptr(), ks, vs, n, _TORCH_CODES[k.dtype], k_scale, v_scale)
-    lib, bl = load_library(), _block_layout(block_layout)
-    _check(_on(dev, stream, lambda st: lib.kvx_append(
-        layout._c, layer, pool._c, bl, at, rows, _ptr(skipped), st)), "kvx_append")
+    _check(_launch(dev, stream, (_lib or load_library()).kvx_append, layout._c, layer, pool._c,
+                   _block_layout(block_layout), at, rows, _ptr(skipped)), "kvx_append")
 
 
 class Prefix:
@@ -808,7 +811,7 @@ def attend(layout: Layout, layer: int, pool: Pool, reqs: Requests, ctx_len: torc
                       _pool_tensor(pool), workspace, skipped)
     if prefix is not None:
         _one_device(q, prefix.grp_off, prefix.lens, prefix.table.pg_off, prefix.table.page_ids)
-    lib, bl = load_library(), _block_layout(block_layout)
+    lib, bl = _lib or load_library(), _block_layout(block_layout)
     if workspace is None:
         need = attend_workspace(layout, reqs, hq, prefix)
         if stream is None:
@@ -824,6 +827,5 @@ def attend(layout: Layout, layer: int, pool: Pool, reqs: Requests, ctx_len: torc
                     hq, _TORCH_CODES[q.dtype], d ** -0.5 if scale is None else scale, k_scale,
                     v_scale, ATTEND_CAUSAL if causal else 0, workspace.data_ptr(),
                     _nbytes(workspace))
-    _check(_on(dev, stream, lambda st: lib.kvx_attend(
-        layout._c, layer, pool._c, bl, reqs._c, ctx, table._c,
-        prefix._c if prefix is not None else None, a, _ptr(skipped), st)), "kvx_attend")
+    _check(_launch(dev, stream, lib.kvx_attend, layout._c, layer, pool._c, bl, reqs._c, ctx, table._c,
+                   prefix._c if prefix is not None else None, a, _ptr(skipped)), "kvx_attend")

@@ -245,6 +245,7 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
     a.num_free = num_free;
     a.num_reqs = num_reqs;
     a.page_size = page_size;
+    a.page_shift = shift_of(page_size);
     a.ctx = out->ctx_len;
     a.tok_off = out->tok_off;
     a.pg_off = out->pg_off;
@@ -253,14 +254,21 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
     a.slots = out->slots;
     a.cap_tokens = out->cap_tokens;
     a.totals = out->totals;
-    int64_t grid = std::max((out->cap_tokens + tb::kSlotWindow - 1) / tb::kSlotWindow,
-                            (out->cap_ids + tb::kIdWindow - 1) / tb::kIdWindow);
-    grid = std::max<int64_t>(grid, 1);
+    auto grid_of = [&](int64_t slot_run, int64_t id_run) {
+        const int64_t s = slot_run * tb::kBuildThreads, i = id_run * tb::kBuildThreads;
+        return std::max<int64_t>(1, std::max(out->cap_tokens / s + (out->cap_tokens % s != 0),
+                                             out->cap_ids / i + (out->cap_ids % i != 0)));
+    };
+    int64_t grid = grid_of(1, 1);
+    const void* fn = reinterpret_cast<const void*>(&tb::k_build_tables<1, 1>);
+    if (grid > tb::kShortGrid) {
+        grid = grid_of(tb::kLongSlotRun, tb::kLongIdRun);
+        fn = reinterpret_cast<const void*>(&tb::k_build_tables<tb::kLongSlotRun, tb::kLongIdRun>);
+    }
     if (log_enabled())
         std::fprintf(stderr, "kvx: build_tables reqs=%d page=%d grid=%lld\n", num_reqs, page_size,
                      static_cast<long long>(grid));
-    return launch_one(reinterpret_cast<const void*>(&tb::k_build_tables), grid, tb::kBuildThreads, a,
-                      stream);
+    return launch_one(fn, grid, tb::kBuildThreads, a, stream);
 }
 
 kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* pool,
@@ -330,8 +338,10 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.vh_magic = magic(a.VH);
     a.scale[0] = rows->k_scale;
     a.scale[1] = rows->v_scale;
+    a.inverse[0] = 1.0f / rows->k_scale;
+    a.inverse[1] = 1.0f / rows->v_scale;
     a.skipped = skipped;
-    const int64_t per = static_cast<int64_t>(tb::kAppendThreads) * tb::kPieces;
+    const int64_t per = tb::kAppendThreads;
     const int64_t grid = (rows->num_tokens * 2 * a.V + per - 1) / per;
     const void* fn = reinterpret_cast<const void*>(&tb::k_append<tb::kCopyBytes>);
     if (!copies)

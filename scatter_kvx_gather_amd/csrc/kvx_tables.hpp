@@ -16,16 +16,24 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // h_r = ceil(have[r] / B) held ones, three exclusive sums over the requests
 // (of a, P and P - h) give the token offsets, the table offsets and the place
 // of each request's new pages in the free list.  The outputs are cut into
-// windows of kSlotWindow slots and kIdWindow page ids, one workgroup each.
-// Every workgroup sums the requests itself, kChunk at a time, keeps a chunk's
-// sums in shared memory and fills the outputs of its window that belong to the
-// chunk, each found by a binary search there: one launch, no order between
+// windows of slots and page ids, one workgroup each.  Every workgroup sums the
+// requests itself, kChunk at a time, keeps a chunk's sums in shared memory and
+// fills the outputs of its window that belong to the chunk, each run of a
+// thread found by a binary search there: one launch, no order between
 // workgroups, and no request's length makes one workgroup's work longer.
+//
+// Bound by the chain launch - lengths - sums - search - ids of a workgroup, not
+// by bytes.  One slot and one id a thread shorten the chain (a decode step of
+// 64 requests 5.5 us against 8.0 with 4 and 2, 32 prompts page by token 5.4
+// against 7.5); with many workgroups their sums are what counts, and 4 and 2
+// are faster (2048 requests, 540 thousand ids: 18.7 us against 25.3).  The host
+// takes the short runs up to kShortGrid workgroups.
 constexpr int kBuildThreads = 256;
 constexpr int kPerThread = 4;
 constexpr int kChunk = kBuildThreads * kPerThread;
-constexpr int kSlotWindow = 2048;
-constexpr int kIdWindow = 1024;
+constexpr int kLongSlotRun = 4;         // outputs of a thread in a large grid
+constexpr int kLongIdRun = 2;
+constexpr int64_t kShortGrid = 512;
 
 struct BuildArgs {
     const int32_t* have;        // or NULL: none
@@ -37,6 +45,7 @@ struct BuildArgs {
     int64_t num_free;
     int32_t num_reqs;
     int32_t page_size;
+    int32_t page_shift;         // log2(page_size), or -1
     int32_t* ctx;
     int64_t* tok_off;
     int64_t* pg_off;
@@ -46,6 +55,12 @@ struct BuildArgs {
     int64_t cap_tokens;
     int64_t* totals;            // or NULL
 };
+
+// x / page_size; lengths and their sum with a page size fit 32 bits.
+template <class Args>
+__device__ inline uint32_t page_index(const Args& A, uint32_t x) {
+    return A.page_shift >= 0 ? x >> A.page_shift : x / static_cast<uint32_t>(A.page_size);
+}
 
 struct Sums {
     int64_t tok, pg, fresh;
@@ -77,7 +92,7 @@ __device__ inline int last_not_above(const int64_t* off, int n, int64_t x) {
 // Page k of request r (i-th of the chunk): a held page, or one of the free list; -1 if there is none.
 __device__ inline int32_t page_of(const BuildArgs& A, const BuildShared& S, int32_t r, int i,
                                   int64_t k) {
-    const int64_t held = (static_cast<int64_t>(S.have[i]) + A.page_size - 1) / A.page_size;
+    const int64_t held = page_index(A, static_cast<uint32_t>(S.have[i]) + A.page_size - 1);
     if (k < held) {
         const int64_t off = A.held_off[r];
         if (off < -k || off >= A.num_held - k) return -1;
@@ -87,7 +102,9 @@ __device__ inline int32_t page_of(const BuildArgs& A, const BuildShared& S, int3
     return at < A.num_free ? A.free_ids[at] : -1;
 }
 
+template <int kSlotRun, int kIdRun>
 __global__ __launch_bounds__(kBuildThreads) void k_build_tables(const BuildArgs A) {
+    constexpr int kSlotWindow = kBuildThreads * kSlotRun, kIdWindow = kBuildThreads * kIdRun;
     __shared__ BuildShared S;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const bool first = blockIdx.x == 0;
@@ -109,8 +126,9 @@ __global__ __launch_bounds__(kBuildThreads) void k_build_tables(const BuildArgs 
                 if (h + a > INT32_MAX) a = INT32_MAX - h;
             }
             have[i] = static_cast<int32_t>(h);
-            const int64_t b = A.page_size;
-            const int64_t pages = (h + a + b - 1) / b, held = (h + b - 1) / b;
+            const uint32_t b = A.page_size;
+            const int64_t pages = page_index(A, static_cast<uint32_t>(h + a) + b - 1);
+            const int64_t held = page_index(A, static_cast<uint32_t>(h) + b - 1);
             mine[i] = sum;                              // exclusive inside the thread
             sum = sum + Sums{a, pages, pages - held};
         }
@@ -151,18 +169,47 @@ __global__ __launch_bounds__(kBuildThreads) void k_build_tables(const BuildArgs 
                 A.ctx[c0 + j] = S.have[j] + static_cast<int32_t>(S.tok[j + 1] - S.tok[j]);
             }
         }
-        const int64_t s0 = slot0 > run.tok ? slot0 : run.tok, s1 = slot1 < all.tok ? slot1 : all.tok;
-        for (int64_t x = s0 + tid; x < s1; x += kBuildThreads) {
-            const int i = last_not_above(S.tok, n, x);
-            const int64_t t = S.have[i] + (x - S.tok[i]);
-            const int64_t k = t / A.page_size;
-            const int32_t page = page_of(A, S, c0 + i, i, k);
-            A.slots[x] = page < 0 ? -1 : static_cast<int64_t>(page) * A.page_size + (t - k * A.page_size);
+        // runs of neighbouring outputs per thread: one search, then a walk along
+        // the chunk's requests; all of a run's table reads are under way at once
+        const int64_t s1 = slot1 < all.tok ? slot1 : all.tok;
+        for (int64_t x0 = slot0 + tid * kSlotRun; x0 < s1; x0 += kBuildThreads * kSlotRun) {
+            if (x0 + kSlotRun <= run.tok) continue;
+            const int64_t from = x0 > run.tok ? x0 : run.tok;
+            int i = last_not_above(S.tok, n, from);
+            int32_t page[kSlotRun];
+            uint32_t in_page[kSlotRun];
+#pragma unroll
+            for (int y = 0; y < kSlotRun; ++y) {
+                const int64_t x = x0 + y;
+                page[y] = -1;
+                if (x < from || x >= s1) continue;
+                while (i + 1 < n && S.tok[i + 1] <= x) ++i;
+                const uint32_t t = S.have[i] + static_cast<uint32_t>(x - S.tok[i]);
+                const uint32_t k = page_index(A, t);
+                in_page[y] = t - k * A.page_size;
+                page[y] = page_of(A, S, c0 + i, i, k);
+            }
+#pragma unroll
+            for (int y = 0; y < kSlotRun; ++y)
+                if (x0 + y >= from && x0 + y < s1)
+                    A.slots[x0 + y] = page[y] < 0 ? -1 : static_cast<int64_t>(page[y]) * A.page_size + in_page[y];
         }
-        const int64_t p0 = id0 > run.pg ? id0 : run.pg, p1 = id1 < all.pg ? id1 : all.pg;
-        for (int64_t x = p0 + tid; x < p1; x += kBuildThreads) {
-            const int i = last_not_above(S.pg, n, x);
-            A.ids[x] = page_of(A, S, c0 + i, i, x - S.pg[i]);
+        const int64_t p1 = id1 < all.pg ? id1 : all.pg;
+        for (int64_t x0 = id0 + tid * kIdRun; x0 < p1; x0 += kBuildThreads * kIdRun) {
+            if (x0 + kIdRun <= run.pg) continue;
+            const int64_t from = x0 > run.pg ? x0 : run.pg;
+            int i = last_not_above(S.pg, n, from);
+            int32_t page[kIdRun];
+#pragma unroll
+            for (int y = 0; y < kIdRun; ++y) {
+                const int64_t x = x0 + y;
+                if (x < from || x >= p1) continue;
+                while (i + 1 < n && S.pg[i + 1] <= x) ++i;
+                page[y] = page_of(A, S, c0 + i, i, x - S.pg[i]);
+            }
+#pragma unroll
+            for (int y = 0; y < kIdRun; ++y)
+                if (x0 + y >= from && x0 + y < p1) A.ids[x0 + y] = page[y];
         }
         run = all;
         if (!first && run.tok >= slot1 && run.pg >= id1) return;   // the same for every thread
@@ -183,10 +230,14 @@ __global__ __launch_bounds__(kBuildThreads) void k_build_tables(const BuildArgs 
 // ----------------------------------------------------------- appending --
 //
 // Row t of K and of V goes to slot slots[t] of the layer's planes.  The rows'
-// 16-byte pieces are numbered token by token (K's pieces, then V's); a thread
-// takes kPieces of them a workgroup apart, all loads before the first store.
+// 16-byte pieces are numbered token by token (K's pieces, then V's), one to a
+// thread.  Bound by memory: 49152 tokens of 1 KiB rows move at 5.08 TB/s read
+// and written (39.7 us); 2, 4 or 8 pieces a thread lose (42.9, 46.3, 48.3 us;
+// one decode step of 64 tokens 2.4 us against 2.7, 3.5, 5.0): more workgroups
+// hide the slot's load better than more loads per thread.  Sources are read
+// past the caches (46.5 us against 52.1 with 4 pieces); the rows are left in
+// them for the attention that follows (nontemporal stores: 48.5 us).
 constexpr int kAppendThreads = 256;
-constexpr int kPieces = 4;
 
 struct AppendArgs {
     const char* src[2];
@@ -205,6 +256,7 @@ struct AppendArgs {
     uint32_t VH;                // pieces of a head
     uint32_t vh_magic;
     float scale[2];
+    float inverse[2];           // 1 / scale, rounded
     unsigned long long* skipped;
 };
 
@@ -227,8 +279,17 @@ __device__ inline float held(float x) {
     return x > 448.0f ? 448.0f : (x < -448.0f ? -448.0f : x);
 }
 
+// x / scale, correctly rounded, from the rounded inverse: the quotient's
+// remainder is exact, and corrects it (Markstein's theorem).  3 instructions for
+// the dozen of a division, which bounded the kernel.
+__device__ inline float quotient(float x, float scale, float inverse) {
+    const float q = x * inverse;
+    const float fine = __builtin_fmaf(__builtin_fmaf(-q, scale, x), inverse, q);
+    return __builtin_fabsf(q) <= 1.0e6f ? fine : q;     // also no NaN from an infinity's remainder
+}
+
 template <int FROM>
-__device__ inline u32x4 to_pool(const Source<FROM>& s, float scale) {
+__device__ inline u32x4 to_pool(const Source<FROM>& s, float scale, float inverse) {
     if constexpr (FROM == kCopyBytes) {
         return s.x[0];
     } else {
@@ -246,7 +307,7 @@ __device__ inline u32x4 to_pool(const Source<FROM>& s, float scale) {
                 else
                     f[i] = static_cast<float>(__builtin_bit_cast(_Float16, h));
             }
-            f[i] = held(f[i] / scale);
+            f[i] = held(quotient(f[i], scale, inverse));
         }
         u32x4 r;
 #pragma unroll
@@ -261,39 +322,30 @@ __device__ inline u32x4 to_pool(const Source<FROM>& s, float scale) {
 
 template <int FROM>
 __global__ __launch_bounds__(kAppendThreads) void k_append(const AppendArgs A) {
-    const int64_t piece0 = static_cast<int64_t>(blockIdx.x) * (kAppendThreads * kPieces);
+    const int64_t piece0 = static_cast<int64_t>(blockIdx.x) * kAppendThreads;
     const int64_t row0 = piece0 / A.V;                  // rows: 2 t + (0 for K, 1 for V)
-    const uint32_t rest = static_cast<uint32_t>(piece0 - row0 * A.V);
-    Source<FROM> src[kPieces];
-    char* to[kPieces];
-    float scale[kPieces];
+    const uint32_t f = static_cast<uint32_t>(piece0 - row0 * A.V) + threadIdx.x;
+    const uint32_t rr = divide(f, A.v_magic);
+    const uint32_t x = f - rr * A.V;
+    const int64_t row = row0 + rr;
+    const int64_t t = row >> 1;
+    const int kv = static_cast<int>(row & 1);
+    if (t >= A.T) return;
+    const int64_t slot = A.slots[t];
+    Source<FROM> src;
+    const char* s = A.src[kv] + t * A.src_stride[kv] + static_cast<int64_t>(x) * (16 * Source<FROM>::N);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        const uint32_t f = rest + i * kAppendThreads + threadIdx.x;
-        const uint32_t rr = divide(f, A.v_magic);
-        const uint32_t x = f - rr * A.V;
-        const int64_t row = row0 + rr;
-        const int64_t t = row >> 1;
-        const int kv = static_cast<int>(row & 1);
-        to[i] = nullptr;
-        if (t >= A.T) continue;
-        const int64_t slot = A.slots[t];
-        const char* s = A.src[kv] + t * A.src_stride[kv] + static_cast<int64_t>(x) * (16 * Source<FROM>::N);
-#pragma unroll
-        for (int j = 0; j < Source<FROM>::N; ++j) src[i].x[j] = reinterpret_cast<const u32x4*>(s)[j];
-        scale[i] = A.scale[kv];
-        const int64_t page = A.page_shift >= 0 ? slot >> A.page_shift : slot / A.page_size;
-        if (slot < 0 || page >= A.num_pages) {
-            if (kv == 0 && x == 0 && A.skipped != nullptr) atomicAdd(A.skipped, 1ull);
-            continue;
-        }
-        const uint32_t h = divide(x, A.vh_magic);
-        to[i] = A.dst[kv] + page * A.page_stride + (slot - page * A.page_size) * A.row_stride +
-                h * A.head_stride + (x - h * A.VH) * 16;
+    for (int j = 0; j < Source<FROM>::N; ++j)
+        src.x[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(s) + j);
+    const int64_t page = A.page_shift >= 0 ? slot >> A.page_shift : slot / A.page_size;
+    if (slot < 0 || page >= A.num_pages) {
+        if (kv == 0 && x == 0 && A.skipped != nullptr) atomicAdd(A.skipped, 1ull);
+        return;
     }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-        if (to[i] != nullptr) *reinterpret_cast<u32x4*>(to[i]) = to_pool<FROM>(src[i], scale[i]);
+    const uint32_t h = divide(x, A.vh_magic);
+    char* to = A.dst[kv] + page * A.page_stride + (slot - page * A.page_size) * A.row_stride +
+               h * A.head_stride + (x - h * A.VH) * 16;
+    *reinterpret_cast<u32x4*>(to) = to_pool<FROM>(src, A.scale[kv], A.inverse[kv]);
 }
 
 }  // namespace tables
