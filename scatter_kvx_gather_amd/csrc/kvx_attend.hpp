@@ -473,30 +473,37 @@ __device__ inline void clear(Rows<C>* R) {
     for (int j = 0; j < C::NJ; ++j) R->o[j] = f32x4{0, 0, 0, 0};
 }
 
-// Scores s of 32 keys to weights in the query's type.  The weights are taken
+// Scores s of 32 U keys to weights in the query's type.  The weights are taken
 // against the row's reference maximum as it stands, and only when a lane's sum
 // of them passes kMostWeight (or is a NaN) is the maximum looked for, the
 // accumulators rescaled and the weights taken anew: looking for it every time
 // cost as many instructions as the rest.
-template <class T, class C>
+template <class T, class C, int U>
 __device__ inline float take_weights(const Rows<C>& R, const f32x4* s, float scale, u32x4* pf) {
-    float part[2] = {0.0f, 0.0f}, p[8];
+    float part[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], scale, -R.ref));
-        part[i & 1] += p[i];
+    for (int u = 0; u < U; ++u) {
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * u + (i >> 2)][i & 3], scale, -R.ref));
+            part[i & 1] += p[i];
+        }
+        pf[u] = u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]), Mma<T>::pack(p[4], p[5]),
+                      Mma<T>::pack(p[6], p[7])};
     }
-    *pf = u32x4{Mma<T>::pack(p[0], p[1]), Mma<T>::pack(p[2], p[3]), Mma<T>::pack(p[4], p[5]),
-                Mma<T>::pack(p[6], p[7])};
     return part[0] + part[1];
 }
 
 __device__ inline bool too_much(float sum) { return __any(!(sum <= kMostWeight)); }
 
-template <class T, class C>
+template <class T, class C, int U>
 __device__ inline float move_maximum(Rows<C>* R, const f32x4* s, float scale, u32x4* pf) {
-    float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * scale;
+    float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < 2 * U; ++x)
+        top = fmaxf(fmaxf(fmaxf(top, s[x][0]), s[x][1]), fmaxf(s[x][2], s[x][3]));
+    top *= scale;
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const float m = fmaxf(R->m, top);
@@ -506,7 +513,7 @@ __device__ inline float move_maximum(Rows<C>* R, const f32x4* s, float scale, u3
     R->l *= a;
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) R->o[j] *= a;
-    return take_weights<T, C>(*R, s, scale, pf);
+    return take_weights<T, C, U>(*R, s, scale, pf);
 }
 
 // In a matrix product a weight of 0 times an infinity or a NaN is a NaN, so in
@@ -777,8 +784,8 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             const bool partial = all_see < key0 + kKeys;
             if (valid != 0xffffffffu || partial) mask_scores(s, key0, limit, valid);
             u32x4 pf[1];
-            float sum = take_weights<T, C>(R, s, A.scale, pf);
-            if (too_much(sum)) sum = move_maximum<T, C>(&R, s, A.scale, pf);
+            float sum = take_weights<T, C, 1>(R, s, A.scale, pf);
+            if (too_much(sum)) sum = move_maximum<T, C, 1>(&R, s, A.scale, pf);
             R.l += sum;
             if (valid != 0xffffffffu) {
 #pragma unroll
@@ -857,13 +864,14 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
 // ---------------------------------------------------------------- wide --
 
 // A wide tile's shapes: RT row tiles of 16 per wave, KT keys staged at a time
-// in one of two buffers.
+// in one of two buffers, U steps of 32 computed together.
 template <class C>
 struct Wide {
     static constexpr int DP = C::KS * 32;
     static constexpr int RT = DP <= 128 ? 2 : 1;
     static constexpr int ROWS = kWaves * 16 * RT;
     static constexpr int KT = DP <= 128 ? 128 : 64;
+    static constexpr int U = DP <= 128 ? 2 : 1;
     static constexpr int NB = KT / kKeys;               // steps of 32 keys
     static constexpr int WPG = 128 / KT;                // waves that stage one group of 16 keys
     static constexpr int VR = 16 / WPG;                 // V rows that a wave stages
@@ -1065,38 +1073,42 @@ __device__ inline bool take_out_not_finite(char* buf, int wave) {
     return __any(mine);
 }
 
-// The order of a block of N operands, each read from shared memory and used in
-// RT products, beside the instructions that take the last step's weights:
-// operands are read AHEAD of their products (left to itself the compiler asks
-// for one and waits for it), and vector instructions stand between products.
-template <int N, int RT>
-__device__ inline void interleave() {
-    constexpr int AHEAD = N < 6 ? N : 6;
-    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);          // shared memory reads
+// Orders a block of products and the shared memory reads of their operands: N
+// groups of PRODUCTS products, the READS reads of each a group ahead of them
+// (left to itself the compiler asks for an operand and waits for it).
+template <int N, int READS, int PRODUCTS>
+__device__ inline void read_ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, RT, 0);         // products
-        if (i + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 4 * RT, 0);     // vector
-        __builtin_amdgcn_sched_group_barrier(0x400, RT, 0);         // exponentials
+        if (i + 1 < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS, 0);
     }
 }
 
-// The keys of one buffer against the wave's rows: scores of a step of 32 keys
-// while the weights of the step before are taken, then that step's product
-// with V, so that matrix and vector unit work side by side.
+// The keys of one buffer against the wave's rows, U steps of 32 keys at a time.
 template <class T, class C>
 __device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>* S, int32_t tile0,
                                  const char* buf, const uint32_t* flags) {
     using W = Wide<C>;
+    constexpr int U = W::U;
     const char* v = buf + W::KF * 1024;
-    int32_t n = (S->most - tile0 + kKeys - 1) / kKeys;          // steps that some row sees
-    n = n < W::NB ? n : W::NB;
-    if (n <= 0) return;
     const int lane = here_lane();
-    auto scores_of = [&](int b, f32x4 (&s)[W::RT][2]) {
+    const int vb = v_base<C>();
+#pragma unroll 1
+    for (int b = 0; b < W::NB; b += U) {
+        const int32_t key0 = tile0 + b * kKeys;
+        if (key0 >= S->most) break;
+        bool masked = S->all_see < key0 + U * kKeys;            // some row does not see some key
+        uint32_t valid[U];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int u = 0; u < U; ++u) {
+            valid[u] = __builtin_amdgcn_readfirstlane(flags[b + u]);
+            masked = masked || valid[u] != 0xffffffffu;
+        }
+        f32x4 s[W::RT][2 * U];
+#pragma unroll
+        for (int x = 0; x < 2 * U; ++x) {
 #pragma unroll
             for (int t = 0; t < W::RT; ++t) s[t][x] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -1107,49 +1119,31 @@ __device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>*
                 for (int t = 0; t < W::RT; ++t) s[t][x] = Mma<T>::run(f, S->q[t][ks], s[t][x]);
             }
         }
-    };
-    auto mask = [&](int b, f32x4 (&s)[W::RT][2]) {
-        const int32_t key0 = tile0 + b * kKeys;
-        const uint32_t valid = __builtin_amdgcn_readfirstlane(flags[b]);
-        if (valid != 0xffffffffu || S->all_see < key0 + kKeys) {
+        read_ahead<2 * U, C::KS, C::KS * W::RT>();
+        if (masked) {
 #pragma unroll
-            for (int t = 0; t < W::RT; ++t) mask_scores(s[t], key0, S->limit[t], valid);
+            for (int t = 0; t < W::RT; ++t)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    mask_scores(&s[t][2 * u], key0 + u * kKeys, S->limit[t], valid[u]);
         }
-    };
-    const int vb = v_base<C>();
-    auto step = [&](int b, f32x4 (&s)[W::RT][2], f32x4 (&next)[W::RT][2]) {
-        u32x4 pf[W::RT];
-        float sum[W::RT];
-        if (b + 1 < n) {
-            scores_of(b + 1, next);
-#pragma unroll
-            for (int t = 0; t < W::RT; ++t) sum[t] = take_weights<T, C>(S->R[t], s[t], A.scale, &pf[t]);
-            interleave<2 * C::KS, W::RT>();
-        } else {
-#pragma unroll
-            for (int t = 0; t < W::RT; ++t) sum[t] = take_weights<T, C>(S->R[t], s[t], A.scale, &pf[t]);
-        }
+        u32x4 pf[W::RT][U];
 #pragma unroll
         for (int t = 0; t < W::RT; ++t) {
-            if (__builtin_expect(too_much(sum[t]), 0))
-                sum[t] = move_maximum<T, C>(&S->R[t], s[t], A.scale, &pf[t]);
-            S->R[t].l += sum[t];
+            float sum = take_weights<T, C, U>(S->R[t], s[t], A.scale, pf[t]);
+            if (__builtin_expect(too_much(sum), 0))
+                sum = move_maximum<T, C, U>(&S->R[t], s[t], A.scale, pf[t]);
+            S->R[t].l += sum;
         }
 #pragma unroll
-        for (int j = 0; j < C::NJ; ++j) {
-            const u32x4 f = v_frag<C>(v, vb, b, j);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int t = 0; t < W::RT; ++t) S->R[t].o[j] = Mma<T>::run(f, pf[t], S->R[t].o[j]);
-        }
-        if (b + 1 < n) mask(b + 1, next);
-    };
-    f32x4 s[2][W::RT][2];
-    scores_of(0, s[0]);
-    mask(0, s[0]);
-#pragma unroll 1
-    for (int b = 0; b < n; b += 2) {
-        step(b, s[0], s[1]);
-        if (b + 1 < n) step(b + 1, s[1], s[0]);
+            for (int j = 0; j < C::NJ; ++j) {
+                const u32x4 f = v_frag<C>(v, vb, b + u, j);
+#pragma unroll
+                for (int t = 0; t < W::RT; ++t) S->R[t].o[j] = Mma<T>::run(f, pf[t][u], S->R[t].o[j]);
+            }
+        read_ahead<U * C::NJ / 4, 8, 4 * W::RT>();
     }
 }
 
