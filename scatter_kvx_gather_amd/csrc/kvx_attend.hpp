@@ -1086,17 +1086,17 @@ __device__ inline void read_ahead() {
     }
 }
 
-// The keys of one buffer against the wave's rows, U steps of 32 keys at a time.
+// Steps [from, to) of one buffer against the wave's rows, U steps of 32 keys at a time.
 template <class T, class C>
 __device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>* S, int32_t tile0,
-                                 const char* buf, const uint32_t* flags) {
+                                 const char* buf, const uint32_t* flags, int from, int to) {
     using W = Wide<C>;
     constexpr int U = W::U;
     const char* v = buf + W::KF * 1024;
     const int lane = here_lane();
     const int vb = v_base<C>();
 #pragma unroll 1
-    for (int b = 0; b < W::NB; b += U) {
+    for (int b = from; b < to; b += U) {
         const int32_t key0 = tile0 + b * kKeys;
         if (key0 >= S->most) break;
         bool masked = S->all_see < key0 + U * kKeys;            // some row does not see some key
@@ -1199,11 +1199,16 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
     // one tile: the next one is on its way to the other buffer meanwhile
     auto turn = [&](int32_t tile0, char* here, char* there, uint32_t* fh, uint32_t* ft) {
         const bool more = tile0 + W::KT < P.key1;
-        if (more) {
+        // half of the waves ask for the next tile before the first of their
+        // steps, half after it: the memory pipe takes the loads at one rate
+        // anyway, and the two waves of a SIMD then run their products and
+        // their exponentials at different times
+        auto stage_next = [&]() {
             next.off = page_offset(A, P.lists, P.pg0, page, stage_key<C>(tile0 + W::KT, wave), P.key1);
             page = stage_page<C>(A, P, tile0 + 2 * W::KT, wave);
             stage_load<T, C>(A, &next, kh, vhd, wave, there, ft);
-        }
+        };
+        if (more && wave < kWaves / 2) stage_next();
         // where some row of the workgroup does not see some key, values that are
         // not finite leave the buffer (see add_not_finite); once some have, the
         // piece's later ones are added whatever they are
@@ -1216,7 +1221,9 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
             for (int w = 0; w < kWaves; ++w) any |= odds[w];
             if (S.first_odd < 0 && __builtin_amdgcn_readfirstlane(any) != 0) S.first_odd = tile0;
         }
-        wide_tile<T, C>(A, P, &S, tile0, here, fh);
+        wide_tile<T, C>(A, P, &S, tile0, here, fh, 0, W::U);
+        if (more && wave >= kWaves / 2) stage_next();
+        wide_tile<T, C>(A, P, &S, tile0, here, fh, W::U, W::NB);
         if (more) stage_store<T, C>(next, wave, there);
         __syncthreads();
     };
@@ -1270,6 +1277,7 @@ struct Mine {
     int64_t w, lo, hi;
     int64_t slot0;              // the line's first slot
     int32_t seg;
+    int32_t window;             // first segment of the window in shared memory
     int64_t seg_start;
 };
 
@@ -1280,13 +1288,14 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     int64_t total[2] = {0, 0};
     int64_t start = 0, cost = 0;            // of this thread's segment in the last chunk
     bool wide = false;
+    Seg mine = {};
+    int64_t units = 0, pg0 = 0;
     for (int32_t c0 = 0; c0 < nseg; c0 += kThreads) {
         const int32_t s = c0 + static_cast<int32_t>(threadIdx.x);
         cost = 0;
         wide = false;
-        Seg mine;
-        int64_t units = 0;
         if (s < nseg) {
+            pg0 = s < A.num_groups ? A.pre.pg_off[s] : A.own.pg_off[s - A.num_groups];
             mine = segment(A, s);
             units = set_units(mine);
             cost = units * mine.sets;
@@ -1346,14 +1355,14 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     const int64_t xcd = block % 8, j = block / 8;
     M.line = j < wgs[1] / 8 ? 1 : 0;
     M.slot0 = M.line ? 0 : 2 * wgs[1];
-    const int64_t mine = M.line ? wgs[1] : wgs[0];
+    const int64_t all = M.line ? wgs[1] : wgs[0];
     const int64_t jj = M.line ? j : j - wgs[1] / 8;
-    M.w = xcd * (mine / 8) + jj;
+    M.w = xcd * (all / 8) + jj;
     M.lo = M.hi = 0;
-    if (jj >= mine / 8) return M;
+    if (jj >= all / 8) return M;
     M.n = M.line ? total[1] : total[0];
-    M.wgs = mine;
-    const Cuts cuts(M.n, mine);
+    M.wgs = all;
+    const Cuts cuts(M.n, all);
     M.lo = uniform(cuts.start(M.w));
     M.hi = uniform(cuts.start(M.w + 1));
     if (M.lo >= M.hi) return M;
@@ -1394,6 +1403,17 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     }
     M.seg = uniform(static_cast<int32_t>(L->at[0]));
     M.seg_start = uniform(L->at[1]);
+    M.window = M.seg - kWindow;
+    if (nseg <= kThreads) {                 // the window is at hand
+        const int32_t i = static_cast<int32_t>(threadIdx.x) - M.seg;
+        if (i >= 0 && i < kWindow) {
+            L->seg[i] = mine;
+            L->units[i] = units;
+            L->pg0[i] = pg0;
+        }
+        M.window = M.seg;
+        __syncthreads();
+    }
     return M;
 }
 
@@ -1425,7 +1445,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
 
     Piece P;
     int64_t pos = M.lo;                     // on the line
-    int32_t s = M.seg, first = M.seg - kWindow;
+    int32_t s = M.seg, first = M.window;
     int64_t seg_start = M.seg_start;
     while (pos < M.hi && s < nseg) {
         if (s >= first + kWindow) {

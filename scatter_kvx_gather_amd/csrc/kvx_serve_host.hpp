@@ -459,10 +459,10 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.thin_min_log2 = 6;
     a.wide_min_log2 = 8;
     a.thin_item = 64;
-    a.wide_item = 320;
+    a.wide_item = 450;
     // a compute unit's time for a wide key (its products) over that for a thin
     // key (its bytes)
-    const double wide_ns = 4.0 * s.wide_rows * s.DP / 2000.0;
+    const double wide_ns = 4.0 * s.wide_rows * s.DP / 2350.0;
     const double thin_ns = 2.0 * a.hs * g.Db / a.parts / 26.0;
     a.wide_weight = static_cast<float>(wide_ns / thin_ns);
     char* ws = static_cast<char*>(x.workspace);
