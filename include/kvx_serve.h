@@ -50,9 +50,9 @@ typedef struct kvx_batch_tables {
  * in page t / page_size of the new table.  A page past the end of free_ids,
  * or a held one outside held->page_ids, is written as -1, and a token in a page
  * with a negative id gets slot -1: kvx's calls skip such rows.  Negative
- * lengths count as 0, and a request's total stops at 2^31 - 1 tokens.  The
- * outputs must not overlap the inputs (a held table is read while the new one
- * is written).  One launch. */
+ * lengths count as 0, and a request's total stops at 2^31 - 1 tokens.  At most
+ * 2^24 requests (KVX_E_RANGE).  The outputs must not overlap the inputs (a held
+ * table is read while the new one is written).  One launch. */
 kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* have_len,
                             const int32_t* add_len, const kvx_table* held,
                             const int32_t* free_ids, int64_t num_free,
@@ -66,11 +66,11 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
  * bit by bit where dtype is the pool's; a KVX_FP8 pool also takes f16, bf16 and
  * f32 rows, which it holds as e4m3 (OCP, nearest even) of x / k_scale and
  * x / v_scale, values past +-448 held at +-448 and NaN kept (other pairs:
- * KVX_E_UNSUPPORTED).  Scales are finite and positive, and 1 is required where
- * nothing is rounded.  A slot outside the pool is skipped and counted once in
- * *skipped (if not NULL).  Distinct tokens have distinct slots (unchecked;
- * KVX_VALIDATE=1 returns KVX_E_DUPLICATE).  The layout has num_kv = 2.  One
- * launch. */
+ * KVX_E_UNSUPPORTED).  Scales are finite, positive and from 2^-64 to 2^64
+ * (KVX_E_RANGE), and 1 is required where nothing is rounded.  A slot outside the
+ * pool is skipped and counted once in *skipped (if not NULL).  Distinct tokens
+ * have distinct slots (unchecked; KVX_VALIDATE=1 returns KVX_E_DUPLICATE).  The
+ * layout has num_kv = 2.  One launch. */
 typedef struct kvx_rows {
     const void* k;
     const void* v;
@@ -141,7 +141,8 @@ typedef struct kvx_attention {
  * The contracts of tok_off and grp_off are unchecked (KVX_VALIDATE=1 checks
  * them, and that lengths are not negative: KVX_E_SHAPE); with broken ones the
  * kernels stay inside the pool, the workspace, q, out and lse, and the result
- * is unspecified.  Negative lengths count as 0.
+ * is unspecified.  Negative lengths count as 0, and those past 2^30 as 2^30.  At
+ * most 2^24 requests and groups and 2^23 - 1 query tokens (KVX_E_RANGE).
  *
  * The workspace holds partial sums during the call and nothing between calls.
  * Calls that may run at the same time, graph replays among them, need a

@@ -63,6 +63,7 @@ constexpr int kWaves = 8;               // waves of an attention workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kKeys = 32;               // keys of one step of a wave
 constexpr int kThinRows = 16;
+constexpr int32_t kMaxKeys = 1 << 30;    // of a context or a prefix: step indices stay in 32 bits
 constexpr int kJoinWaves = 8;
 constexpr int kJoinParts = 4;
 
@@ -200,7 +201,7 @@ __device__ inline Seg segment(const Args& A, int32_t s) {
     } else {
         keys = A.ctx[r0];
     }
-    g.keys = keys > 0 ? keys : 0;
+    g.keys = clamp_to(keys, 0, kMaxKeys);
     g.tok0 = clamp_to(A.tok_off[r0], 0, A.T);
     g.ntok = clamp_to(A.tok_off[r1], g.tok0, A.T) - g.tok0;
     g.causal = !pre && A.causal != 0;

@@ -15,12 +15,26 @@ int32_t shift_of(int32_t page_size) {
     return (page_size & (page_size - 1)) == 0 ? __builtin_ctz(static_cast<uint32_t>(page_size)) : -1;
 }
 
+constexpr int32_t kMaxReqs = 1 << 24;          // requests (and groups) of a batch
+constexpr int64_t kMaxQueries = 1 << 23;       // query tokens of an attention call, exclusive
+
 bool positive(float x) { return std::isfinite(x) && x > 0.0f; }
+
+// The debug checks copy tables to host vectors: a failed allocation is a
+// status, and no exception passes the C entries.
+template <class F>
+kvx_status no_throw(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return KVX_E_RANGE;
+    }
+}
 
 template <class Args>
 kvx_status launch_one(const void* fn, int64_t grid, int threads, Args& a, hipStream_t stream) {
     if (grid <= 0) return KVX_OK;
-    if (grid > INT32_MAX) return KVX_E_RANGE;
+    if (grid > UINT32_MAX / threads) return KVX_E_RANGE;     // a launch's threads are counted in 32 bits
     void* params[] = {&a};
     return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(grid)), dim3(threads), params, 0, stream) ==
                    hipSuccess
@@ -36,6 +50,7 @@ kvx_status check_build(int32_t num_reqs, int32_t page_size, const int32_t* have,
     if (o == nullptr) return KVX_E_NULL;
     if (num_reqs < 0 || page_size < 1 || num_free < 0 || o->cap_ids < 0 || o->cap_tokens < 0)
         return KVX_E_SHAPE;
+    if (num_reqs > kMaxReqs) return KVX_E_RANGE;
     if (num_free > 0 && free_ids == nullptr) return KVX_E_NULL;
     if (o->tok_off == nullptr || o->pg_off == nullptr) return KVX_E_NULL;
     if (num_reqs > 0 && (add == nullptr || o->ctx_len == nullptr)) return KVX_E_NULL;
@@ -116,6 +131,22 @@ kvx_status check_layer(const kvx_layout* layout, int32_t layer, const kvx_pool* 
     return KVX_OK;
 }
 
+// KVX_VALIDATE=1: no slot of the pool is written twice.
+kvx_status validate_slots(const int64_t* slots, int64_t n, const kvx_pool* pool, hipStream_t stream) {
+    if (hipStreamSynchronize(stream) != hipSuccess) return KVX_E_HIP;
+    std::vector<int64_t> s;
+    KVX_TRY(to_host(slots, n, &s));
+    s.erase(std::remove_if(s.begin(), s.end(),
+                           [&](int64_t x) { return x < 0 || x / pool->page_size >= pool->num_pages; }),
+            s.end());
+    std::sort(s.begin(), s.end());
+    const auto twice = std::adjacent_find(s.begin(), s.end());
+    if (twice == s.end()) return KVX_OK;
+    std::fprintf(stderr, "kvx: KVX_VALIDATE: append: slot %lld twice; nothing enqueued\n",
+                 static_cast<long long>(*twice));
+    return KVX_E_DUPLICATE;
+}
+
 // ------------------------------------------------------------ attention --
 
 namespace at = kvx::attend;
@@ -142,8 +173,7 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     if (g.Db % 16 != 0) return KVX_E_ALIGN;
     if (num_reqs < 0 || num_groups < 0 || tokens < 0 || q_heads < 1 || q_heads % g.H != 0)
         return KVX_E_SHAPE;
-    if (q_heads / g.H > 128 || tokens >= (int64_t(1) << 31) ||
-        static_cast<int64_t>(num_reqs) + num_groups > INT32_MAX)
+    if (q_heads / g.H > 128 || tokens >= kMaxQueries || num_reqs > kMaxReqs || num_groups > kMaxReqs)
         return KVX_E_RANGE;
     const int32_t D = layout->head_dim;
     s->DP = D <= 64 ? 64 : (D <= 128 ? 128 : 256);
@@ -206,14 +236,14 @@ kvx_status validate_attend(const kvx_reqs* reqs, const int32_t* ctx, const kvx_p
     kvx_status s = check_tok_off(&hr);
     KVX_TRY(to_host(ctx, reqs->num_reqs, &len));
     for (int32_t x : len)
-        if (x < 0) s = KVX_E_SHAPE;
+        if (x < 0 || x > at::kMaxKeys) s = KVX_E_SHAPE;
     if (prefix != nullptr && prefix->num_groups > 0) {
         KVX_TRY(to_host(prefix->grp_off, static_cast<int64_t>(prefix->num_groups) + 1, &off));
         const kvx_reqs hg{prefix->num_groups, reqs->num_reqs, off.data()};
         if (s == KVX_OK) s = check_tok_off(&hg);
         KVX_TRY(to_host(prefix->len, prefix->num_groups, &len));
         for (int32_t x : len)
-            if (x < 0) s = KVX_E_SHAPE;
+            if (x < 0 || x > at::kMaxKeys) s = KVX_E_SHAPE;
     }
     if (s != KVX_OK)
         std::fprintf(stderr, "kvx: KVX_VALIDATE: attend: %s; nothing enqueued\n", kvx_status_str(s));
@@ -231,7 +261,9 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
     namespace tb = kvx::tables;
     KVX_TRY(check_build(num_reqs, page_size, have_len, add_len, held, free_ids, num_free, out));
     if (validate_enabled())
-        KVX_TRY(validate_build(num_reqs, page_size, have_len, add_len, held, out, stream));
+        KVX_TRY(no_throw([&] {
+            return validate_build(num_reqs, page_size, have_len, add_len, held, out, stream);
+        }));
     tb::BuildArgs a;
     std::memset(&a, 0, sizeof(a));
     a.have = num_reqs > 0 ? have_len : nullptr;
@@ -286,6 +318,10 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     const bool copies = rows->dtype == layout->dtype;
     if (!copies && layout->dtype != KVX_FP8) return KVX_E_UNSUPPORTED;
     if (!positive(rows->k_scale) || !positive(rows->v_scale)) return KVX_E_SHAPE;
+    // inside these the kernel's quotients by a rounded inverse are exact: no
+    // remainder of a value that e4m3 holds underflows
+    auto far = [](float x) { return x < 0x1p-64f || x > 0x1p64f; };
+    if (far(rows->k_scale) || far(rows->v_scale)) return KVX_E_RANGE;
     if (copies && (rows->k_scale != 1.0f || rows->v_scale != 1.0f)) return KVX_E_UNSUPPORTED;
     if (rows->num_tokens == 0) return KVX_OK;
     if (rows->k == nullptr || rows->v == nullptr || slots == nullptr) return KVX_E_NULL;
@@ -297,21 +333,8 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     int64_t span = 0;
     if (!mul_ok(rows->num_tokens, std::max(rows->k_stride, rows->v_stride), &span))
         return KVX_E_RANGE;
-    if (validate_enabled()) {
-        if (hipStreamSynchronize(stream) != hipSuccess) return KVX_E_HIP;
-        std::vector<int64_t> s;
-        KVX_TRY(to_host(slots, rows->num_tokens, &s));
-        s.erase(std::remove_if(s.begin(), s.end(),
-                               [&](int64_t x) { return x < 0 || x / pool->page_size >= pool->num_pages; }),
-                s.end());
-        std::sort(s.begin(), s.end());
-        const auto twice = std::adjacent_find(s.begin(), s.end());
-        if (twice != s.end()) {
-            std::fprintf(stderr, "kvx: KVX_VALIDATE: append: slot %lld twice; nothing enqueued\n",
-                         static_cast<long long>(*twice));
-            return KVX_E_DUPLICATE;
-        }
-    }
+    if (validate_enabled())
+        KVX_TRY(no_throw([&] { return validate_slots(slots, rows->num_tokens, pool, stream); }));
     tb::AppendArgs a;
     std::memset(&a, 0, sizeof(a));
     a.src[0] = static_cast<const char*>(rows->k);
@@ -408,7 +431,8 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
         return KVX_E_ALIGN;
     if (x.workspace_bytes < s.bytes) return KVX_E_SHAPE;
     if (x.q == x.out) return KVX_E_OVERLAP;
-    if (validate_enabled()) KVX_TRY(validate_attend(reqs, ctx_len, prefix, stream));
+    if (validate_enabled())
+        KVX_TRY(no_throw([&] { return validate_attend(reqs, ctx_len, prefix, stream); }));
 
     at::Args a;
     std::memset(&a, 0, sizeof(a));

@@ -5,6 +5,7 @@ validation compares and never reads."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -71,6 +72,8 @@ def test_build_tables_refusals():
     assert build(held=(A, A, -1)) == E_SHAPE
     assert build(cap_tokens=1 << 62) == E_RANGE
     assert build(cap_ids=1 << 62) == E_RANGE
+    assert build(n=(1 << 24) + 1) == E_RANGE
+    assert build(cap_tokens=1 << 36) == E_RANGE
 
 
 # ----------------------------------------------------------------- append --
@@ -106,6 +109,9 @@ def test_append_refusals():
         assert append(**f8, k_scale=bad) == E_SHAPE
         assert append(**f8, v_scale=bad) == E_SHAPE
     assert append(**f8, dtype=FP8, v_scale=0.5) == E_UNSUPPORTED
+    for bad in (1e-38, 2.0 ** -65, 2.0 ** 65, 1e38):
+        assert append(**f8, k_scale=bad) == E_RANGE
+        assert append(**f8, v_scale=bad) == E_RANGE
     for f in ("k", "v"):
         assert append(**{f: None}) == E_NULL
         assert append(**{f: A + 8}) == E_ALIGN
@@ -113,6 +119,7 @@ def test_append_refusals():
         assert append(**{f + "_stride": 2056}) == E_ALIGN
     assert append(slots=None) == E_NULL
     assert append(k_stride=1 << 62, num_tokens=1 << 20) == E_RANGE
+    assert append(num_tokens=1 << 27) == E_RANGE                # more threads than a launch counts
     assert append(p=pool(stride=1024)) == E_SHAPE
     assert append(p=pool(base=A + 8)) == E_ALIGN
     assert append(p=pool(base=0)) == E_NULL
@@ -152,6 +159,8 @@ def test_attend_refusals():
     assert attend(reqs=(0, 4, A)) == E_SHAPE
     assert attend(reqs=(2, 4, 0)) == E_NULL
     assert attend(reqs=(2, 1 << 31, A)) == E_RANGE
+    assert attend(reqs=(2, 1 << 23, A)) == E_RANGE
+    assert attend(reqs=((1 << 24) + 1, 4, A)) == E_RANGE
     assert attend(layer=2) == E_SHAPE
     assert attend(bl=-1) == E_SHAPE
     assert attend(lay=layout(kv=1), p=pool(2)) == E_UNSUPPORTED
@@ -207,7 +216,9 @@ def test_attend_workspace():
     assert workspace(lay, 1, 0, -1, 8) == -E_SHAPE
     assert workspace(lay, 1, 0, 1, 12) == -E_SHAPE
     assert workspace(lay, 1, 0, 1, 8 * 129) == -E_RANGE
-    assert workspace(lay, 1, 0, 1 << 31, 8) == -E_RANGE
+    assert workspace(lay, 1, 0, 1 << 23, 8) == -E_RANGE
+    assert workspace(lay, (1 << 24) + 1, 0, 1, 8) == -E_RANGE
+    assert workspace(lay, 1, (1 << 24) + 1, 1, 8) == -E_RANGE
     # a smaller batch never needs more
     sizes = [0, 1, 3, 64, 1000]
     for hq in (8, 32, 64):
@@ -285,3 +296,14 @@ def test_reference_attention():
     exp = (torch.softmax(s, -1) @ vv).transpose(0, 1)
     assert np.allclose(out, exp.numpy(), rtol=1e-12)
     assert np.allclose(lse, torch.logsumexp(s, -1).T.numpy(), rtol=1e-12)
+
+
+def test_header_compiles_as_c99(tmp_path):
+    src = tmp_path / "t.c"
+    src.write_text('#define __HIP_PLATFORM_AMD__ 1\n#include "kvx_serve.h"\n'
+                   "int main(void) { kvx_rows r; kvx_attention a; kvx_prefix p; kvx_batch_tables t;\n"
+                   "(void)r; (void)a; (void)p; (void)t;\n"
+                   "return kvx_attend_workspace(0, 0, 0, 0, 1, 0) == KVX_OK; }\n")
+    inc = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-fsyntax-only", "-I", inc,
+                    "-I", os.path.join(ROOT, "include"), str(src)], check=True)
