@@ -28,7 +28,8 @@ extern "C" {
 #endif
 
 /* Outputs of kvx_build_tables, all DEVICE.  Entries past the counts that the
- * batch needs keep their prior contents. */
+ * batch needs keep their prior contents (a replayed step whose batches shrink
+ * fills slots with -1 first, and kvx_append skips the rows behind the last). */
 typedef struct kvx_batch_tables {
     int32_t* ctx_len;       /* [num_reqs] have + add */
     int64_t* tok_off;       /* [num_reqs + 1] offsets of the new tokens (kvx_reqs) */
@@ -129,7 +130,10 @@ typedef struct kvx_attention {
  * id is out of range are not seen, whatever memory holds, and are counted in
  * *skipped (if not NULL): once per request with query tokens for a context,
  * once per group with query tokens for a prefix.  Values outside what a query
- * sees never reach its output, infinities and NaN included.  A sum over more
+ * sees never reach its output, infinities and NaN included.  tok_off[num_reqs]
+ * may be less than total_tokens here: rows of q from there on are not read, and
+ * those of out and lse keep their contents, so that one captured call serves
+ * batches of up to total_tokens.  A sum over more
  * keys than one workgroup takes is joined in an order that depends on the
  * lengths alone, so results repeat bit for bit.
  *

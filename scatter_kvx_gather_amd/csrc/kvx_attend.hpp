@@ -10,8 +10,8 @@
 // so a prefix is computed once for all rows of its group, a long axis is cut
 // anywhere, and out = o / l, lse = m + ln l at the end.  m, l and o are 32
 // bits throughout; weights are rounded to the query's type for the second
-// product (relative 2^-9 for bf16, 2^-12 for f16, averaged over the keys),
-// while l sums them unrounded.
+// product (relative 2^-8 at most for bf16, 2^-11 for f16, averaged over the
+// keys), while l sums them unrounded.
 //
 // Work.  A segment is a group's prefix or a request's own context; an item is
 // (segment, head set, tile of query rows), and its length is the number of
@@ -67,9 +67,15 @@ constexpr int32_t kMaxKeys = 1 << 30;    // of a context or a prefix: step indic
 constexpr int kJoinWaves = 8;
 constexpr int kJoinParts = 4;
 
-// A row's reference maximum may lag the true one while a lane's weights of one
-// step sum to no more than this: they stay exact in every type here.
-constexpr float kMostWeight = 256.0f;
+// Weights are taken against a reference, which is a row's maximum less kRoom
+// when it moves and may lag it while a lane's weights of one step sum to no
+// more than kMostWeight.  f16's weights start at 2^8, or those below 2^-14 of
+// the largest would be subnormal and, where many are alike, rounded to one
+// side together; so they have eight bits more, and stay below f16's largest.
+template <class T>
+constexpr float kRoom = std::is_same_v<T, _Float16> ? 8.0f : 0.0f;
+template <class T>
+constexpr float kMostWeight = std::is_same_v<T, _Float16> ? 32768.0f : 256.0f;
 // The reference of a row that has seen no key: any score's weight against it
 // is infinite, and -inf's is 0.
 constexpr float kNoKey = -3.0e38f;
@@ -496,7 +502,10 @@ __device__ inline float take_weights(const Rows<C>& R, const f32x4* s, float sca
     return part[0] + part[1];
 }
 
-__device__ inline bool too_much(float sum) { return __any(!(sum <= kMostWeight)); }
+template <class T>
+__device__ inline bool too_much(float sum) {
+    return __any(!(sum <= kMostWeight<T>));
+}
 
 template <class T, class C, int U>
 __device__ inline float move_maximum(Rows<C>* R, const f32x4* s, float scale, u32x4* pf) {
@@ -507,7 +516,7 @@ __device__ inline float move_maximum(Rows<C>* R, const f32x4* s, float scale, u3
     top *= scale;
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float m = fmaxf(R->m, top);
+    const float m = fmaxf(R->m, top - kRoom<T>);
     const float a = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(R->m - m);
     R->m = m;
     R->ref = m == -INFINITY ? kNoKey : m;
@@ -786,7 +795,7 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             if (valid != 0xffffffffu || partial) mask_scores(s, key0, limit, valid);
             u32x4 pf[1];
             float sum = take_weights<T, C, 1>(R, s, A.scale, pf);
-            if (too_much(sum)) sum = move_maximum<T, C, 1>(&R, s, A.scale, pf);
+            if (too_much<T>(sum)) sum = move_maximum<T, C, 1>(&R, s, A.scale, pf);
             R.l += sum;
             if (valid != 0xffffffffu) {
 #pragma unroll
@@ -1132,7 +1141,7 @@ __device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>*
 #pragma unroll
         for (int t = 0; t < W::RT; ++t) {
             float sum = take_weights<T, C, U>(S->R[t], s[t], A.scale, pf[t]);
-            if (__builtin_expect(too_much(sum), 0))
+            if (__builtin_expect(too_much<T>(sum), 0))
                 sum = move_maximum<T, C, U>(&S->R[t], s[t], A.scale, pf[t]);
             S->R[t].l += sum;
         }
@@ -1683,6 +1692,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
     if (uniform(static_cast<int32_t>(token < part[0].g.tok0 || token >= part[0].g.tok0 + part[0].g.ntok))) {
         r = uniform(find_list(A.tok_off, A.num_reqs, token));
         part[0] = A.placed[A.num_groups + r];
+        const int32_t end = part[0].g.tok0 + part[0].g.ntok;
+        if (uniform(static_cast<int32_t>(token >= end)) != 0) return;      // behind the last request
     }
     if (A.num_groups > 1) part[1] = A.placed[uniform(find_list(A.grp_off, A.num_groups, r))];
 #pragma unroll

@@ -232,7 +232,7 @@ kvx_status validate_attend(const kvx_reqs* reqs, const int32_t* ctx, const kvx_p
     std::vector<int64_t> off;
     std::vector<int32_t> len;
     KVX_TRY(to_host(reqs->tok_off, static_cast<int64_t>(reqs->num_reqs) + 1, &off));
-    const kvx_reqs hr{reqs->num_reqs, reqs->total_tokens, off.data()};
+    const kvx_reqs hr{reqs->num_reqs, std::min(off.back(), reqs->total_tokens), off.data()};
     kvx_status s = check_tok_off(&hr);
     KVX_TRY(to_host(ctx, reqs->num_reqs, &len));
     for (int32_t x : len)

@@ -124,10 +124,10 @@ def bounds(dtype, dim, out, lse, mass, size, seen, vmax):
     exponential; l and o sum `seen` of them (2^-24 each), and out divides the
     two, so the relative error of a weight counts twice.  For the second
     product a weight is rounded to the type (half a step of it; in f16 at
-    least 2^-25, where it is subnormal), and out once more at the end."""
+    least 2^-25, where it is subnormal, and the largest weights are at least 2^8), and out once more at the end."""
     u = HALF[dtype]
     e = (dim + 8) * 2.0 ** -24 * size + 2.0 ** -22 + (seen[:, None] + 64) * 2.0 ** -24
-    tiny = seen * 2.0 ** -25 * vmax if dtype == "f16" else seen * 2.0 ** -126 * vmax
+    tiny = seen * 2.0 ** -33 * vmax if dtype == "f16" else seen * 2.0 ** -126 * vmax
     # a result below the type's normal range is off by half its smallest step
     floor = 2.0 ** -25 if dtype == "f16" else 2.0 ** -126
     tol = u * np.abs(out) * 1.01 + (u + 2 * e[..., None]) * mass + tiny[:, None, None] + floor

@@ -200,6 +200,28 @@ def test_many_requests(n):
         members=[0, *cuts, n], prefix=[10, 0, 33, 70])
 
 
+@pytest.mark.parametrize("new", [1, 80])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_small_weights(dtype, new):
+    """One key of weight 1 and value 0 before 60000 of weight 2^-22.6 and value
+    1: in f16 such weights would be subnormal, and all rounded alike."""
+    say("small weights", dtype, new)
+    n = 60000
+    c = Case(19, new=[new], ctx=[n], H=1, G=1, D=64, dtype=dtype, page=64)
+    rows = np.array(c.b.rows(c.b.pg_off[0], c.b.ids, n))
+    k, v = (torch.zeros(n, 1, 64) for _ in range(2))
+    k[:, 0, 0] = 0.335
+    k[0, 0, 0] = 16.0
+    v[1:] = 1.0
+    c.kv[0][rows], c.kv[1][rows] = k.to(c.kv[0].dtype), v.to(c.kv[1].dtype)
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    c.upload()
+    out, lse = c.run(scale=1.0, causal=False)
+    torch.cuda.synchronize()
+    c.check(out, lse, 1.0, False)
+
+
 def test_strided_queries_and_outputs():
     """q as a slice of a fused projection, out with padded tokens: the bytes
     between are left alone."""
@@ -213,6 +235,27 @@ def test_strided_queries_and_outputs():
     _, lse = c.run(q=wide[:, 2:2 + Hq], out=out)
     c.check(out, lse)
     assert (room[T:] == 7).all() and (room[:, 0] == 7).all() and (room[:, -1] == 7).all()
+
+
+@pytest.mark.parametrize("new", [[1, 1, 0, 1], [3, 0, 90, 2], [1, 2, 3, 0], [0, 0, 0, 0]])
+@pytest.mark.parametrize("prefix", [False, True])
+def test_rows_behind_the_last_request(new, prefix):
+    """total_tokens beyond tok_off[num_reqs]: those rows stay as they were, and
+    NaN in their queries harms nothing."""
+    say("rows behind", new, prefix)
+    extra = dict(members=[0, 1, 4], prefix=[40, 33]) if prefix else {}
+    c = Case(18, new=new, ctx=[50, 9, 120, 3], H=2, G=4, D=64, **extra)
+    T, room = sum(new), sum(new) + 7
+    q = torch.full((room, 8, 64), float("nan"), dtype=c.qd.dtype, device=DEV)
+    q[:T] = c.qd
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((room, 8), 7.0, device=DEV)
+    c.reqs = kvx.Requests(c.tok_off, room)
+    c.run(q=q, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out[T:] == 7).all() and (lse[T:] == 7).all()
+    if T:
+        c.check(out[:T], lse[:T])
 
 
 @pytest.mark.parametrize("new", [1, 64])

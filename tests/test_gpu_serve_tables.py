@@ -329,3 +329,61 @@ def test_serving_step(pool, layout, page, captured):
         remember(range(N), [1] * N, data)
         check(outs, range(N), [1] * N, data, True)
         S.free = S.free[T2[1].totals[2].item():]
+
+
+def test_captured_step_of_batches_that_shrink():
+    """One capture of tables, append and attend with room for 40 tokens of 4
+    requests, replayed with fewer: rows and slots behind the batch are left."""
+    say("padded step")
+    rng = np.random.default_rng(31)
+    H, G, D, page, room, N = 2, 2, 64, 16, 40, 4
+    lay = kvx.Layout(1, 2, H, D, "bf16")
+    store = torch.zeros(2, 64, page, H, D, dtype=torch.bfloat16, device=DEV)
+    pool = kvx.Pool(store, 64, page, slot_stride=H * D * 2)
+    t = kvx.BatchTables(N, room, 16)
+    free = ints(rng.permutation(64), torch.int32)
+    add = ints([1] * N, torch.int32)
+    q, out = (torch.zeros(room, H * G, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k, v = (torch.zeros(room, H, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    skipped = torch.zeros(1, dtype=torch.int64, device=DEV)
+    reqs = t.requests(room)
+    ws = torch.empty(kvx.attend_workspace(lay, reqs, H * G), dtype=torch.uint8, device=DEV)
+
+    def step():
+        t.slots.fill_(-1)
+        kvx.build_tables(t, page, add, free)
+        kvx.append(lay, 0, pool, t.slots, k, v, skipped=skipped)
+        kvx.attend(lay, 0, pool, reqs, t.ctx_len, t.table, q, out, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new in ([20, 1, 3, 16], [0, 5, 0, 1], [0, 0, 0, 0], [17, 17, 2, 0]):
+        T = sum(new)
+        host = [torch.randn(room, h, D).to(torch.bfloat16) for h in (H * G, H, H)]
+        for x, y in zip((q, k, v), host):
+            x.copy_(y)
+        add.copy_(ints(new, torch.int32))
+        out.fill_(7)
+        skipped.zero_()
+        before = store.clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert skipped.item() == room - T and (out[T:] == 7).all()
+        rows = t.slots[:T].cpu().numpy()
+        left = np.setdiff1d(np.arange(64 * page), rows)
+        now = store.view(2, 64 * page, H, D)
+        assert torch.equal(now[:, left], before.view(now.shape)[:, left])
+        off = np.concatenate([[0], np.cumsum(new)])
+        for r, n in enumerate(new):
+            if n == 0:
+                continue
+            mine = slice(off[r], off[r + 1])
+            b = ref.Batch(n, 1, [n], [n], np.array([0, 1]), np.array([0]))
+            a = [x[mine].double().numpy() for x in host]
+            eo, el, mass, size, seen = ref.attend(b, *a, D ** -0.5)
+            tol, _ = ref.bounds("bf16", D, eo, el, mass, size, seen, np.abs(a[2]).max())
+            assert (np.abs(out[mine].double().cpu().numpy() - eo) <= tol).all()
