@@ -28,19 +28,35 @@
 // Thin tiles (16 query rows a wave) are for segments with few rows, where the
 // KV rows' bytes are the bound: the waves of a workgroup take the heads of
 // one key range, so a pool row is read whole by one workgroup, and K and V go
-// from memory to the matrix instructions through registers alone.  Wide tiles
-// (128 or 256 rows a workgroup) are for segments with many rows, where the
-// matrix units are the bound: the workgroup stages fragments of K and V in
-// shared memory, each read by all of its waves.
+// from memory to the matrix instructions through registers alone, a step of 32
+// keys ahead, page ids two.  256 requests behind 256 to 2048 tokens, 8 kv heads
+// of 128 dims: 255 us, 4.9 TB/s, what a large copy reaches on this card.
+//
+// Wide tiles (128 or 256 rows a workgroup) are for segments with many rows,
+// where the matrix units and what feeds them are the bound: 64 or 128 keys at a
+// time go from memory to one of two buffers in shared memory without passing
+// registers, and each wave reads them for its 32 rows (16 above 128 dims).
+// 8 prompts of 2048 tokens, 32 heads over 8 of 128 dims: 397 us, 693 TFLOP/s;
+// with 64 dims 2 prompts of 8192 740 TFLOP/s, with 256 2 of 4096 615.  Of a
+// tile's 10 thousand cycles the products' own are 4.1; the exponentials and
+// their packing come next, then loads issued and waits at the end of a tile.
+// Two steps of 32 keys together, their products in the shadow of each other's
+// softmax, and half of the waves staging after their first step beat one step
+// (664 -> 442 us with the split items' join, 410 -> 397).
+//
+// The second launch joins what is split: 3 to 10 us, as long as a chain of its
+// launch and three dependent loads.
 //
 // Fragments.  S^T = K Q^T by 16x16x32 products: K rows are loaded as the A
 // operand holds them (lane a + 16 g: key a, 8 dims at 8 g).  The result has
 // query row a in lanes a + 16 g, keys 4 g + r of two 16-key tiles, which is
 // how the B operand of O^T = V^T P^T holds them when its 8 k-slots of lane
 // group g stand for keys {4g..4g+3, 16+4g..16+4g+3}: the weights never leave
-// their registers.  V is loaded row by row (lane a: dims 8a .. 8a+7 of the
-// group's 8 keys) and its 8 x 8 blocks are transposed in registers with byte
-// permutes; row a of the j-th product is then dim 8 a + j.
+// their registers.  V's operand is a transposition of its rows.  Thin tiles
+// load V row by row (lane a: dims 8a .. 8a+7 of the group's 8 keys) and
+// transpose 8 x 8 blocks in registers with byte permutes; row a of the j-th
+// product is then dim 8 a + j.  Wide tiles read rows from shared memory with
+// transposing reads; row a of the j-th product is dim 16 j + a.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -90,11 +106,11 @@ __device__ inline int here_lane() {
     return lane;
 }
 
-// The item that begins in a workgroup's piece and ends in a later one's, if there is one.
+// The item that reaches from a workgroup's piece into a later one's, if there is one.
 struct Split {
     int64_t item;                       // its first unit
     int32_t last;                       // the piece that it ends in; -1: no such item
-    int32_t w, slot0;                   // this piece, the line's first slot
+    int32_t w, slot0;                   // the piece that it begins in, the line's first slot
     int32_t wide;
     int32_t tok0, ntok;                 // of its segment
     int32_t set, tile;
@@ -157,7 +173,7 @@ struct Args {
     // workspace
     struct Placed* placed;              // [num_groups + num_reqs]: segments on their lines
     int64_t* plan;                      // [6]: Cuts of the thin and the wide line, workgroups of each
-    struct Split* splits;               // [grid]
+    struct Split* splits;               // [grid], by slot / 2
     float* slot_o;                      // [2 * grid][slot rows][D]
     float* slot_ml;                     // [2 * grid][slot rows][2]
     float* row_o;                       // [2][T][Hq][D]: own, prefix (only with prefixes)
@@ -671,18 +687,6 @@ __device__ inline void load_q(const Args& A, u32x4 (&q)[C::KS], int32_t token, i
     }
 }
 
-// One step of 32 keys against 16 query rows, K as fragments from `kf(kt, ks)`
-// and V as operands from `vf(j)`.
-template <class T, class C, class KF>
-__device__ inline void scores(const u32x4 (&q)[C::KS], f32x4 (&s)[2], KF kf) {
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-        s[kt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int ks = 0; ks < C::KS; ++ks) s[kt] = Mma<T>::run(kf(kt, ks), q[ks], s[kt]);
-    }
-}
-
 // Keys this lane's row does not see get -inf: key index key0 + ..., seen below
 // `limit` and where `valid` has its bit.
 __device__ inline void mask_scores(f32x4* s, int32_t key0, int32_t limit, uint32_t valid) {
@@ -729,7 +733,8 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
         const int32_t step = kKeys * A.kp;
 
         // K and V of a step as loaded.  Up to 128 dims both are loaded a step
-        // ahead; above, K and then V of the present step, one after the other.
+        // ahead; above, K and then V of the present step, or they would not
+        // fit the registers (64 contexts of 2048 keys 64 us, a step ahead 72).
         constexpr bool AHEAD = C::NC == 1;
         KTile<C> kt[2];
         Words<C::VW> vr[8][C::NC];
@@ -786,7 +791,13 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
             const bool more = key0 + step < P.key1;
             if (!AHEAD) load_keys(off);
             f32x4 s[2];
-            scores<T, C>(q, s, [&](int x, int ks) { return k_frag<T, C>(kt[x], ks, g, A.D); });
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                s[x] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int ks = 0; ks < C::KS; ++ks)
+                    s[x] = Mma<T>::run(k_frag<T, C>(kt[x], ks, g, A.D), q[ks], s[x]);
+            }
             if (!AHEAD) load_values(off);
             const int64_t off_next = offset_of(key0 + step, page);
             page = page_of(key0 + 2 * step);
@@ -960,7 +971,7 @@ template <class T, class C>
 __device__ inline void stage_load(const Args& A, Stage<T, C>* S, const char* kh, const char* vhd,
                                   int wave, char* buf, uint32_t* flags) {
     using W = Wide<C>;
-    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
+    const int lane = here_lane(), g = lane >> 4;
     const int grp = wave / W::WPG, sub = wave % W::WPG;
     const uint64_t seen = __ballot(S->off >= 0);
     const bool whole = seen == ~0ull && A.D == W::DP;       // every lane loads
@@ -1098,7 +1109,7 @@ __device__ inline void read_ahead() {
 
 // Steps [from, to) of one buffer against the wave's rows, U steps of 32 keys at a time.
 template <class T, class C>
-__device__ inline void wide_tile(const Args& A, const Piece& P, WideState<T, C>* S, int32_t tile0,
+__device__ inline void wide_tile(const Args& A, WideState<T, C>* S, int32_t tile0,
                                  const char* buf, const uint32_t* flags, int from, int to) {
     using W = Wide<C>;
     constexpr int U = W::U;
@@ -1231,9 +1242,9 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
             for (int w = 0; w < kWaves; ++w) any |= odds[w];
             if (S.first_odd < 0 && __builtin_amdgcn_readfirstlane(any) != 0) S.first_odd = tile0;
         }
-        wide_tile<T, C>(A, P, &S, tile0, here, fh, 0, W::U);
+        wide_tile<T, C>(A, &S, tile0, here, fh, 0, W::U);
         if (more && wave >= kWaves / 2) stage_next();
-        wide_tile<T, C>(A, P, &S, tile0, here, fh, W::U, W::NB);
+        wide_tile<T, C>(A, &S, tile0, here, fh, W::U, W::NB);
         if (more) stage_store<T, C>(next, wave, there);
         __syncthreads();
     };
@@ -1309,9 +1320,10 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
             mine = segment(A, s);
             units = set_units(mine);
             cost = units * mine.sets;
-            wide = LINES == 3 && mine.wide;
+            wide = (LINES & 2) && mine.wide;
         }
-        const int64_t x = wave_scan(wide ? 0 : cost), y = LINES == 3 ? wave_scan(wide ? cost : 0) : 0;
+        const int64_t x = LINES & 1 ? wave_scan(wide ? 0 : cost) : 0;
+        const int64_t y = LINES & 2 ? wave_scan(wide ? cost : 0) : 0;
         if (lane == 63) {
             L->sums[wave][0] = x;
             L->sums[wave][1] = y;
@@ -1370,6 +1382,7 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     M.w = xcd * (all / 8) + jj;
     M.lo = M.hi = 0;
     if (jj >= all / 8) return M;
+    if (threadIdx.x == 0) A.splits[M.slot0 / 2 + M.w].last = -1;
     M.n = M.line ? total[1] : total[0];
     M.wgs = all;
     const Cuts cuts(M.n, all);
@@ -1427,11 +1440,11 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     return M;
 }
 
-// LINES: 1 thin only, 3 thin and wide.
+// LINES: 1 thin, 2 wide, 3 both.
 template <class T, bool FP8, int DP, int LINES>
 struct Shared {
     using C = Cfg<T, FP8, DP>;
-    static constexpr int THIN = (kWaves / 2) * 64 * (4 * C::NJ + 2) * 4;
+    static constexpr int THIN = LINES & 1 ? (kWaves / 2) * 64 * (4 * C::NJ + 2) * 4 : 16;
     static constexpr int BUF = LINES == 1 ? 16 : Wide<C>::BUF;
     static constexpr int BUF0 = BUF > THIN ? BUF : THIN;
 };
@@ -1446,10 +1459,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
     __shared__ __attribute__((aligned(16))) char buf1[S::BUF];
     __shared__ uint32_t flags[2 * Wide<C>::NB];
     __shared__ uint32_t odds[kWaves];
-    if (threadIdx.x == 0) A.splits[blockIdx.x].last = -1;
     const Mine M = plan_work<LINES>(A, &plan, blockIdx.x, gridDim.x);
     if (M.lo >= M.hi) return;
-    const bool wide_line = LINES == 3 && M.line == 1;
+    const bool wide_line = LINES == 2 || (LINES == 3 && M.line == 1);
     const int32_t nseg = A.num_groups + A.num_reqs;
     const int step_log2 = wide_line ? (Wide<C>::KT == 128 ? 7 : 6) : 5;
 
@@ -1512,11 +1524,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
             to.part = pre ? 1 : 0;
             to.slot = static_cast<int32_t>(M.slot0 + 2 * M.w + (from_start ? 1 : 0));
             pos = end;
-            if (from_start && !to_end && threadIdx.x == 0) {
+            if (!to_end && threadIdx.x == 0) {
+                const Cuts cuts(M.n, M.wgs);
                 Split x;
                 x.item = item;
-                x.last = static_cast<int32_t>(Cuts(M.n, M.wgs).piece_of(item + len - 1));
-                x.w = static_cast<int32_t>(M.w);
+                x.last = static_cast<int32_t>(cuts.piece_of(item + len - 1));
+                x.w = static_cast<int32_t>(cuts.piece_of(item));
                 x.slot0 = static_cast<int32_t>(M.slot0);
                 x.wide = wide_line;
                 x.tok0 = P.seg.tok0;
@@ -1525,14 +1538,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
                 x.tile = P.tile;
                 x.keys = static_cast<int32_t>(keys < P.seg.keys ? keys : P.seg.keys);
                 x.extra = P.seg.extra;
-                A.splits[blockIdx.x] = x;
+                A.splits[M.slot0 / 2 + M.w] = x;
             }
             // a piece without a step of its own leaves nothing (k_attend_join sees it the same way)
             if (to.kind == kSlot && P.key0 >= P.key1) continue;
-            if constexpr (LINES == 3) {
+            if constexpr (LINES & 2) {
                 if (wide_line) run_wide<T, C>(A, P, to, buf0, buf1, flags, odds);
             }
-            if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(buf0));
+            if constexpr (LINES & 1) {
+                if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(buf0));
+            }
         }
         seg_start += cost;
         ++s;
@@ -1585,20 +1600,21 @@ struct Sum {
     }
 };
 
-// Adds row `slot_row` of the pieces w0 .. w1 of an item that begins at unit
-// `item`; a workgroup has left its slot if its piece has a step of keys.
+// Adds row `slot_row` of the pieces w0 + way, w0 + way + ways .. w1 of an item
+// that begins at unit `item`; a workgroup has left its slot if its piece has a
+// step of keys.
 __device__ inline void add_slots(const Args& A, Sum* sum, const Seg& g, const Cuts& cuts, int64_t item,
                                  int32_t keys, int32_t w0, int32_t w1, int32_t slot0, int slot_row,
-                                 int d, int step_log2) {
+                                 int d, int step_log2, int way, int ways) {
     constexpr int B = 4;                    // slots under way at once
-    for (int32_t w = w0; w <= w1; w += B) {
+    for (int32_t w = w0 + way; w <= w1; w += B * ways) {
         float2 ml[B];
         f32x4 x[B];
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             ml[i] = make_float2(0.0f, 0.0f);
             x[i] = f32x4{0, 0, 0, 0};
-            const int32_t v = w + i;
+            const int32_t v = w + i * ways;
             if (v > w1) continue;
             const int32_t k0 = v == w0 ? 0 : cut_key(g, cuts.start(v) - item, step_log2);
             const int32_t k1 = v == w1 ? keys : cut_key(g, cuts.start(v + 1) - item, step_log2);
@@ -1612,13 +1628,37 @@ __device__ inline void add_slots(const Args& A, Sum* sum, const Seg& g, const Cu
     }
 }
 
-// Without prefixes: kJoinParts workgroups join the item that begins in a piece
-// and ends in a later one; workgroups behind those write the rows of requests
-// without keys, 64 requests a wave.
+// The sums of `ways` neighbouring waves, in the first of them, in the order of
+// the waves.
+__device__ inline void join_ways(Sum* sum, float (*lds)[6][64], int wave, int way, int ways) {
+    if (ways == 1) return;
+    const int lane = threadIdx.x & 63;
+    __syncthreads();                        // the last rows' sums are read
+    if (way > 0) {
+        lds[wave][0][lane] = sum->m;
+        lds[wave][1][lane] = sum->l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds[wave][2 + i][lane] = sum->o[i];
+    }
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll 1
+    for (int w = wave + 1; w < wave + ways; ++w)
+        sum->add(make_float2(lds[w][0][lane], lds[w][1][lane]),
+                 f32x4{lds[w][2][lane], lds[w][3][lane], lds[w][4][lane], lds[w][5][lane]});
+}
+
+// Without prefixes: an item that lies in n pieces is joined by kJoinParts
+// workgroups for each of the first n - 1, its rows dealt to their waves; with
+// many pieces, `ways` waves share a row's.  (One wave for all pieces of a row
+// took 26 us for 4 requests behind 2048 tokens, most of the call.)  Workgroups
+// behind those write the rows of requests without keys, 64 requests a wave.
 template <class T, int DP>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Args A, int32_t pieces) {
     constexpr int LPR = DP / 4, RPW = 64 / LPR;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float sums[kJoinWaves][6][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int d = lane % LPR * 4, sub_row = lane / LPR;
     const int32_t hq = A.H * A.G;
     const int32_t block = blockIdx.x;
@@ -1638,19 +1678,24 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Arg
         }
         return;
     }
-    const Split S = A.splits[block / kJoinParts];
-    if (S.last < 0) return;
+    const int32_t piece = block / kJoinParts;
+    const Split S = A.splits[piece];
+    if (piece >= A.plan[4] + A.plan[5] || S.last < 0) return;
+    const int32_t n = uniform(S.last - S.w);            // pieces less one
+    const int ways = n < 4 ? 1 : (n < 8 ? 2 : (n < 16 ? 4 : 8));
+    const int way = wave % ways, teams = kJoinWaves / ways;
+    const int32_t me = uniform((piece - S.slot0 / 2 - S.w) * kJoinParts) + block % kJoinParts;
     Cuts cuts;
     cuts.q = A.plan[S.wide ? 2 : 0];
     cuts.r = A.plan[S.wide ? 3 : 1];
     Seg g;
     g.extra = S.extra;
     const int step_log2 = S.wide ? (DP <= 128 ? 7 : 6) : 5;
-    const int rows = S.wide ? A.wide_tokens * A.G : A.hs * kThinRows;
-    for (int row = (block % kJoinParts * kJoinWaves + wave) * RPW + sub_row; row < rows;
-         row += kJoinParts * kJoinWaves * RPW) {
+    const int rows = uniform(S.wide ? A.wide_tokens * A.G : A.hs * kThinRows);
+    for (int row0 = me * teams * RPW; row0 < rows; row0 += kJoinParts * n * teams * RPW) {
+        const int row = row0 + wave / ways * RPW + sub_row;
         int32_t local, head;
-        bool live = true;
+        bool live = row < rows;
         if (S.wide) {
             local = S.tile * A.wide_tokens + row / A.G;
             head = S.set * A.G + row % A.G;
@@ -1660,22 +1705,26 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Arg
             const int32_t kvh = vh / A.parts, hin = vh % A.parts * A.gv + a % A.gv;
             local = S.tile * A.thin_tokens + a / A.gv;
             head = kvh * A.G + hin;
-            live = a < A.thin_tokens * A.gv && kvh < A.H && hin < A.G;
+            live = live && a < A.thin_tokens * A.gv && kvh < A.H && hin < A.G;
         }
-        if (!live || local >= S.ntok) continue;
+        live = live && local < S.ntok;
         Sum sum;
-        add_slots(A, &sum, g, cuts, S.item, S.keys, S.w, S.last, S.slot0, row, d, step_log2);
-        sum.store<T>(A, S.tok0 + local, head, d);
+        if (live)
+            add_slots(A, &sum, g, cuts, S.item, S.keys, S.w, S.last, S.slot0, row, d, step_log2, way, ways);
+        join_ways(&sum, sums, wave, way, ways);
+        if (live && way == 0) sum.store<T>(A, S.tok0 + local, head, d);
     }
 }
 
 // With prefixes: the workgroups (x, .) join the rows of token x, each from its
-// two parts, a thin head's query heads (256 / DP of them) by a wave.
+// two parts, a thin head's query heads (256 / DP of them) by `ways` waves.
 // Bound by its launch and its dependent loads: the lists that the token is in
 // (guessed for one token per request, searched for otherwise), then the parts.
-template <class T, int DP>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
+template <class T, int DP, bool SHARED>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A, int32_t many) {
+    const int32_t ways = SHARED ? many : 1;
     constexpr int LPR = DP / 4, RPW = 64 / LPR;
+    __shared__ float sums[kJoinWaves][6][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t token = blockIdx.x;
@@ -1705,11 +1754,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
 
     const int32_t per = (A.gv + RPW - 1) / RPW, units = A.H * A.parts * per;
     {
-        const int32_t u = blockIdx.y * kJoinWaves + wave;
-        if (u >= units) return;
+        const int32_t way = wave % ways, mine = (blockIdx.y * kJoinWaves + wave) / ways;
+        const bool works = mine < units;
+        const int32_t u = works ? mine : 0;
         const int32_t vh = u / per, kvh = vh / A.parts, sub = vh - kvh * A.parts;
         const int32_t in = (u - vh * per) * RPW + lane / LPR, hin = sub * A.gv + in;
-        const bool live = in < A.gv && hin < A.G;
+        const bool live = works && in < A.gv && hin < A.G;
         const int32_t head = kvh * A.G + (live ? hin : 0);
         const int64_t row = static_cast<int64_t>(token) * A.H * A.G + head;
         Sum sum;
@@ -1717,7 +1767,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
         for (int k = 0; k < 2; ++k) {
             const Seg& g = part[k].g;
             const int32_t local = token - g.tok0;
-            if (g.tiles == 0 || local < 0 || local >= g.ntok) continue;
+            if (!works || g.tiles == 0 || local < 0 || local >= g.ntok) continue;
             const Cuts& cuts = g.wide ? wide : thin;
             const int32_t tile = local / g.tp, in_tile = local - tile * g.tp;
             const int32_t set = g.wide ? kvh : vh / A.hs;
@@ -1725,6 +1775,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
             const int64_t keys = tile_keys(g, tile);
             const int32_t w0 = static_cast<int32_t>(cuts.piece_of(item));
             if (item + keys + g.extra <= cuts.start(w0 + 1)) {     // one workgroup had it all
+                if (way > 0) continue;
                 const int64_t at = static_cast<int64_t>(k) * A.T * A.H * A.G + row;
                 const float2 ml = *reinterpret_cast<const float2*>(A.row_ml + at * 2);
                 sum.add(ml, d < A.D ? *reinterpret_cast<const f32x4*>(A.row_o + at * A.D + d) : f32x4{0, 0, 0, 0});
@@ -1733,10 +1784,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join(const Args A) {
                 const int slot_row = g.wide ? in_tile * A.G + (live ? hin : 0)
                                             : (vh - set * A.hs) * kThinRows + in_tile * A.gv + (live ? in : 0);
                 add_slots(A, &sum, g, cuts, item, static_cast<int32_t>(keys < g.keys ? keys : g.keys), w0,
-                          w1, g.wide ? 0 : 2 * wgs1, slot_row, d, !g.wide ? 5 : (DP <= 128 ? 7 : 6));
+                          w1, g.wide ? 0 : 2 * wgs1, slot_row, d, !g.wide ? 5 : (DP <= 128 ? 7 : 6), way, ways);
             }
         }
-        if (live) sum.store<T>(A, token, head, d);
+        join_ways(&sum, sums, wave, way, ways);
+        if (live && way == 0) sum.store<T>(A, token, head, d);
     }
 }
 

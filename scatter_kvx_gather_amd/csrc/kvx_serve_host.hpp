@@ -152,9 +152,17 @@ kvx_status validate_slots(const int64_t* slots, int64_t n, const kvx_pool* pool,
 namespace at = kvx::attend;
 
 constexpr int64_t kAttendGrid = 256;    // one workgroup per compute unit of an MI355X
+constexpr int64_t kJoinPlaces = 2048;   // waves of a join that shares rows among waves
 
-// A segment's rows on the average batch decide its tiles: wide ones from
-// kWideRows query rows per kv head on.
+// The average query rows per kv head of a batch's contexts (and those of its
+// prefixes) decide their tiles: wide ones from kWideRows on.  64 contexts of
+// 2048 keys, thin against wide: 8 kv heads of 128 dims with 16 / 32 / 64 / 128
+// rows 123 : 130, 142 : 132, 202 : 134, 384 : 149 us; with 64 dims 66 : 85, 81 :
+// 86, 125 : 87, 230 : 89; from e4m3 73 : 132, 94 : 133, 143 : 135, 265 : 139.
+// Above 128 dims of 16 bits K and V of a step ahead and the accumulators pass a
+// wave's registers, and wide tiles win at any number of rows (256 dims, 4 kv
+// heads: 1 row 152 : 110, 16 rows 159 : 112; 4 contexts 47 : 26; 512 of 300 keys
+// 185 : 157): these have no thin ones.
 constexpr int64_t kWideRows = 64;
 
 struct AttendShape {
@@ -179,8 +187,9 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     s->DP = D <= 64 ? 64 : (D <= 128 ? 128 : 256);
     s->G = q_heads / g.H;
     const int64_t rows = tokens * s->G;
-    s->own_wide = num_reqs > 0 && rows / num_reqs >= kWideRows;
-    s->pre_wide = num_groups > 0 && rows / num_groups >= kWideRows;
+    const bool all_wide = s->DP > 128 && layout->dtype != KVX_FP8;
+    s->own_wide = num_reqs > 0 && (all_wide || rows / num_reqs >= kWideRows);
+    s->pre_wide = num_groups > 0 && (all_wide || rows / num_groups >= kWideRows);
     s->wide_rows = s->DP <= 128 ? 256 : 128;
     // of the larger tile whichever this batch takes, so that a smaller batch needs no more
     s->slot_rows = std::max(s->wide_rows, at::kWaves * at::kThinRows);
@@ -208,14 +217,19 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
 }
 
 struct AttendKernels {
-    const void *main, *join, *join_items;
+    const void *main, *join, *join_shared, *join_items;
 };
 
 template <class T, bool FP8, int DP>
 AttendKernels attend_kernels(int lines) {
-    return {lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 1>)
-                       : reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 3>),
-            reinterpret_cast<const void*>(&at::k_attend_join<T, DP>),
+    const void* main;
+    if constexpr (DP > 128 && !FP8)
+        main = reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 2>);
+    else
+        main = lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 1>)
+                          : reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 3>);
+    return {main, reinterpret_cast<const void*>(&at::k_attend_join<T, DP, false>),
+            reinterpret_cast<const void*>(&at::k_attend_join<T, DP, true>),
             reinterpret_cast<const void*>(&at::k_attend_join_items<T, DP>)};
 }
 
@@ -480,12 +494,20 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.wide_tokens = s.wide_rows / s.G;
     a.pre_wide = s.pre_wide;
     a.own_wide = s.own_wide;
+    // The fewest units of a piece, and the units that an item's fixed time
+    // (queries, first loads, stores) counts for.  Shorter pieces spread a small
+    // batch over more workgroups and leave more to join: with 2^5 / 2^6 / 2^7
+    // units 4 contexts of 300 keys take 19.9 / 21.4 / 22.5 us, 4 of 2048 keys
+    // 28.1 / 22.9 / 26.5, 64 of 64 keys 19.1 / 20.5 / 16.5, one of 8192 keys 33.1 /
+    // 26.4 / 28.3.  Items of 40 to 100 (thin) and 320 to 600 units (wide) are
+    // within 3% of each other on ragged batches; without them the workgroups
+    // with many short items end last.
     a.thin_min_log2 = 6;
     a.wide_min_log2 = 8;
     a.thin_item = 64;
     a.wide_item = 450;
-    // a compute unit's time for a wide key (its products) over that for a thin
-    // key (its bytes)
+    // a compute unit's time for a wide key (its products, 2350 a ns) over that
+    // for a thin key (its bytes, 26 a ns): rates of the two loops alone
     const double wide_ns = 4.0 * s.wide_rows * s.DP / 2350.0;
     const double thin_ns = 2.0 * a.hs * g.Db / a.parts / 26.0;
     a.wide_weight = static_cast<float>(wide_ns / thin_ns);
@@ -515,9 +537,16 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     if (ng > 0) {
         const int32_t per_head = (a.gv + 256 / s.DP - 1) / (256 / s.DP);
         const int32_t units = heads * per_head;
-        void* join_params[] = {&a};
-        return hipLaunchKernel(k.join, dim3(static_cast<uint32_t>(a.T), (units + at::kJoinWaves - 1) / at::kJoinWaves),
-                               dim3(64 * at::kJoinWaves), join_params, 0, stream) == hipSuccess
+        // waves that share a row's pieces, so that a few rows' many pieces are
+        // not one wave's each (4 requests behind a prefix of 4096 tokens 50 -> 28
+        // us); with many rows the waves are better spent on those (64 requests
+        // in 8 groups 36 us; 41 with 4 waves a row)
+        int32_t ways = at::kJoinWaves;
+        while (ways > 1 && static_cast<int64_t>(a.T) * units * ways > kJoinPlaces) ways /= 2;
+        const uint32_t deep = (units * ways + at::kJoinWaves - 1) / at::kJoinWaves;
+        void* join_params[] = {&a, &ways};
+        return hipLaunchKernel(ways > 1 ? k.join_shared : k.join, dim3(static_cast<uint32_t>(a.T), deep), dim3(64 * at::kJoinWaves),
+                               join_params, 0, stream) == hipSuccess
                    ? KVX_OK
                    : KVX_E_HIP;
     }
