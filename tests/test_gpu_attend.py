@@ -174,6 +174,23 @@ def test_long_context_few_rows_is_split():
     run("long", seed=3, new=[1], ctx=[20000], H=2, G=4, D=128, page=16)
 
 
+@pytest.mark.parametrize("prefix", [0, 5000])
+@pytest.mark.parametrize("new", [[1], [3, 1], [40]])
+@pytest.mark.parametrize("D,H,G,pool", [(64, 1, 5, "bf16"), (128, 3, 2, "bf16"), (256, 1, 3, "bf16"),
+                                        (256, 1, 3, "fp8"), (128, 1, 9, "fp8")])
+def test_many_pieces(D, H, G, pool, new, prefix):
+    """Few rows and long contexts: items in two to a hundred pieces, thin and
+    wide, whose joins share a row among waves and workgroups."""
+    say("pieces", D, H, G, pool, new, prefix)
+    n = len(new)
+    extra = dict(members=[0, n], prefix=[prefix]) if prefix else {}
+    for own in (700, 6000):
+        c = Case(24, new=new, ctx=[own, 333][:n], H=H, G=G, D=D, pool=pool, page=32, **extra)
+        out, lse = c.run()
+        torch.cuda.synchronize()
+        c.check(out, lse)
+
+
 def test_scores_that_grow():
     """Maxima that rise along the keys (the accumulators are rescaled often)
     and scores of large size."""
