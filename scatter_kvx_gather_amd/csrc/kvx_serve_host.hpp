@@ -305,11 +305,15 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
         return std::max<int64_t>(1, std::max(out->cap_tokens / s + (out->cap_tokens % s != 0),
                                              out->cap_ids / i + (out->cap_ids % i != 0)));
     };
+    const bool few = num_reqs <= tb::kFewRequests;
     int64_t grid = grid_of(1, 1);
-    const void* fn = reinterpret_cast<const void*>(&tb::k_build_tables<1, 1>);
+    const void* fn = few ? reinterpret_cast<const void*>(&tb::k_build_tables<1, 1, 1>)
+                         : reinterpret_cast<const void*>(&tb::k_build_tables<1, 1, tb::kManyPerThread>);
     if (grid > tb::kShortGrid) {
-        grid = grid_of(tb::kLongSlotRun, tb::kLongIdRun);
-        fn = reinterpret_cast<const void*>(&tb::k_build_tables<tb::kLongSlotRun, tb::kLongIdRun>);
+        constexpr int S = tb::kLongSlotRun, I = tb::kLongIdRun;
+        grid = grid_of(S, I);
+        fn = few ? reinterpret_cast<const void*>(&tb::k_build_tables<S, I, 1>)
+                 : reinterpret_cast<const void*>(&tb::k_build_tables<S, I, tb::kManyPerThread>);
     }
     if (log_enabled())
         std::fprintf(stderr, "kvx: build_tables reqs=%d page=%d grid=%lld\n", num_reqs, page_size,

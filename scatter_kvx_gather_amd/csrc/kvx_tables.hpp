@@ -17,7 +17,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // (of a, P and P - h) give the token offsets, the table offsets and the place
 // of each request's new pages in the free list.  The outputs are cut into
 // windows of slots and page ids, one workgroup each.  Every workgroup sums the
-// requests itself, kChunk at a time, keeps a chunk's sums in shared memory and
+// requests itself, a chunk at a time, keeps a chunk's sums in shared memory and
 // fills the outputs of its window that belong to the chunk, each run of a
 // thread found by a binary search there: one launch, no order between
 // workgroups, and no request's length makes one workgroup's work longer.
@@ -27,13 +27,16 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // 64 requests 5.5 us against 8.0 with 4 and 2, 32 prompts page by token 5.4
 // against 7.5); with many workgroups their sums are what counts, and 4 and 2
 // are faster (2048 requests, 540 thousand ids: 18.7 us against 25.3).  The host
-// takes the short runs up to kShortGrid workgroups.
+// takes the short runs up to kShortGrid workgroups.  Likewise a thread sums one
+// request where a chunk of those holds the batch (64 requests 4.5 us against
+// 5.5 with four, 256 4.9 against 5.9), and four where not: every chunk is
+// another round of the chain (1024 requests 8.3 us against 15.7 with one).
 constexpr int kBuildThreads = 256;
-constexpr int kPerThread = 4;
-constexpr int kChunk = kBuildThreads * kPerThread;
 constexpr int kLongSlotRun = 4;         // outputs of a thread in a large grid
 constexpr int kLongIdRun = 2;
 constexpr int64_t kShortGrid = 512;
+constexpr int kFewRequests = kBuildThreads;     // one a thread
+constexpr int kManyPerThread = 4;
 
 struct BuildArgs {
     const int32_t* have;        // or NULL: none
@@ -70,7 +73,9 @@ __device__ inline Sums operator+(const Sums& a, const Sums& b) {
     return Sums{a.tok + b.tok, a.pg + b.pg, a.fresh + b.fresh};
 }
 
+template <int kPerThread>
 struct BuildShared {
+    static constexpr int kChunk = kBuildThreads * kPerThread;
     int64_t tok[kChunk + 1];
     int64_t pg[kChunk + 1];
     int64_t fresh[kChunk];
@@ -90,8 +95,8 @@ __device__ inline int last_not_above(const int64_t* off, int n, int64_t x) {
 }
 
 // Page k of request r (i-th of the chunk): a held page, or one of the free list; -1 if there is none.
-__device__ inline int32_t page_of(const BuildArgs& A, const BuildShared& S, int32_t r, int i,
-                                  int64_t k) {
+template <class Shared>
+__device__ inline int32_t page_of(const BuildArgs& A, const Shared& S, int32_t r, int i, int64_t k) {
     const int64_t held = page_index(A, static_cast<uint32_t>(S.have[i]) + A.page_size - 1);
     if (k < held) {
         const int64_t off = A.held_off[r];
@@ -102,10 +107,11 @@ __device__ inline int32_t page_of(const BuildArgs& A, const BuildShared& S, int3
     return at < A.num_free ? A.free_ids[at] : -1;
 }
 
-template <int kSlotRun, int kIdRun>
+template <int kSlotRun, int kIdRun, int kPerThread>
 __global__ __launch_bounds__(kBuildThreads) void k_build_tables(const BuildArgs A) {
     constexpr int kSlotWindow = kBuildThreads * kSlotRun, kIdWindow = kBuildThreads * kIdRun;
-    __shared__ BuildShared S;
+    constexpr int kChunk = kBuildThreads * kPerThread;
+    __shared__ BuildShared<kPerThread> S;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const bool first = blockIdx.x == 0;
     const int64_t slot0 = static_cast<int64_t>(blockIdx.x) * kSlotWindow;

@@ -53,7 +53,7 @@ def lists(rng, have, page, pool):
 
 @pytest.mark.parametrize("page", [1, 2, 7, 16, 64])
 @pytest.mark.parametrize("n,most_have,most_add", [(1, 0, 1), (1, 5000, 1), (3, 40, 40), (64, 300, 1),
-                                                  (257, 20, 3), (1023, 9, 2), (1024, 9, 2),
+                                                  (256, 20, 3), (257, 20, 3), (40, 9000, 9000), (1023, 9, 2), (1024, 9, 2),
                                                   (1025, 9, 2), (3000, 3, 1), (2, 0, 9000)])
 def test_build_tables(page, n, most_have, most_add):
     say("build", page, n, most_have, most_add)
