@@ -25,7 +25,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // Bound by the chain launch - lengths - sums - search - ids of a workgroup, not
 // by bytes.  One slot and one id a thread shorten the chain (a decode step of
 // 64 requests 5.5 us against 8.0 with 4 and 2, 32 prompts page by token 5.4
-// against 7.5); with many workgroups their sums are what counts, and 4 and 2
+// against 7.5, both with four requests a thread); with many workgroups their sums are what counts, and 4 and 2
 // are faster (2048 requests, 540 thousand ids: 18.7 us against 25.3).  The host
 // takes the short runs up to kShortGrid workgroups.  Likewise a thread sums one
 // request where a chunk of those holds the batch (64 requests 4.5 us against
