@@ -25,9 +25,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // Bound by the chain launch - lengths - sums - search - ids of a workgroup, not
 // by bytes.  One slot and one id a thread shorten the chain (a decode step of
 // 64 requests 5.5 us against 8.0 with 4 and 2, 32 prompts page by token 5.4
-// against 7.5, both with four requests a thread); with many workgroups their sums are what counts, and 4 and 2
-// are faster (2048 requests, 540 thousand ids: 18.7 us against 25.3).  The host
-// takes the short runs up to kShortGrid workgroups.  Likewise a thread sums one
+// against 7.5, both with four requests a thread); with many workgroups their
+// sums are what counts, and 4 and 2 are faster (2048 requests, 540 thousand
+// ids: 18.7 us against 25.3).  The host takes the short runs up to kShortGrid
+// workgroups.  Likewise a thread sums one
 // request where a chunk of those holds the batch (64 requests 4.5 us against
 // 5.5 with four, 256 4.9 against 5.9), and four where not: every chunk is
 // another round of the chain (1024 requests 8.3 us against 15.7 with one).
