@@ -265,9 +265,13 @@ __device__ inline int64_t tile_keys(const Seg& g, int32_t i) {
 __device__ inline int64_t set_units(const Seg& g) {
     return g.tiles > 0 ? tile_start(g, g.tiles - 1) + tile_keys(g, g.tiles - 1) + g.extra : 0;
 }
-// The key that a cut x units into an item falls on: a whole step of 2^log2 keys.
-__device__ inline int32_t cut_key(const Seg& g, int64_t x, int step_log2) {
-    return x <= g.extra ? 0 : static_cast<int32_t>((x - g.extra) >> step_log2 << step_log2);
+// The key that a cut x units into an item falls on: a whole step of 2^log2 keys,
+// or the item's end (`keys`: an item is longer than its segment has keys where a
+// causal segment has more tokens than keys).
+__device__ inline int32_t cut_key(const Seg& g, int64_t x, int step_log2, int32_t keys) {
+    if (x <= g.extra) return 0;
+    const int64_t k = (x - g.extra) >> step_log2 << step_log2;
+    return k < keys ? static_cast<int32_t>(k) : keys;
 }
 
 // A line of n units cut into `wgs` pieces whose lengths differ by one at most.
@@ -1511,9 +1515,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
             const int64_t end = M.hi < item + len ? M.hi : item + len;
             const bool from_start = pos == item, to_end = end == item + len;
             // cuts inside an item fall on whole steps, both sides alike
-            P.key0 = cut_key(P.seg, pos - item, step_log2);
-            P.key1 = to_end ? static_cast<int32_t>(keys < P.seg.keys ? keys : P.seg.keys)
-                            : cut_key(P.seg, end - item, step_log2);
+            const int32_t seen = static_cast<int32_t>(keys < P.seg.keys ? keys : P.seg.keys);
+            P.key0 = cut_key(P.seg, pos - item, step_log2, seen);
+            P.key1 = to_end ? seen : cut_key(P.seg, end - item, step_log2, seen);
             P.counts = P.set == 0 && P.tile == P.seg.tiles - 1;
             Dest to;
             if (from_start && to_end) {
@@ -1536,7 +1540,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
                 x.ntok = P.seg.ntok;
                 x.set = P.set;
                 x.tile = P.tile;
-                x.keys = static_cast<int32_t>(keys < P.seg.keys ? keys : P.seg.keys);
+                x.keys = seen;
                 x.extra = P.seg.extra;
                 A.splits[M.slot0 / 2 + M.w] = x;
             }
@@ -1616,8 +1620,8 @@ __device__ inline void add_slots(const Args& A, Sum* sum, const Seg& g, const Cu
             x[i] = f32x4{0, 0, 0, 0};
             const int32_t v = w + i * ways;
             if (v > w1) continue;
-            const int32_t k0 = v == w0 ? 0 : cut_key(g, cuts.start(v) - item, step_log2);
-            const int32_t k1 = v == w1 ? keys : cut_key(g, cuts.start(v + 1) - item, step_log2);
+            const int32_t k0 = v == w0 ? 0 : cut_key(g, cuts.start(v) - item, step_log2, keys);
+            const int32_t k1 = v == w1 ? keys : cut_key(g, cuts.start(v + 1) - item, step_log2, keys);
             if (k0 >= k1) continue;
             const int64_t at = static_cast<int64_t>(slot0 + 2 * v + (v == w0 ? 1 : 0)) * A.slot_rows + slot_row;
             ml[i] = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);

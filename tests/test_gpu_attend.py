@@ -383,3 +383,23 @@ def test_random_batches(seed):
         v_scale=0.2 if pool else 1.0, page=int(rng.choice([1, 5, 16, 32])),
         layout=str(rng.choice(["nhd", "hnd"])), bad=float(rng.choice([0, 0, 0.2])),
         causal=bool(rng.random() < 0.8), **kw)
+
+
+@pytest.mark.parametrize("kind", ["wide", "thin"])
+@pytest.mark.parametrize("prefix", [0, 33])
+@pytest.mark.parametrize("ctx", [2, 130])
+def test_skipped_where_tokens_outnumber_the_context(kind, prefix, ctx):
+    """More query tokens than context, in items that are cut: the page table
+    behind a request's own list is no key of it, and is not counted."""
+    say("skipped", kind, prefix, ctx)
+    # 2000 rows of one kv head in wide tiles; 200 among 41 requests in thin ones
+    new, G = ([1000, 3], 4) if kind == "wide" else ([200] + [0] * 40, 1)
+    n = len(new)
+    extra = dict(members=[0, n], prefix=[prefix]) if prefix else {}
+    for bad in (0.0, 0.4):
+        c = Case(90, new=new, ctx=[ctx] + [0] * (n - 1), H=1, G=G, D=64, bad=bad, page=4, **extra)
+        skipped = torch.zeros(1, dtype=torch.int64, device=DEV)
+        out, lse = c.run(skipped=skipped)
+        torch.cuda.synchronize()
+        c.check(out, lse)
+        assert skipped.item() == c.b.skipped(), bad
