@@ -403,3 +403,28 @@ def test_skipped_where_tokens_outnumber_the_context(kind, prefix, ctx):
         torch.cuda.synchronize()
         c.check(out, lse)
         assert skipped.item() == c.b.skipped(), bad
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_groups_equal_contexts_of_their_own(new):
+    """Several groups, one of them without requests and one without a prefix:
+    the prefix's pages in front of each request's own list, as one context,
+    give the same sums within the bounds of both."""
+    say("groups as contexts", new)
+    members, prefix = [0, 2, 2, 3, 6], [48, 16, 0, 112]
+    c = Case(32, new=[new, 1, new, 1, 2, new], ctx=[new + 5, 1, new, 20, 33, new + 64], H=2, G=4, D=64,
+             members=members, prefix=prefix)
+    b = c.b
+    lists, off, ctx = [], [0], []
+    for r, n in enumerate(b.ctx):
+        g = b.group_of(r)
+        lists += list(b.pre_ids[b.pre_off[g]:b.pre_off[g + 1]]) + list(b.ids[b.pg_off[r]:b.pg_off[r + 1]])
+        off.append(len(lists))
+        ctx.append(n + prefix[g])
+    out, lse = c.run()
+    out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    kvx.attend(c.lay, 0, c.pool, c.reqs, ints(ctx, torch.int32),
+               kvx.Table(ints(off, torch.int64), ints(lists, torch.int32)), c.qd, out2, lse=lse2)
+    torch.cuda.synchronize()
+    c.check(out, lse)
+    c.check(out2, lse2)
