@@ -122,7 +122,8 @@ typedef enum kvx_status {
     KVX_E_UNSUPPORTED = 6,  /* a valid request this build does not implement */
     KVX_E_HIP = 7,          /* the HIP runtime refused a launch or a device query */
     KVX_E_DUPLICATE = 8,    /* checkers: two written rows are the same row or overlap */
-    KVX_E_OVERLAP = 9       /* kvx_check_disjoint: a written row overlaps a row the call reads */
+    KVX_E_OVERLAP = 9       /* kvx_check_disjoint, kvx_serve.h: a written row (or array) overlaps
+                             * one that the call reads */
 } kvx_status;
 
 typedef enum kvx_dtype {

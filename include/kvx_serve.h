@@ -52,8 +52,9 @@ typedef struct kvx_batch_tables {
  * or a held one outside held->page_ids, is written as -1, and a token in a page
  * with a negative id gets slot -1: kvx's calls skip such rows.  Negative
  * lengths count as 0, and a request's total stops at 2^31 - 1 tokens.  At most
- * 2^24 requests (KVX_E_RANGE).  The outputs must not overlap the inputs (a held
- * table is read while the new one is written).  One launch. */
+ * 2^24 requests (KVX_E_RANGE).  No output may overlap an input (the lengths and
+ * the held table are read while the new ones are written) or another output:
+ * KVX_E_OVERLAP, by the arrays' addresses and sizes.  One launch. */
 kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* have_len,
                             const int32_t* add_len, const kvx_table* held,
                             const int32_t* free_ids, int64_t num_free,

@@ -708,8 +708,9 @@ def build_tables(out: BatchTables, page_size: int, add_len: torch.Tensor, free_i
                  stream=None) -> None:
     """Page table, token offsets and slots of a batch in which request r holds
     have_len[r] tokens in the pages of `held` and gets add_len[r] more, new
-    pages taken from free_ids in order (kvx_build_tables).  `out` must not
-    share memory with `held`: a loop keeps two BatchTables and alternates."""
+    pages taken from free_ids in order (kvx_build_tables).  `out` shares no
+    memory with the inputs, `have_len` and `held` among them (KvxError): a loop
+    keeps two BatchTables and alternates."""
     n = out.num_reqs
     add, free = _vector("add_len", add_len, torch.int32, n), _vector("free_ids", free_ids,
                                                                      torch.int32, 0)

@@ -31,10 +31,13 @@ kvx_status no_throw(F f) {
     }
 }
 
+// A launch's threads are counted in 32 bits.
+bool launch_fits(int64_t grid, int threads) { return grid <= UINT32_MAX / threads; }
+
 template <class Args>
 kvx_status launch_one(const void* fn, int64_t grid, int threads, Args& a, hipStream_t stream) {
     if (grid <= 0) return KVX_OK;
-    if (grid > UINT32_MAX / threads) return KVX_E_RANGE;     // a launch's threads are counted in 32 bits
+    if (!launch_fits(grid, threads)) return KVX_E_RANGE;
     void* params[] = {&a};
     return hipLaunchKernel(fn, dim3(static_cast<uint32_t>(grid)), dim3(threads), params, 0, stream) ==
                    hipSuccess
@@ -42,7 +45,48 @@ kvx_status launch_one(const void* fn, int64_t grid, int threads, Args& a, hipStr
                : KVX_E_HIP;
 }
 
+// Bytes of a buffer, to compare with another's (a count that passes the address
+// space ends with it).
+struct Extent {
+    uintptr_t lo, hi;
+    Extent(const void* p, int64_t count, int64_t size) : lo(reinterpret_cast<uintptr_t>(p)), hi(lo) {
+        uintptr_t bytes = 0;
+        if (p == nullptr || count <= 0) return;
+        if (__builtin_mul_overflow(static_cast<uintptr_t>(count), static_cast<uintptr_t>(size), &bytes) ||
+            __builtin_add_overflow(lo, bytes, &hi))
+            hi = UINTPTR_MAX;
+    }
+    bool meets(const Extent& x) const { return std::max(lo, x.lo) < std::min(hi, x.hi); }
+};
+
 // ------------------------------------------------------------- building --
+
+// The first workgroup writes lengths and offsets while others read theirs, and
+// ids and slots are written window by window.
+kvx_status check_build_overlap(int32_t n, const int32_t* have, const int32_t* add,
+                               const kvx_table* held, const int32_t* free_ids, int64_t num_free,
+                               const kvx_batch_tables* o) {
+    const bool holds = have != nullptr && n > 0;
+    const Extent in[] = {{have, n, 4},
+                         {add, n, 4},
+                         {holds ? held->pg_off : nullptr, n, 8},
+                         {holds ? held->page_ids : nullptr, holds ? held->num_ids : 0, 4},
+                         {free_ids, num_free, 4}};
+    const Extent out[] = {{o->ctx_len, n, 4},
+                          {o->tok_off, int64_t(n) + 1, 8},
+                          {o->pg_off, int64_t(n) + 1, 8},
+                          {o->page_ids, o->cap_ids, 4},
+                          {o->slots, o->cap_tokens, 8},
+                          {o->totals, 4, 8}};
+    constexpr int N = sizeof(out) / sizeof(out[0]);
+    for (int i = 0; i < N; ++i) {
+        for (const Extent& x : in)
+            if (out[i].meets(x)) return KVX_E_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (out[i].meets(out[j])) return KVX_E_OVERLAP;
+    }
+    return KVX_OK;
+}
 
 kvx_status check_build(int32_t num_reqs, int32_t page_size, const int32_t* have,
                        const int32_t* add, const kvx_table* held, const int32_t* free_ids,
@@ -274,10 +318,6 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
                             const kvx_batch_tables* out, hipStream_t stream) {
     namespace tb = kvx::tables;
     KVX_TRY(check_build(num_reqs, page_size, have_len, add_len, held, free_ids, num_free, out));
-    if (validate_enabled())
-        KVX_TRY(no_throw([&] {
-            return validate_build(num_reqs, page_size, have_len, add_len, held, out, stream);
-        }));
     tb::BuildArgs a;
     std::memset(&a, 0, sizeof(a));
     a.have = num_reqs > 0 ? have_len : nullptr;
@@ -315,6 +355,12 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
         fn = few ? reinterpret_cast<const void*>(&tb::k_build_tables<S, I, 1>)
                  : reinterpret_cast<const void*>(&tb::k_build_tables<S, I, tb::kManyPerThread>);
     }
+    if (!launch_fits(grid, tb::kBuildThreads)) return KVX_E_RANGE;
+    KVX_TRY(check_build_overlap(num_reqs, have_len, add_len, held, free_ids, num_free, out));
+    if (validate_enabled())
+        KVX_TRY(no_throw([&] {
+            return validate_build(num_reqs, page_size, have_len, add_len, held, out, stream);
+        }));
     if (log_enabled())
         std::fprintf(stderr, "kvx: build_tables reqs=%d page=%d grid=%lld\n", num_reqs, page_size,
                      static_cast<long long>(grid));

@@ -104,6 +104,55 @@ def test_build_tables_total_stops_at_int32():
     assert o.slots[2].item() == 4 * (1 << 20) + 5
 
 
+def test_build_tables_in_buffers_side_by_side():
+    """Inputs and outputs that touch, in one allocation, do not overlap; one
+    that is an input's memory is refused and nothing is written."""
+    say("build side by side")
+    n, page, have, add = 3, 4, [5, 0, 9], [4, 1, 7]
+    held_lists, free = [[3, 4], [], [7, 8, 9]], list(range(20, 30))
+    exp = ref.build_tables(page, have, add, held_lists, free)
+    arena = torch.full((4096,), 77, dtype=torch.uint8, device=DEV)
+    at = 0
+
+    def take(count, dtype):
+        nonlocal at
+        size = count * torch.empty(0, dtype=dtype).element_size()
+        at += size
+        return arena[at - size:at].view(dtype)
+
+    ids = [x for h in held_lists for x in h]
+    slots, pages = len(exp["slots"]), len(exp["ids"])
+    free_ids, held_ids, page_ids = (take(c, torch.int32) for c in (len(free), len(ids), pages + pages % 2 + 1))
+    have_len, ctx, add_len = (take(n, torch.int32) for _ in range(3))
+    at += -at % 8
+    held_off, tok_off, pg_off = (take(n + 1, torch.int64) for _ in range(3))
+    o = kvx.BatchTables(n, slots, pages)
+    o.slots, o.totals = take(slots, torch.int64), take(4, torch.int64)
+    o.ctx_len, o.tok_off, o.pg_off, o.page_ids = ctx, tok_off, pg_off, page_ids[:pages]
+    o._c = kvx._CBatchTables(*(x.data_ptr() for x in (ctx, tok_off, pg_off, page_ids)), pages,
+                             o.slots.data_ptr(), slots, o.totals.data_ptr())
+    for dst, src in ((free_ids, free), (held_ids, ids), (have_len, have), (add_len, add),
+                     (held_off, offsets([len(x) for x in held_lists]))):
+        dst.copy_(torch.as_tensor(np.asarray(src)))
+    held = kvx.Table(held_off, held_ids)
+    kvx.build_tables(o, page, add_len, free_ids, have_len=have_len, held=held)
+    torch.cuda.synchronize()
+    assert ctx.tolist() == exp["ctx"] and tok_off.tolist() == exp["tok_off"]
+    assert pg_off.tolist() == exp["pg_off"] and o.page_ids.tolist() == exp["ids"]
+    assert o.slots.tolist() == exp["slots"] and o.totals.tolist() == exp["totals"]
+    assert have_len.tolist() == have and add_len.tolist() == add and held_ids.tolist() == ids
+    before = arena.clone()
+    for kw in (dict(have_len=ctx), dict(add_len=ctx), dict(held=kvx.Table(pg_off, held_ids)),
+               dict(free_ids=page_ids)):
+        args = dict(add_len=add_len, free_ids=free_ids, have_len=have_len, held=held)
+        args.update(kw)
+        with pytest.raises(kvx.KvxError) as e:
+            kvx.build_tables(o, page, **args)
+        assert e.value.status == 9, kw
+    torch.cuda.synchronize()
+    assert torch.equal(arena, before)
+
+
 # ----------------------------------------------------------------- append --
 
 def e4m3(x):

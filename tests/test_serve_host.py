@@ -76,6 +76,32 @@ def test_build_tables_refusals():
     assert build(cap_tokens=1 << 36) == E_RANGE
 
 
+BUILD_SIZES = dict(have=12, add=12, held_off=24, held_ids=32, free=40, ctx_len=12, tok_off=32, pg_off=32,
+                   page_ids=1024, slots=2048, totals=32)     # bytes, of 3 requests
+BUILD_OUT = ("ctx_len", "tok_off", "pg_off", "page_ids", "slots", "totals")
+
+
+def build_at(**at):
+    """build() with each buffer a MiB from the next one, but for those at `at`."""
+    a = {f: A + (i << 20) for i, f in enumerate(BUILD_SIZES)}
+    a.update(at)
+    return build(have=a["have"], add=a["add"], held=(a["held_off"], a["held_ids"], 8), free=a["free"],
+                 cap_ids=256, cap_tokens=256, **{f: a[f] for f in BUILD_OUT})
+
+
+def test_build_tables_refuses_overlaps():
+    """A workgroup writes an output while others read the lengths and the held
+    table, so no output may share a byte with them, nor with another output."""
+    at = {f: A + (i << 20) for i, f in enumerate(BUILD_SIZES)}
+    for out in BUILD_OUT:
+        for f, size in BUILD_SIZES.items():
+            if f == out:
+                continue
+            assert build_at(**{out: at[f]}) == E_OVERLAP, (out, f)
+            assert build_at(**{out: at[f] + size - 4}) == E_OVERLAP, (out, f)
+            assert build_at(**{out: at[f] - BUILD_SIZES[out] + 4}) == E_OVERLAP, (out, f)
+
+
 # ----------------------------------------------------------------- append --
 
 def append(lay=None, layer=0, p=None, bl=0, slots=A, skipped=None, rows=True, **r):
