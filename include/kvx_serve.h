@@ -104,7 +104,7 @@ typedef struct kvx_prefix {
 
 typedef struct kvx_attention {
     const void* q;          /* DEVICE [total_tokens][q_heads][head_dim] */
-    void* out;              /* DEVICE, of the same shape and type; not q's memory */
+    void* out;              /* DEVICE, of the same shape and type */
     float* lse;             /* NULL or DEVICE [total_tokens][q_heads] */
     int64_t q_stride;       /* bytes between tokens: multiples of 16, at least a row */
     int64_t out_stride;
@@ -148,6 +148,9 @@ typedef struct kvx_attention {
  * kernels stay inside the pool, the workspace, q, out and lse, and the result
  * is unspecified.  Negative lengths count as 0, and those past 2^30 as 2^30.  At
  * most 2^24 requests and groups and 2^23 - 1 query tokens (KVX_E_RANGE).
+ *
+ * No row of out may share a byte with one of q, nor lse or the workspace with
+ * either or each other (KVX_E_OVERLAP); slices of one fused buffer are fine.
  *
  * The workspace holds partial sums during the call and nothing between calls.
  * Calls that may run at the same time, graph replays among them, need a

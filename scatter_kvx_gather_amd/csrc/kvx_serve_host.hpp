@@ -284,6 +284,32 @@ AttendKernels attend_kernels(int DP, int lines) {
                        : attend_kernels<T, FP8, 256>(lines);
 }
 
+// n rows of `len` bytes, `stride` apart.
+struct StridedRows {
+    const void* at;
+    int64_t stride, len, n;
+};
+
+// Whether a row of `a` shares a byte with a row of `b`.  q and out may be slices
+// of one fused buffer, whose spans overlap while their rows do not.
+bool rows_meet(const StridedRows& a, const StridedRows& b) {
+    if (a.at == nullptr || b.at == nullptr) return false;
+    const Extent ea(a.at, (a.n - 1) * a.stride + a.len, 1), eb(b.at, (b.n - 1) * b.stride + b.len, 1);
+    if (!ea.meets(eb)) return false;
+    // rows i of a and j of b, k = i - j, of one stride s meet if and only if
+    // -a.len < d + k s < b.len, d = a - b: the smallest k for the left side
+    // decides.  With other strides, one row of b after the other.
+    const int64_t d0 = static_cast<int64_t>(ea.lo - eb.lo), s = a.stride;
+    const bool alike = a.stride == b.stride;
+    for (int64_t j = 0; j < (alike ? 1 : b.n); ++j) {
+        const int64_t d = d0 - j * b.stride, x = -a.len - d;
+        int64_t k = (x >= 0 ? x / s : -((-x + s - 1) / s)) + 1;
+        k = std::max(k, alike ? 1 - b.n : int64_t(0));
+        if (k < a.n && d + k * s < b.len) return true;
+    }
+    return false;
+}
+
 kvx_status validate_attend(const kvx_reqs* reqs, const int32_t* ctx, const kvx_prefix* prefix,
                            hipStream_t stream) {
     if (hipStreamSynchronize(stream) != hipSuccess) return KVX_E_HIP;
@@ -494,7 +520,14 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
         (reinterpret_cast<uintptr_t>(x.lse) & 3u) != 0)
         return KVX_E_ALIGN;
     if (x.workspace_bytes < s.bytes) return KVX_E_SHAPE;
-    if (x.q == x.out) return KVX_E_OVERLAP;
+    const int64_t T = reqs->total_tokens, lse_bytes = T * x.q_heads * 4;    // inside T * row
+    const StridedRows buffers[] = {{x.q, x.q_stride, row, T},
+                                   {x.out, x.out_stride, row, T},
+                                   {x.lse, lse_bytes, lse_bytes, 1},
+                                   {x.workspace, s.bytes, s.bytes, 1}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (rows_meet(buffers[i], buffers[j])) return KVX_E_OVERLAP;
     if (validate_enabled())
         KVX_TRY(no_throw([&] { return validate_attend(reqs, ctx_len, prefix, stream); }));
 

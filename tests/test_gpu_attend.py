@@ -428,3 +428,30 @@ def test_groups_equal_contexts_of_their_own(new):
     torch.cuda.synchronize()
     c.check(out, lse)
     c.check(out2, lse2)
+
+
+@pytest.mark.parametrize("new", [[1], [3, 1, 50]])
+def test_queries_and_outputs_of_one_buffer(new):
+    """q and out as slices of one fused buffer do not overlap; outputs that
+    share a byte with a query are refused and nothing is written."""
+    say("one buffer", new)
+    n, T, Hq, D = len(new), sum(new), 8, 64
+    c = Case(9, new=new, ctx=[30, 64, 90][:n], H=2, G=4, D=D, members=[0, n], prefix=[20])
+    for q_at, out_at in ((0, Hq), (Hq + 2, 1)):
+        fused = torch.full((T, 2 * Hq + 3, D), 7.0, device=DEV, dtype=c.qd.dtype)
+        q, out = fused[:, q_at:q_at + Hq], fused[:, out_at:out_at + Hq]
+        q.copy_(c.qd)
+        _, lse = c.run(q=q, out=out)
+        torch.cuda.synchronize()
+        c.check(out, lse)
+        rest = [h for h in range(2 * Hq + 3) if not out_at <= h < out_at + Hq]
+        before = fused[:, rest].clone()
+        c.run(q=q, out=out)
+        assert torch.equal(fused[:, rest], before) and torch.equal(q, c.qd)
+    for out_at in (Hq - 1, Hq + 3, Hq + 2):
+        before = fused.clone()
+        with pytest.raises(kvx.KvxError) as e:
+            c.run(q=q, out=fused[:, out_at:out_at + Hq])
+        assert e.value.status == 9
+        torch.cuda.synchronize()
+        assert torch.equal(fused, before)

@@ -228,6 +228,37 @@ def test_attend_refusals():
     assert attend(prefix=ok, workspace_bytes=1 << 20) == E_SHAPE
 
 
+def attend_at(T=4, q_stride=8192, out_stride=8192, **at):
+    """attend() of T tokens (rows of 8192 bytes) with its buffers 1 GiB apart, but
+    for those at `at`, and exactly the workspace that it needs."""
+    ws = ctypes.c_int64(0)
+    assert kvx.load_library().kvx_attend_workspace(layout(), 2, 0, T, 32, ctypes.byref(ws)) == OK
+    a = dict(q=A, out=A + (1 << 30), lse=A + (2 << 30), workspace=A + (3 << 30))
+    a.update(at)
+    return attend(reqs=(2, T, A), q_stride=q_stride, out_stride=out_stride, workspace_bytes=ws.value, **a)
+
+
+def test_attend_refuses_overlaps():
+    """Rows of out are written while other workgroups read q's; lse and the
+    workspace are no one's rows either.  (What is disjoint is run on the GPU.)"""
+    for d in (0, 16, 8176, -16, -8176, 8192, 3 * 8192 + 16, -3 * 8192 - 16):
+        assert attend_at(out=A + d) == E_OVERLAP, d
+    for d in (0, 16, 8176, -8176):
+        assert attend_at(T=1, out=A + d) == E_OVERLAP, d
+    # rows of one fused buffer that share bytes, of other tokens too
+    for d in (0, 8176, -8176, 12304, 20480 + 8176, -20480 + 16, 3 * 20480, -3 * 20480):
+        assert attend_at(q_stride=20480, out_stride=20480, out=A + d) == E_OVERLAP, d
+    # different strides: row 1 of out ends in row 2 of q
+    assert attend_at(T=3, q_stride=32768, out_stride=40960, out=A + 2 * 32768 - 40960 - 16) == E_OVERLAP
+    assert attend_at(T=3, q_stride=40960, out_stride=8192, out=A + 40960 - 2 * 8192 - 16) == E_OVERLAP
+    for d in (0, 4, 3 * 8192 + 8188, -4 * 32 * 4 + 4):      # lse has 4 * 32 * 4 bytes
+        assert attend_at(lse=A + d) == E_OVERLAP, d
+        assert attend_at(lse=A + (1 << 30) + d) == E_OVERLAP, d
+        assert attend_at(lse=A + (3 << 30) + d) == E_OVERLAP, d
+    for f in ("q", "out", "lse"):
+        assert attend_at(**{f: A + (3 << 30) + (1 << 20)}) == E_OVERLAP, f
+
+
 def workspace(lay, n, g, t, hq):
     out = ctypes.c_int64(-7)
     s = kvx.load_library().kvx_attend_workspace(lay, n, g, t, hq, ctypes.byref(out))
