@@ -663,6 +663,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _launch(dev: int, stream, fn, *args) -> int:
     """fn(*args, stream handle) with GPU `dev` current; the default stream is
     that GPU's current one."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"a stream of GPU {stream.device_index} for tensors on GPU {dev}")
     if dev == torch.cuda.current_device():
         return fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
     with torch.cuda.device(dev):

@@ -328,6 +328,23 @@ def test_binding_refusals():
             kvx.build_tables(o, 16, **args)
 
 
+def test_binding_refuses_a_stream_of_another_gpu(monkeypatch):
+    """A launch goes to the tensors' GPU, whose stream it has to be."""
+    class Stream:
+        def __init__(self, index):
+            self.device_index, self.cuda_stream = index, 5
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    calls = []
+    for dev, index in ((0, 1), (1, 0)):
+        with pytest.raises(ValueError, match="stream"):
+            kvx._launch(dev, Stream(index), lambda *a: calls.append(a), 1, 2)
+    assert not calls
+    kvx._launch(0, Stream(0), lambda *a: calls.append(a), 1, 2)
+    assert calls == [(1, 2, 5)]
+
+
 # ------------------------------------------------------- the plain reference --
 
 def test_reference_tables():
