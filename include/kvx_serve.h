@@ -71,8 +71,10 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
  * KVX_E_UNSUPPORTED).  Scales are finite, positive and from 2^-64 to 2^64
  * (KVX_E_RANGE), and 1 is required where nothing is rounded.  A slot outside the
  * pool is skipped and counted once in *skipped (if not NULL).  Distinct tokens
- * have distinct slots (unchecked; KVX_VALIDATE=1 returns KVX_E_DUPLICATE).  The
- * layout has num_kv = 2.  One launch. */
+ * have distinct slots, and no row of k or v lies in a slot that the call writes
+ * (a page may be copied to another); both are unchecked, and KVX_VALIDATE=1
+ * returns KVX_E_DUPLICATE or KVX_E_OVERLAP.  The layout has num_kv = 2.  One
+ * launch. */
 typedef struct kvx_rows {
     const void* k;
     const void* v;

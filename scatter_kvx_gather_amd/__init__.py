@@ -736,7 +736,8 @@ def append(layout: Layout, layer: int, pool: Pool, slots: torch.Tensor, k: torch
            skipped: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows k[t], v[t] ([tokens, kv_heads, head_dim], dense in the last two
     dimensions) to slot slots[t] of the layer's planes; an "fp8" pool holds
-    e4m3 of x / scale (kvx_append)."""
+    e4m3 of x / scale (kvx_append).  Rows of the same pool may be appended to
+    slots that none of them lies in."""
     _check_pool("pool", layout, pool)
     h, d = layout.kv_heads, layout.head_dim
     ks, vs = _token_rows("k", k, h, d), _token_rows("v", v, h, d)

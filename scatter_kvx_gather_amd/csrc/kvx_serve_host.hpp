@@ -175,20 +175,49 @@ kvx_status check_layer(const kvx_layout* layout, int32_t layer, const kvx_pool* 
     return KVX_OK;
 }
 
-// KVX_VALIDATE=1: no slot of the pool is written twice.
-kvx_status validate_slots(const int64_t* slots, int64_t n, const kvx_pool* pool, hipStream_t stream) {
+// KVX_VALIDATE=1: no slot of the pool is written twice, and no row of k or v
+// (`row` bytes) lies in one that is written.
+kvx_status validate_append(const LayerRef& ref, int32_t block_layout, const kvx_pool* pool,
+                           const int64_t* slots, const kvx_rows* rows, int64_t row,
+                           hipStream_t stream) {
     if (hipStreamSynchronize(stream) != hipSuccess) return KVX_E_HIP;
-    std::vector<int64_t> s;
-    KVX_TRY(to_host(slots, n, &s));
-    s.erase(std::remove_if(s.begin(), s.end(),
-                           [&](int64_t x) { return x < 0 || x / pool->page_size >= pool->num_pages; }),
-            s.end());
+    std::vector<int64_t> at;
+    KVX_TRY(to_host(slots, rows->num_tokens, &at));
+    auto skipped = [&](int64_t x) { return x < 0 || x / pool->page_size >= pool->num_pages; };
+    std::vector<int64_t> s = at;
+    s.erase(std::remove_if(s.begin(), s.end(), skipped), s.end());
     std::sort(s.begin(), s.end());
     const auto twice = std::adjacent_find(s.begin(), s.end());
-    if (twice == s.end()) return KVX_OK;
-    std::fprintf(stderr, "kvx: KVX_VALIDATE: append: slot %lld twice; nothing enqueued\n",
-                 static_cast<long long>(*twice));
-    return KVX_E_DUPLICATE;
+    if (twice != s.end()) {
+        std::fprintf(stderr, "kvx: KVX_VALIDATE: append: slot %lld twice; nothing enqueued\n",
+                     static_cast<long long>(*twice));
+        return KVX_E_DUPLICATE;
+    }
+    const int64_t runs = block_layout == KVX_HND ? ref.g.H : 1;     // a head-major row is a run per head
+    std::vector<Span> written, read;
+    for (int64_t t = 0; t < rows->num_tokens; ++t) {
+        const int64_t x = at[static_cast<size_t>(t)];
+        if (skipped(x)) continue;
+        const uint64_t off = static_cast<uint64_t>(x / pool->page_size * ref.page_stride +
+                                                   x % pool->page_size * ref.row_stride);
+        for (const char* plane : {ref.k, ref.v})
+            for (int64_t h = 0; h < runs; ++h) {
+                const uint64_t lo = reinterpret_cast<uint64_t>(plane) + off +
+                                    static_cast<uint64_t>(h * ref.head_stride);
+                written.push_back(Span{lo, lo + static_cast<uint64_t>(ref.g.R / runs), t});
+            }
+        const uint64_t k = reinterpret_cast<uint64_t>(rows->k) + static_cast<uint64_t>(t * rows->k_stride);
+        const uint64_t v = reinterpret_cast<uint64_t>(rows->v) + static_cast<uint64_t>(t * rows->v_stride);
+        read.push_back(Span{k, k + static_cast<uint64_t>(row), t});
+        read.push_back(Span{v, v + static_cast<uint64_t>(row), t});
+    }
+    int64_t bad = 0;
+    const kvx_status st = spans_disjoint(&written, &read, &bad);
+    if (st != KVX_OK)
+        std::fprintf(stderr, "kvx: KVX_VALIDATE: append: a row is %s (token %lld); nothing enqueued\n",
+                     st == KVX_E_OVERLAP ? "read and written" : "written twice",
+                     static_cast<long long>(bad));
+    return st;
 }
 
 // ------------------------------------------------------------ attention --
@@ -424,7 +453,9 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     if (!mul_ok(rows->num_tokens, std::max(rows->k_stride, rows->v_stride), &span))
         return KVX_E_RANGE;
     if (validate_enabled())
-        KVX_TRY(no_throw([&] { return validate_slots(slots, rows->num_tokens, pool, stream); }));
+        KVX_TRY(no_throw([&] {
+            return validate_append(ref, block_layout, pool, slots, rows, row, stream);
+        }));
     tb::AppendArgs a;
     std::memset(&a, 0, sizeof(a));
     a.src[0] = static_cast<const char*>(rows->k);

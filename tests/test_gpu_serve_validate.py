@@ -91,3 +91,50 @@ def test_validate_mode_refuses_broken_tables():
     assert "validate ok" in p.stdout
     for call in ("request 1's lengths", "append: slot", "attend: KVX_E_SHAPE"):
         assert call in p.stderr, call
+
+
+CHILD_OVERLAP = r"""
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import scatter_kvx_gather_amd as kvx
+
+dev = torch.device("cuda:0")
+for bl in ("nhd", "hnd"):
+    for dtype in ("bf16", "fp8"):
+        t = torch.bfloat16 if dtype == "bf16" else torch.float8_e4m3fn
+        lay = kvx.Layout(2, 2, 2, 64, dtype)
+        store = (torch.arange(4 * 8 * 4 * 128, device=dev) % 200).view(4, 8, 4, 2, 64).to(torch.bfloat16).to(t)
+        pool = kvx.Pool(store, 8, 4)
+        slots = torch.tensor([8, -1, 10, 11], device=dev)           # in page 2
+        page = lambda plane, p: store[plane, p].view(torch.uint8).view(4, 2, -1).view(t)
+        before = store.clone()
+        # page 2 of another layer, and page 3 of this one, are not written: a page is copied
+        for k, v in ((page(0, 2), page(1, 2)), (page(2, 3), page(3, 3)), (page(3, 1), page(2, 1))):
+            kvx.append(lay, 1, pool, slots, k, v, block_layout=bl)
+        torch.cuda.synchronize()
+        assert not torch.equal(store.view(torch.uint8), before.view(torch.uint8))
+        store.copy_(before)
+        for k, v in ((page(2, 2), page(0, 0)), (page(0, 0), page(2, 2)), (page(3, 2), page(0, 0)),
+                     (store[2].view(t).reshape(32, 2, 64)[5:9], page(0, 0))):
+            torch.cuda.synchronize()
+            try:
+                kvx.append(lay, 1, pool, slots, k, v, block_layout=bl)
+            except kvx.KvxError as e:
+                assert e.status == 9, e.status
+            else:
+                raise AssertionError("not refused")
+            torch.cuda.synchronize()
+            assert torch.equal(store.view(torch.uint8), before.view(torch.uint8))
+print("overlap ok", flush=True)
+"""
+
+
+def test_validate_mode_refuses_appended_rows_that_are_written():
+    """Rows of k and v that lie in the slots that the call writes; others of the
+    same pool may be appended (a page copied to another)."""
+    p = subprocess.run([sys.executable, "-c", CHILD_OVERLAP.format(root=ROOT)], capture_output=True,
+                       text=True, timeout=120, env=dict(os.environ, KVX_VALIDATE="1"), cwd=ROOT)
+    assert p.returncode == 0, p.stdout + p.stderr
+    assert "overlap ok" in p.stdout
+    assert "append: a row is read and written" in p.stderr
