@@ -143,7 +143,14 @@ typedef struct kvx_attention {
  * The pool holds the type of q, or KVX_FP8 (e4m3); f32 pools, num_kv = 1 and
  * head_dim above 256 are KVX_E_UNSUPPORTED.  head_dim * element size is a
  * multiple of 16.  Products and sums are 32 bits; the softmax's weights are
- * rounded to q's type for their product with V.
+ * rounded to q's type for their product with V (half a step: 2^-8 of a weight
+ * in bf16, 2^-11 in f16).
+ *
+ * Range.  Weights are taken against a reference that may lag the maximum and
+ * reach 2^8 (in bf16) before the division by their sum, so bf16 values larger
+ * than 2^119 over the number of keys seen may make an infinity where their mean
+ * is finite; those of f16 and e4m3 pools cannot.  Scores of finite inputs
+ * (scale * q.k * log2 e) have to stay inside +-2^127.
  *
  * The contracts of tok_off and grp_off are unchecked (KVX_VALIDATE=1 checks
  * them, and that lengths are not negative: KVX_E_SHAPE); with broken ones the

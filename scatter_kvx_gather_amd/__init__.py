@@ -794,7 +794,8 @@ def attend(layout: Layout, layer: int, pool: Pool, reqs: Requests, ctx_len: torc
     ones (kvx_attend).  ``scale`` defaults to head_dim ** -0.5.  ``lse``: float32
     [tokens, q_heads].  ``workspace``: a uint8 tensor of attend_workspace bytes,
     kept by a caller whose calls do not overlap; by default one is allocated
-    for the call."""
+    for the call.  Softmax weights are rounded to q's type; bf16 values have to
+    stay below 2^119 over the keys seen (the sums' range)."""
     _check_pool("pool", layout, pool)
     _check_table("table", table, reqs)
     t, d = reqs.total_tokens, layout.head_dim

@@ -455,3 +455,24 @@ def test_queries_and_outputs_of_one_buffer(new):
         assert e.value.status == 9
         torch.cuda.synchronize()
         assert torch.equal(fused, before)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_largest_values(new):
+    """bf16 values at the size that the sums' range allows for (2^119 over the
+    keys seen), with scores that rise along the keys past the first maximum."""
+    say("largest values", new)
+    n = 96
+    c = Case(33, new=[new], ctx=[n], H=2, G=4, D=64, page=16)
+    rows = c.b.rows(c.b.pg_off[0], c.b.ids, n)
+    c.q = torch.ones_like(c.q)
+    k = torch.zeros(n, 2, 64)
+    k[:, :, 0] = torch.linspace(0, 5.4, n)[:, None]
+    c.kv[0][rows] = k.to(c.kv[0].dtype)
+    sign = torch.where(torch.rand(n, 2, 64, generator=torch.Generator().manual_seed(1)) < 0.9, 1.0, -1.0)
+    c.kv[1][rows] = (sign * 2.0 ** 119 / 128).to(c.kv[1].dtype)
+    c.upload()
+    out, lse = c.run(scale=1.0, causal=False)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all()
+    c.check(out, lse, 1.0, False)
