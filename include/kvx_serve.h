@@ -150,7 +150,9 @@ typedef struct kvx_attention {
  * reach 2^8 (in bf16) before the division by their sum, so bf16 values larger
  * than 2^119 over the number of keys seen may make an infinity where their mean
  * is finite; those of f16 and e4m3 pools cannot.  Scores of finite inputs
- * (scale * q.k * log2 e) have to stay inside +-2^127.
+ * (scale * q.k * log2 e) have to stay inside +-2^127.  An infinity or a NaN among
+ * the values makes an infinity or a NaN in the outputs that see it (a NaN also
+ * from an infinity whose weight rounds to 0).
  *
  * The contracts of tok_off and grp_off are unchecked (KVX_VALIDATE=1 checks
  * them, and that lengths are not negative: KVX_E_SHAPE); with broken ones the

@@ -30,7 +30,7 @@
 // one key range, so a pool row is read whole by one workgroup, and K and V go
 // from memory to the matrix instructions through registers alone, a step of 32
 // keys ahead, page ids two.  256 requests behind 256 to 2048 tokens, 8 kv heads
-// of 128 dims: 255 us, 4.9 TB/s, what a large copy reaches on this card.
+// of 128 dims: 255 us, 4.9 TB/s (a copy of 2 GiB: 4.91, read and written).
 //
 // Wide tiles (128 or 256 rows a workgroup) are for segments with many rows,
 // where the matrix units and what feeds them are the bound: 64 or 128 keys at a
@@ -44,8 +44,10 @@
 // softmax, and half of the waves staging after their first step beat one step
 // (664 -> 442 us with the split items' join, 410 -> 397).
 //
-// The second launch joins what is split: 3 to 10 us, as long as a chain of its
-// launch and three dependent loads.
+// The second launch joins what is split: 3 to 10 us where that is a chain of its
+// launch and three dependent loads, more where its bytes count: behind a prefix
+// every row has two parts, of which it reads 32-bit partial rows (256 requests
+// of 64 heads 15 us, 8 chunks of 100 to 256 tokens of 32 heads, 47 MB, 26 us).
 //
 // Fragments.  S^T = K Q^T by 16x16x32 products: K rows are loaded as the A
 // operand holds them (lane a + 16 g: key a, 8 dims at 8 g).  The result has

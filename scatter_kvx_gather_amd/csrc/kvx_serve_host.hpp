@@ -228,14 +228,18 @@ constexpr int64_t kAttendGrid = 256;    // one workgroup per compute unit of an 
 constexpr int64_t kJoinPlaces = 2048;   // waves of a join that shares rows among waves
 
 // The average query rows per kv head of a batch's contexts (and those of its
-// prefixes) decide their tiles: wide ones from kWideRows on.  64 contexts of
-// 2048 keys, thin against wide: 8 kv heads of 128 dims with 16 / 32 / 64 / 128
-// rows 123 : 130, 142 : 132, 202 : 134, 384 : 149 us; with 64 dims 66 : 85, 81 :
-// 86, 125 : 87, 230 : 89; from e4m3 73 : 132, 94 : 133, 143 : 135, 265 : 139.
-// Above 128 dims of 16 bits K and V of a step ahead and the accumulators pass a
-// wave's registers, and wide tiles win at any number of rows (256 dims, 4 kv
-// heads: 1 row 152 : 110, 16 rows 159 : 112; 4 contexts 47 : 26; 512 of 300 keys
-// 185 : 157): these have no thin ones.
+// prefixes) decide their tiles, one kind for all: wide ones from kWideRows on.
+// The host has no lengths but total_tokens, so rows that a padded batch does not
+// use count too, and in a batch that mixes prompts with single tokens one of the
+// two runs in the other's tiles (63 tokens from e4m3 beside a prompt of 2048: 226
+// us, apart 60 + 87; 255 beside a chunk of 512: 253, apart 209 + 56).  Contexts
+// all alike, 64 of 2048 keys, thin against wide: 8 kv heads of 128 dims with 16 /
+// 32 / 64 / 128 rows 123 : 130, 142 : 132, 202 : 134, 384 : 149 us; with 64 dims
+// 66 : 85, 81 : 86, 125 : 87, 230 : 89; from e4m3 73 : 132, 94 : 133, 143 : 135,
+// 265 : 139. Above 128 dims of 16 bits K and V of a step ahead and the
+// accumulators pass a wave's registers, and wide tiles win at any number of rows
+// (256 dims, 4 kv heads: 1 row 152 : 110, 16 rows 159 : 112; 4 contexts 47 : 26;
+// 512 of 300 keys 185 : 157): these have no thin ones.
 constexpr int64_t kWideRows = 64;
 
 struct AttendShape {
