@@ -130,12 +130,26 @@ typedef enum kvx_dtype {
     KVX_F16 = 1,            /* 2-byte elements */
     KVX_BF16 = 2,           /* 2-byte elements */
     KVX_FP8 = 3,            /* 1-byte elements */
-    KVX_F32 = 4             /* 4-byte elements */
+    KVX_F32 = 4,            /* 4-byte elements */
+    KVX_FP4 = 5             /* 4-bit elements with a scale byte per 32 (below) */
 } kvx_dtype;
 
 /* Row shape of a KV cache ([distserve] byte formula; [mini] tensor shapes).
  * R = kv_heads * head_dim * element size must be a multiple of 16 bytes and
- * at most 65536; Q = num_layers * num_kv. */
+ * at most 65536; Q = num_layers * num_kv.
+ *
+ * KVX_FP4 rows hold e2m1 numbers (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign in the
+ * highest bit) and, for each 32 dims of a head, a scale byte s that stands for
+ * 2^(s - 127), 255 for a block of NaN (OCP MX's FP4 with E8M0 scales).
+ * head_dim is a multiple of 32 (KVX_E_ALIGN).  All heads' numbers come first,
+ * head_dim / 2 bytes each, dim 2 i in the low half of byte i; then all heads'
+ * scales, head_dim / 32 bytes each; then padding:
+ *   R = kv_heads * head_dim * 17 / 32, rounded up to a multiple of 16.
+ * In head-major blocks (kvx_block_layout) a page holds its numbers as
+ * [kv_heads][page_size][head_dim / 2] and behind them its scales as
+ * [kv_heads][page_size][head_dim / 32].  kvx_gather, kvx_scatter and
+ * kvx_gather_scatter copy such rows whole; kvx_gather_scatter_heads and the
+ * permutes refuse them (KVX_E_UNSUPPORTED). */
 typedef struct kvx_layout {
     int32_t num_layers;     /* >= 1 */
     int32_t num_kv;         /* 2 for separate K and V planes, 1 for one latent plane per layer */

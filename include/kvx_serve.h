@@ -67,9 +67,15 @@ kvx_status kvx_build_tables(int32_t num_reqs, int32_t page_size, const int32_t* 
  * and V planes, in NHD or HND blocks (kvx_block_layout).  The rows are copied
  * bit by bit where dtype is the pool's; a KVX_FP8 pool also takes f16, bf16 and
  * f32 rows, which it holds as e4m3 (OCP, nearest even) of x / k_scale and
- * x / v_scale, values past +-448 held at +-448 and NaN kept (other pairs:
- * KVX_E_UNSUPPORTED).  Scales are finite, positive and from 2^-64 to 2^64
- * (KVX_E_RANGE), and 1 is required where nothing is rounded.  A slot outside the
+ * x / v_scale, values past +-448 held at +-448 and NaN kept.  A KVX_FP4 pool
+ * takes f16, bf16 and f32 rows: each block of 32 dims is held under the smallest
+ * 2^e that leaves its largest |x / scale| (32 bits) at most 7 * 2^e, e inside
+ * -23 .. 13, its numbers rounded to the nearest of x / scale / 2^e (ties to the
+ * even code, past 6 to 6, so that an infinity is held as 6), and a block with a
+ * NaN as 32 of them; every held value is exact in f16, bf16 and f32, and a row's
+ * padding keeps its contents.  (Other pairs: KVX_E_UNSUPPORTED.)  Scales are
+ * finite, positive and from 2^-64 to 2^64 (KVX_E_RANGE), and 1 is required where
+ * nothing is rounded.  A slot outside the
  * pool is skipped and counted once in *skipped (if not NULL).  Distinct tokens
  * have distinct slots, and no row of k or v lies in a slot that the call writes
  * (a page may be copied to another); both are unchecked, and KVX_VALIDATE=1
@@ -140,16 +146,18 @@ typedef struct kvx_attention {
  * keys than one workgroup takes is joined in an order that depends on the
  * lengths alone, so results repeat bit for bit.
  *
- * The pool holds the type of q, or KVX_FP8 (e4m3); f32 pools, num_kv = 1 and
- * head_dim above 256 are KVX_E_UNSUPPORTED.  head_dim * element size is a
- * multiple of 16.  Products and sums are 32 bits; the softmax's weights are
+ * The pool holds the type of q, KVX_FP8 (e4m3) or KVX_FP4; f32 pools, num_kv = 1
+ * and head_dim above 256 are KVX_E_UNSUPPORTED.  head_dim * element size is a
+ * multiple of 16.  Values of KVX_FP4 pools take part as they are held; their
+ * scale bytes are 104 to 140 or 255, which is what kvx_append writes (the results
+ * of others are unspecified).  Products and sums are 32 bits; the softmax's weights are
  * rounded to q's type for their product with V (half a step: 2^-8 of a weight
  * in bf16, 2^-11 in f16).
  *
  * Range.  Weights are taken against a reference that may lag the maximum and
  * reach 2^8 (in bf16) before the division by their sum, so bf16 values larger
  * than 2^119 over the number of keys seen may make an infinity where their mean
- * is finite; those of f16 and e4m3 pools cannot.  Scores of finite inputs
+ * is finite; those of f16, e4m3 and 4-bit pools cannot.  Scores of finite inputs
  * (scale * q.k * log2 e) have to stay inside +-2^127.  An infinity or a NaN among
  * the values makes an infinity or a NaN in the outputs that see it (a NaN also
  * from an infinity whose weight rounds to 0).

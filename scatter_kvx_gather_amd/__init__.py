@@ -1,10 +1,10 @@
 """kvx: paged KV-cache gather / scatter / gather-scatter and the HF
 [1, H, S, D] <-> [S, H, D] permutes on one MI355X (gfx950), and the serving
-step around a pool: page tables built from lengths, rows appended, attention
-with shared prefixes.
+step around a pool: page tables built from lengths, rows appended and read back,
+attention with shared prefixes, over pools of 16, 8 and 4 bits.
 
-A thin ctypes binding over ``libkvx.so`` (C ABI and contract: include/kvx.h and
-include/kvx_serve.h).  It only marshals arguments -- torch tensors become device pointers and sizes,
+A thin ctypes binding over ``libkvx.so`` (C ABI and contract: include/kvx.h,
+include/kvx_serve.h and include/kvx_read.h).  It only marshals arguments -- torch tensors become device pointers and sizes,
 streams become ``hipStream_t`` handles -- and every byte is moved by the HIP
 kernels in the library.  PyTorch is used for device memory and streams only.
 
@@ -24,15 +24,15 @@ import torch
 __all__ = ["KvxError", "Layout", "Pool", "Requests", "Table", "Heads", "gather", "scatter",
            "gather_scatter", "gather_scatter_heads", "extract_permute", "rebuild_permute",
            "check_tables", "check_disjoint", "library_path", "DTYPE_CODES", "load_library",
-           "BatchTables", "Prefix", "build_tables", "append", "attend", "attend_workspace"]
+           "BatchTables", "Prefix", "build_tables", "append", "read", "attend", "attend_workspace"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkvx.so")
 _lib = None
 
-DTYPE_CODES = {"f16": 1, "bf16": 2, "fp8": 3, "f32": 4}
+DTYPE_CODES = {"f16": 1, "bf16": 2, "fp8": 3, "f32": 4, "fp4": 5}
 OUT_CACHED = 1          # kvx.h KVX_OUT_CACHED
-_ELEM = {"f16": 2, "bf16": 2, "fp8": 1, "f32": 4}
+_ELEM = {"f16": 2, "bf16": 2, "fp8": 1, "f32": 4, "fp4": 0.5}    # fp4: of its numbers
 
 
 class KvxError(RuntimeError):
@@ -138,7 +138,9 @@ def load_library():
     lib.kvx_attend.argtypes = [P(_CLayout), i32, P(_CPool), i32, P(_CReqs), vp, P(_CTable),
                                P(_CPrefix), P(_CAttention), vp, vp]
     lib.kvx_attend_workspace.argtypes = [P(_CLayout), i32, i32, p64, i32, P(p64)]
-    for f in (lib.kvx_build_tables, lib.kvx_append, lib.kvx_attend, lib.kvx_attend_workspace):
+    lib.kvx_read.argtypes = lib.kvx_append.argtypes     # kvx_rows_out has kvx_rows' members
+    for f in (lib.kvx_build_tables, lib.kvx_append, lib.kvx_attend, lib.kvx_attend_workspace,
+              lib.kvx_read):
         f.restype = ctypes.c_int
     lib.kvx_status_str.argtypes = [ctypes.c_int]
     lib.kvx_status_str.restype = ctypes.c_char_p
@@ -336,7 +338,9 @@ def _stream(stream) -> int:
 
 
 class Layout:
-    """Row shape: Q = num_layers * num_kv planes of kv_heads x head_dim elements."""
+    """Row shape: Q = num_layers * num_kv planes of kv_heads x head_dim elements.
+    ``dtype``: "f16", "bf16", "f32", "fp8" (e4m3) or "fp4" (e2m1 with a scale byte
+    per 32 dims, kvx.h KVX_FP4; a pool of it is made of uint8 tensors)."""
 
     def __init__(self, num_layers: int, num_kv: int, kv_heads: int, head_dim: int,
                  dtype: str = "bf16"):
@@ -353,7 +357,10 @@ class Layout:
 
     @property
     def row_bytes(self) -> int:
-        return self.kv_heads * self.head_dim * _ELEM[self.dtype]
+        n = self.kv_heads * self.head_dim
+        if self.dtype == "fp4":     # numbers, scales, padding to 16 bytes
+            return (n * 17 // 32 + 15) // 16 * 16
+        return n * _ELEM[self.dtype]
 
 
 def _plane_array(planes) -> ctypes.Array:
@@ -736,8 +743,27 @@ def append(layout: Layout, layer: int, pool: Pool, slots: torch.Tensor, k: torch
            skipped: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows k[t], v[t] ([tokens, kv_heads, head_dim], dense in the last two
     dimensions) to slot slots[t] of the layer's planes; an "fp8" pool holds
-    e4m3 of x / scale (kvx_append).  Rows of the same pool may be appended to
-    slots that none of them lies in."""
+    e4m3 of x / scale, an "fp4" pool e2m1 of it under a power of two per 32 dims
+    (kvx_append).  Rows of the same pool may be appended to slots that none of
+    them lies in."""
+    _rows_call("kvx_append", (_lib or load_library()).kvx_append, layout, layer, pool, slots, k, v,
+               k_scale, v_scale, block_layout, skipped, stream)
+
+
+def read(layout: Layout, layer: int, pool: Pool, slots: torch.Tensor, k: torch.Tensor,
+         v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0, block_layout: str = "nhd",
+         skipped: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows of slots[t] of the layer's planes into k[t], v[t] ([tokens, kv_heads,
+    head_dim], dense in the last two dimensions): the pool's own type bit by
+    bit, or an "fp8" or "fp4" pool's values times the scales as f16, bf16 or f32
+    (kvx_read, the inverse of append).  Rows of a slot outside the pool stay as
+    they were."""
+    _rows_call("kvx_read", (_lib or load_library()).kvx_read, layout, layer, pool, slots, k, v,
+               k_scale, v_scale, block_layout, skipped, stream)
+
+
+def _rows_call(what: str, fn, layout, layer, pool, slots, k, v, k_scale, v_scale, block_layout,
+               skipped, stream) -> None:
     _check_pool("pool", layout, pool)
     h, d = layout.kv_heads, layout.head_dim
     ks, vs = _token_rows("k", k, h, d), _token_rows("v", v, h, d)
@@ -750,8 +776,8 @@ def append(layout: Layout, layer: int, pool: Pool, slots: torch.Tensor, k: torch
     _counter(skipped)
     dev = _one_device(k, v, slots, _pool_tensor(pool), skipped)
     rows = _CRows(k.data_ptr(), v.data_ptr(), ks, vs, n, _TORCH_CODES[k.dtype], k_scale, v_scale)
-    _check(_launch(dev, stream, (_lib or load_library()).kvx_append, layout._c, layer, pool._c,
-                   _block_layout(block_layout), at, rows, _ptr(skipped)), "kvx_append")
+    _check(_launch(dev, stream, fn, layout._c, layer, pool._c, _block_layout(block_layout), at, rows,
+                   _ptr(skipped)), what)
 
 
 class Prefix:

@@ -81,23 +81,30 @@ bool mul_ok(int64_t a, int64_t b, int64_t* out) {
 struct Geom {
     int32_t Q;
     int64_t R;       // row bytes
-    int64_t Db;      // head_dim * element size
+    int64_t Db;      // head_dim * element size (KVX_FP4: of the numbers)
     int32_t H;
 };
 
 kvx_status check_layout(const kvx_layout* l, Geom* g) {
     if (l == nullptr) return KVX_E_NULL;
+    const bool fp4 = l->dtype == KVX_FP4;
     const int eb = elem_bytes(l->dtype);
-    if (eb == 0) return KVX_E_DTYPE;
+    if (eb == 0 && !fp4) return KVX_E_DTYPE;
     if (l->num_layers < 1 || l->num_kv < 1 || l->num_kv > 2 || l->kv_heads < 1 ||
         l->head_dim < 1)
         return KVX_E_SHAPE;
     int64_t Q = static_cast<int64_t>(l->num_layers) * l->num_kv;
-    int64_t Db = static_cast<int64_t>(l->head_dim) * eb;
+    int64_t Db = fp4 ? l->head_dim / 2 : static_cast<int64_t>(l->head_dim) * eb;
     int64_t R = 0;
     if (Q > (1 << 20)) return KVX_E_RANGE;
-    if (!mul_ok(Db, l->kv_heads, &R) || R > kMaxRowBytes) return KVX_E_RANGE;
-    if (R % 16 != 0) return KVX_E_ALIGN;
+    if (fp4) {
+        if (l->head_dim % 32 != 0) return KVX_E_ALIGN;
+        if (!mul_ok(l->head_dim / 32 * 17, l->kv_heads, &R) || R > kMaxRowBytes) return KVX_E_RANGE;
+        R = (R + 15) / 16 * 16;
+    } else {
+        if (!mul_ok(Db, l->kv_heads, &R) || R > kMaxRowBytes) return KVX_E_RANGE;
+        if (R % 16 != 0) return KVX_E_ALIGN;
+    }
     g->Q = static_cast<int32_t>(Q);
     g->R = R;
     g->Db = Db;
@@ -1337,6 +1344,7 @@ kvx_status kvx_gather_scatter_heads(const kvx_layout* layout,
                                     unsigned long long* skipped, hipStream_t stream) {
     Geom g;
     KVX_TRY(check_layout(layout, &g));
+    if (layout->dtype == KVX_FP4) return KVX_E_UNSUPPORTED;     // a head's scales lie elsewhere
     if (g.Db % 16 != 0) return KVX_E_ALIGN;
     KVX_TRY(check_reqs(reqs));
     KVX_TRY(check_pool(src, g));
@@ -1359,6 +1367,7 @@ kvx_status kvx_extract_permute(const kvx_layout* layout, const void* const* hf_p
     Geom g;
     KVX_TRY(check_out_flags(flags));
     KVX_TRY(check_layout(layout, &g));
+    if (layout->dtype == KVX_FP4) return KVX_E_UNSUPPORTED;
     KVX_TRY(check_hf(g, hf_planes, s_cap, seq_len));
     int64_t need = 0;
     if (!mul_ok(seq_len, static_cast<int64_t>(g.Q) * g.R, &need)) return KVX_E_RANGE;
@@ -1375,6 +1384,7 @@ kvx_status kvx_rebuild_permute(const kvx_layout* layout, const void* in, int64_t
     Geom g;
     KVX_TRY(check_out_flags(flags));
     KVX_TRY(check_layout(layout, &g));
+    if (layout->dtype == KVX_FP4) return KVX_E_UNSUPPORTED;
     KVX_TRY(check_hf(g, hf_planes, s_cap, seq_len));
     int64_t need = 0;
     if (!mul_ok(seq_len, static_cast<int64_t>(g.Q) * g.R, &need)) return KVX_E_RANGE;

@@ -133,9 +133,13 @@ struct Args {
     int64_t row_stride;                 // bytes between the rows of a page, of one head
     int64_t page_stride;
     int64_t head_stride;
+    int64_t s_base;                     // 4 bits: the scales of a page's rows, from s_base on
+    int64_t s_row;
+    int64_t s_head;
     int64_t num_pages;
     int32_t page_size;
     int32_t page_shift;                 // log2(page_size), or -1
+    int32_t tiled;                      // 4 bits: a tile of 16 keys lies in one page
     const int64_t* tok_off;             // [num_reqs + 1]
     const int32_t* ctx;                 // [num_reqs]
     const int64_t* grp_off;             // [num_groups + 1]
@@ -329,6 +333,13 @@ __device__ inline int64_t key_offset(const Args& A, const Lists& L, int64_t pg0,
     return page_offset(A, L, pg0, key_page(A, L, pg0, t), t, end);
 }
 
+// From the offset of key t's numbers of head 0 to that of its scales.
+__device__ inline int64_t scales_from(const Args& A, int32_t t) {
+    const uint32_t tu = static_cast<uint32_t>(t), b = static_cast<uint32_t>(A.page_size);
+    const uint32_t row = A.page_shift >= 0 ? tu & (b - 1) : tu % b;
+    return A.s_base - row * (A.row_stride - A.s_row);
+}
+
 // ------------------------------------------------------------ elements --
 
 template <class T>
@@ -347,6 +358,14 @@ struct Mma<__bf16> {
     static __device__ uint32_t from_fp8(uint32_t w) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
     }
+    // numbers 2 i and 2 i + 1 of w times a power of two (i constant where it is inlined)
+    static __device__ uint32_t from_fp4(uint32_t w, float unit, int i) {
+        const auto r = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 0)
+                       : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 1)
+                       : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 2)
+                                : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 3);
+        return __builtin_bit_cast(uint32_t, r);
+    }
     static __device__ float lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
     static __device__ float hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
     static constexpr uint32_t kExp = 0x7f807f80u;       // exponent bits of both halves
@@ -364,6 +383,14 @@ struct Mma<_Float16> {
     template <bool HI>
     static __device__ uint32_t from_fp8(uint32_t w) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+    }
+    // numbers 2 i and 2 i + 1 of w times a power of two (i constant where it is inlined)
+    static __device__ uint32_t from_fp4(uint32_t w, float unit, int i) {
+        const auto r = i == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, unit, 0)
+                       : i == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, unit, 1)
+                       : i == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, unit, 2)
+                                : __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, unit, 3);
+        return __builtin_bit_cast(uint32_t, r);
     }
     static __device__ float lo(uint32_t w) {
         return static_cast<float>(__builtin_bit_cast(f16x2, w).x);
@@ -386,11 +413,12 @@ __device__ inline uint32_t finite_quad(uint32_t w) {
     return w & ~((nan >> 7) * 0xffu);
 }
 
-// Shapes of one (query type, pool element, padded head dim) combination.
-template <class T, bool FP8, int DP>
+// Shapes of one (query type, bits of a pool's value, padded head dim) combination.
+template <class T, int BITS, int DP>
 struct Cfg {
-    static constexpr int EB = FP8 ? 1 : 2;
+    static constexpr int EB = BITS / 8;                 // bytes of a value (4 bits: 0)
     static constexpr int KS = DP / 32;                  // k-steps of the first product
+    static constexpr bool FP4 = BITS == 4;
     static constexpr int NK = DP * EB / 64;             // 16-byte loads of K per key tile
     static constexpr int VE = DP >= 128 ? 8 : 4;        // dims of V a lane holds per chunk
     static constexpr int NC = DP / (16 * VE);           // chunks of V
@@ -401,6 +429,8 @@ struct Cfg {
 // First dim of the 8 that k-step ks takes from lane group g.
 template <class C>
 __device__ inline int k_dim(int ks, int g) {
+    // 4 bits: a lane group's dims are one scale's 32, or half of them
+    if (C::FP4) return C::KS == 2 ? g * 16 + ks * 8 : (ks >> 2) * 128 + g * 32 + (ks & 3) * 8;
     return C::EB == 2 ? ks * 32 + g * 8 : (ks >> 1) * 64 + g * 16 + (ks & 1) * 8;
 }
 
@@ -554,8 +584,9 @@ __device__ inline float move_maximum(Rows<C>* R, const f32x4* s, float scale, u3
 // whose weights are positive, is added here: the value itself.  Rare, and a V
 // row at a time from memory.  Keys [from, to); `limit` is the lane's row's.
 template <class T, class C, bool WIDE>
-__device__ inline void add_not_finite(const Args& A, const Lists& L, int64_t pg0, const char* vhead,
+__device__ inline void add_not_finite(const Args& A, const Lists& L, int64_t pg0, int32_t kvh,
                                       int32_t from, int32_t to, int32_t limit, Rows<C>* R) {
+    const char* vhead = A.v + kvh * (C::FP4 ? A.s_head : A.head_stride);
     const int g = here_lane() >> 4;
 #pragma unroll 1
     for (int32_t t = from; t < to; ++t) {
@@ -569,7 +600,10 @@ __device__ inline void add_not_finite(const Args& A, const Lists& L, int64_t pg0
             const int d = WIDE ? x * 16 + 4 * g : c * 16 * C::VE + (4 * g + r) * C::VE + x % Q * 4;
             if (d >= A.D || t >= limit) continue;
             uint32_t w[2];
-            if constexpr (C::EB == 2) {
+            if constexpr (C::FP4) {             // a block of NaN, by its scale
+                const uint8_t s = *reinterpret_cast<const uint8_t*>(vhead + off + scales_from(A, t) + d / 32);
+                w[0] = w[1] = s == 255 ? Mma<T>::kExp | 0x00010001u : 0u;
+            } else if constexpr (C::EB == 2) {
                 const u32x2 y = *reinterpret_cast<const u32x2*>(vhead + off + d * 2);
                 w[0] = y.x;
                 w[1] = y.y;
@@ -702,6 +736,40 @@ __device__ inline void mask_scores(f32x4* s, int32_t key0, int32_t limit, uint32
         const int key = (i >> 2) * 16 + 4 * g + (i & 3);
         const bool seen = (key0 + key < limit) & (((valid >> key) & 1) != 0);
         s[i >> 2][i & 3] = seen ? s[i >> 2][i & 3] : -INFINITY;
+    }
+}
+
+// Joins the waves that shared a head's keys: the upper half of the parts hands
+// over to the lower until one is left.
+template <class C>
+__device__ inline void join_parts(const Args& A, Rows<C>* state, float* lds, int h, int part, bool works) {
+    const int lane = here_lane();
+    Rows<C>& R = *state;
+    for (int n = A.kp; n > 1;) {
+        const int half = (n + 1) / 2;
+        __syncthreads();
+        if (works && part >= half && part < n) {
+            float* b = lds + ((part - half) * A.hs + h) * (64 * (4 * C::NJ + 2));
+            b[lane] = R.m;
+            b[64 + lane] = R.l;
+#pragma unroll
+            for (int j = 0; j < C::NJ; ++j)
+                *reinterpret_cast<f32x4*>(b + 128 + (j * 64 + lane) * 4) = R.o[j];
+        }
+        __syncthreads();
+        if (works && part + half < n) {
+            const float* b = lds + (part * A.hs + h) * (64 * (4 * C::NJ + 2));
+            const float m2 = b[lane], l2 = b[64 + lane];
+            const float m = fmaxf(R.m, m2);
+            const float ref = m == -INFINITY ? 0.0f : m;
+            const float w1 = __builtin_amdgcn_exp2f(R.m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
+            R.m = m;
+            R.l = R.l * w1 + l2 * w2;
+#pragma unroll
+            for (int j = 0; j < C::NJ; ++j)
+                R.o[j] = R.o[j] * w1 + *reinterpret_cast<const f32x4*>(b + 128 + (j * 64 + lane) * 4) * w2;
+        }
+        n = half;
     }
 }
 
@@ -851,39 +919,271 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
         if (first_odd >= 0) {
             // the wave's own steps only: `step` apart
             for (int32_t t = first_odd; t < P.key1; t += step)
-                add_not_finite<T, C, false>(A, P.lists, P.pg0, vhd, t,
+                add_not_finite<T, C, false>(A, P.lists, P.pg0, kvh, t,
                                             t + kKeys < P.key1 ? t + kKeys : P.key1, limit, &R);
         }
     }
 
-    // join the waves that shared a head's keys: the upper half of the parts
-    // hands over to the lower until one is left
-    for (int n = A.kp; n > 1;) {
-        const int half = (n + 1) / 2;
-        __syncthreads();
-        if (works && part >= half && part < n) {
-            float* b = lds + ((part - half) * A.hs + h) * (64 * (4 * C::NJ + 2));
-            b[lane] = R.m;
-            b[64 + lane] = R.l;
-#pragma unroll
-            for (int j = 0; j < C::NJ; ++j)
-                *reinterpret_cast<f32x4*>(b + 128 + (j * 64 + lane) * 4) = R.o[j];
+    join_parts<C>(A, &R, lds, h, part, works);
+    if (works && part == 0) store_rows<T, C, false>(A, to, R, h * kThinRows + a, token, head, live);
+    if (A.kp > 1) __syncthreads();
+}
+
+// ------------------------------------------------- thin, 4-bit pools --
+//
+// A step is 64 keys: 4 tiles of 16.  A lane (a, g) holds of K 16-byte pieces of
+// key a, one scale's 32 dims each (8 bytes below 128 dims), so that a piece
+// makes the operands of four products under one scale; of V the numbers of 8
+// dims (4 below 128 dims) of key 4 g + i, whose scale reaches it by a shuffle:
+// lane l loads the scales of key l.  Conversions multiply by the scale, and every
+// held value is exact in 16 bits, so nothing but the weights is rounded.
+//
+// TILED: a tile's keys lie in one page, whose offset is then in scalar
+// registers and each lane's own part is the same for all tiles.
+
+// Scale b of a lane's word(s) as a power of two: the conversions look at a
+// float's exponent alone, so the byte is rotated to it and the rest left there.
+__device__ inline int scale_turn(int b) { return (8 * (b & 3) + 9) & 31; }
+__device__ inline float scale_at(uint32_t w, int turn) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_alignbit(w, w, turn) & 0x7f800000u);
+}
+
+// The scales of a row's head, D / 32 bytes; none past them.
+template <int DP>
+struct Scales {
+    static constexpr int N = DP > 128 ? 2 : 1;
+    uint32_t w[N];
+};
+
+template <int DP>
+__device__ inline Scales<DP> load_scales(const char* p, int D) {
+    Scales<DP> s;
+    if (D == DP) {
+        if constexpr (DP == 64) s.w[0] = *reinterpret_cast<const uint16_t*>(p);
+        if constexpr (DP == 128) s.w[0] = *reinterpret_cast<const uint32_t*>(p);
+        if constexpr (DP == 256) {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+            s.w[0] = x.x;
+            s.w[1] = x.y;
         }
-        __syncthreads();
-        if (works && part + half < n) {
-            const float* b = lds + (part * A.hs + h) * (64 * (4 * C::NJ + 2));
-            const float m2 = b[lane], l2 = b[64 + lane];
-            const float m = fmaxf(R.m, m2);
-            const float ref = m == -INFINITY ? 0.0f : m;
-            const float w1 = __builtin_amdgcn_exp2f(R.m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
-            R.m = m;
-            R.l = R.l * w1 + l2 * w2;
-#pragma unroll
-            for (int j = 0; j < C::NJ; ++j)
-                R.o[j] = R.o[j] * w1 + *reinterpret_cast<const f32x4*>(b + 128 + (j * 64 + lane) * 4) * w2;
-        }
-        n = half;
+        return s;
     }
+#pragma unroll
+    for (int i = 0; i < Scales<DP>::N; ++i) s.w[i] = 0;
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b)
+        if (b * 32 < D) s.w[b / 4] |= static_cast<uint32_t>(*reinterpret_cast<const uint8_t*>(p + b)) << (b % 4 * 8);
+    return s;
+}
+
+// w with bytes of 255 (blocks of NaN) cleared.
+__device__ inline uint32_t finite_scales(uint32_t w) {
+    const uint32_t nan = (w & ((w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+    return w & ~((nan >> 7) * 0xffu);
+}
+
+template <class T, class C, bool TILED>
+__device__ void run_thin4(const Args& A, const Piece& P, const Dest& to, float* lds) {
+    constexpr int DP = C::KS * 32, X = 4, STEP = 16 * X;
+    constexpr int KP = DP > 128 ? 2 : 1;                  // pieces of K a lane holds of a key
+    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = wave % A.hs, part = wave / A.hs;
+    const int32_t vh = P.set * A.hs + h;                  // thin head
+    const int32_t kvh = vh / A.parts, sub = vh % A.parts;
+    const bool works = part < A.kp && vh < A.H * A.parts;
+    count_skipped(A, P, wave);
+
+    // this lane's query row
+    const int32_t local = P.tile * A.thin_tokens + a / A.gv;
+    const int32_t hsub = sub * A.gv + a % A.gv;
+    const bool live = works && a < A.thin_tokens * A.gv && local < P.seg.ntok && hsub < A.G;
+    const int32_t token = P.seg.tok0 + local;
+    const int32_t head = kvh * A.G + hsub;
+    const int32_t past = P.seg.keys - P.seg.ntok;
+    // keys that this row sees, and the fewest that a row of the tile sees
+    int32_t limit = P.key1, all_see = P.key1;
+    if (P.seg.causal) {
+        if (live && past + local + 1 < limit) limit = past + local + 1;
+        all_see = past + P.tile * A.thin_tokens + 1;
+    }
+
+    Rows<C> R;
+    clear(&R);
+    if (works) {
+        u32x4 q[C::KS];
+        load_q<T, C>(A, q, token, head, live);
+        const char* kh = A.k + kvh * A.head_stride;
+        const char* vhd = A.v + kvh * A.head_stride;
+        const char* ks = A.k + kvh * A.s_head;
+        const char* vs = A.v + kvh * A.s_head;
+        const int32_t step = STEP * A.kp;
+
+        // a lane's bytes in a row of K and of V, none past the head (such dims
+        // meet zeros of the query, or are not stored; their scales are finite)
+        int kb[KP], vb[C::NC];
+#pragma unroll
+        for (int x = 0; x < KP; ++x) {
+            kb[x] = DP == 64 ? g * 8 : x * 64 + g * 16;
+            if (kb[x] >= A.D / 2) kb[x] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+            vb[c] = (c * 16 + a) * C::VE / 2;
+            if (vb[c] >= A.D / 2) vb[c] = 0;
+        }
+        // their scales: block of 32 dims, less 4 c of chunk c or piece x
+        const int kturn = scale_turn(DP == 64 ? g >> 1 : g), vturn = scale_turn(a * C::VE / 32);
+        const int row_bytes = static_cast<int>(A.row_stride);     // TILED: small
+
+        u32x4 kr[X][KP];
+        uint32_t vr[X][4][C::NC];
+        Scales<DP> ksc, vsc;
+
+        auto page_of = [&](int32_t key0) -> int32_t { return key_page(A, P.lists, P.pg0, key0 + lane); };
+        auto offset_of = [&](int32_t key0, int32_t page) -> int64_t {
+            return page_offset(A, P.lists, P.pg0, page, key0 + lane, P.key1);
+        };
+        // the row of tile x that this lane reads, `row` of 16
+        auto row_at = [&](const char* base, int64_t off, int x, int row) -> const char* {
+            if constexpr (TILED) {
+                // the offset of the tile's first key; all of a page's rows are there
+                const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(off), x * 16);
+                const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(off >> 32), x * 16);
+                int64_t first = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+                if (first < 0) first = 0;
+                return base + first + row * row_bytes;
+            } else {
+                const int64_t o = __shfl(off, x * 16 + row);
+                return base + (o < 0 ? 0 : o);
+            }
+        };
+        auto load_keys = [&](int32_t key0, int64_t off) {
+#pragma unroll
+            for (int x = 0; x < X; ++x) {
+                const char* row = row_at(kh, off, x, a);
+#pragma unroll
+                for (int y = 0; y < KP; ++y) {
+                    if constexpr (DP == 64) {
+                        const u32x2 w = *reinterpret_cast<const u32x2*>(row + kb[y]);
+                        kr[x][y] = u32x4{w.x, w.y, 0, 0};
+                    } else {
+                        kr[x][y] = *reinterpret_cast<const u32x4*>(row + kb[y]);
+                    }
+                }
+            }
+        };
+        auto load_values = [&](int64_t off) {
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const char* row = row_at(vhd, off, x, 4 * g + i);
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c) {
+                        if constexpr (C::VE == 4) vr[x][i][c] = *reinterpret_cast<const uint16_t*>(row + vb[c]);
+                        else vr[x][i][c] = *reinterpret_cast<const uint32_t*>(row + vb[c]);
+                    }
+                }
+        };
+        // the scales of this lane's key
+        auto load_both_scales = [&](int32_t key0, int64_t off) {
+            const int64_t o = off < 0 ? A.s_base : off + scales_from(A, key0 + lane);
+            ksc = load_scales<DP>(ks + o, A.D);
+            vsc = load_scales<DP>(vs + o, A.D);
+        };
+
+        int32_t first_odd = -1;         // this wave's first step whose product left values out
+        int32_t key0 = P.key0 + part * STEP;
+        int32_t page = -1;
+        int64_t off = -1;
+        if (key0 < P.key1) {
+            off = offset_of(key0, page_of(key0));
+            page = page_of(key0 + step);
+            load_keys(key0, off);
+            load_both_scales(key0, off);
+            load_values(off);
+        }
+        for (; key0 < P.key1; key0 += step) {
+            const uint64_t valid = __ballot(off >= 0);
+            const bool more = key0 + step < P.key1;
+            f32x4 s[X];
+#pragma unroll
+            for (int x = 0; x < X; ++x) {
+                s[x] = f32x4{0, 0, 0, 0};
+                float unit[KP];
+#pragma unroll
+                for (int y = 0; y < KP; ++y) unit[y] = scale_at(__shfl(ksc.w[y], x * 16 + a), kturn);
+#pragma unroll
+                for (int k = 0; k < C::KS; ++k) {
+                    const uint32_t w = kr[x][k >> 2][k & 3];
+                    const float u = unit[k >> 2];
+                    const u32x4 f = u32x4{Mma<T>::from_fp4(w, u, 0), Mma<T>::from_fp4(w, u, 1),
+                                          Mma<T>::from_fp4(w, u, 2), Mma<T>::from_fp4(w, u, 3)};
+                    s[x] = Mma<T>::run(f, q[k], s[x]);
+                }
+            }
+            const bool partial = all_see < key0 + STEP;
+            Scales<DP> here = vsc;
+            const int64_t off_next = offset_of(key0 + step, page);
+            page = page_of(key0 + 2 * step);
+            if (more) {
+                load_keys(key0 + step, off_next);
+                load_both_scales(key0 + step, off_next);
+            }
+            if (valid != ~0ull || partial) {
+                mask_scores(&s[0], key0, limit, static_cast<uint32_t>(valid));
+                mask_scores(&s[2], key0 + 32, limit, static_cast<uint32_t>(valid >> 32));
+            }
+            u32x4 pf[X / 2];
+            float sum = take_weights<T, C, X / 2>(R, s, A.scale, pf);
+            if (too_much<T>(sum)) sum = move_maximum<T, C, X / 2>(&R, s, A.scale, pf);
+            R.l += sum;
+            // keys that are not there, and in steps with unseen keys blocks of NaN
+            // (see add_not_finite), leave the product
+            bool mine = false;
+#pragma unroll
+            for (int y = 0; y < Scales<DP>::N; ++y) {
+                if (off < 0) here.w[y] = 0;
+                if (partial && P.seg.causal) {
+                    const uint32_t w = finite_scales(here.w[y]);
+                    mine = mine || w != here.w[y];
+                    here.w[y] = w;
+                }
+            }
+            if (partial && P.seg.causal && first_odd < 0 && __any(mine)) first_odd = key0;
+#pragma unroll
+            for (int u = 0; u < X / 2; ++u)
+#pragma unroll
+                for (int c = 0; c < C::NC; ++c) {
+                    float unit[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        unit[i] = scale_at(__shfl(here.w[c], (2 * u + (i >> 2)) * 16 + 4 * g + (i & 3)), vturn);
+#pragma unroll
+                    for (int w = 0; w < C::VE / 2; ++w) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = Mma<T>::from_fp4(vr[2 * u + (i >> 2)][i & 3][c], unit[i], w);
+                        u32x4 f[2];
+                        v_transpose(y, &f[0], &f[1]);
+                        const int j = c * C::VE + 2 * w;
+                        R.o[j] = Mma<T>::run(f[0], pf[u], R.o[j]);
+                        R.o[j + 1] = Mma<T>::run(f[1], pf[u], R.o[j + 1]);
+                    }
+                }
+            if (more) load_values(off_next);
+            off = off_next;
+        }
+        if (first_odd >= 0) {
+            // the wave's own steps only: `step` apart
+            for (int32_t t = first_odd; t < P.key1; t += step)
+                add_not_finite<T, C, false>(A, P.lists, P.pg0, kvh, t,
+                                            t + STEP < P.key1 ? t + STEP : P.key1, limit, &R);
+        }
+    }
+    join_parts<C>(A, &R, lds, h, part, works);
     if (works && part == 0) store_rows<T, C, false>(A, to, R, h * kThinRows + a, token, head, live);
     if (A.kp > 1) __syncthreads();
 }
@@ -956,11 +1256,12 @@ __device__ inline u32x4 v_frag(const char* v, int at, int step, int j) {
 template <class T, class C>
 struct Stage {
     using W = Wide<C>;
-    static constexpr int NK = C::EB == 2 ? 1 : C::NK / W::WPG;            // 16-byte loads per lane
-    static constexpr int NV = C::EB == 2 ? 1 : W::VR * W::DP / 1024;
+    static constexpr int NK = C::EB != 1 ? 1 : C::NK / W::WPG;            // 16-byte loads per lane
+    static constexpr int NV = C::EB != 1 ? 1 : W::VR * W::DP / 1024;
     int64_t off;                        // the row offset of key lane % 16 of the group, or -1
     u32x4 k[NK];
     u32x4 v[NV];
+    uint32_t ks, vs;                    // 4 bits: the scale bytes of k and v
 };
 
 // The key whose offset this lane holds, and its page id.
@@ -975,7 +1276,7 @@ __device__ inline int32_t stage_page(const Args& A, const Piece& P, int32_t tile
 
 template <class T, class C>
 __device__ inline void stage_load(const Args& A, Stage<T, C>* S, const char* kh, const char* vhd,
-                                  int wave, char* buf, uint32_t* flags) {
+                                  int wave, char* buf, uint32_t* flags, int32_t tile0, int32_t kvh) {
     using W = Wide<C>;
     const int lane = here_lane(), g = lane >> 4;
     const int grp = wave / W::WPG, sub = wave % W::WPG;
@@ -1017,6 +1318,28 @@ __device__ inline void stage_load(const Args& A, Stage<T, C>* S, const char* kh,
                     *reinterpret_cast<u32x4*>(vb + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
             }
         }
+    } else if constexpr (C::FP4) {
+        constexpr int LB = W::DP == 64 ? 8 : 16;            // bytes of a lane: 16 or 32 dims
+        constexpr int LPR = W::DP / 2 / LB;                 // lanes of a V row
+        const int64_t scales = S->off + scales_from(A, stage_key<C>(tile0, wave));
+        auto load = [&](const char* head, const char* shead, int64_t off, int64_t soff, int b, u32x4* x,
+                        uint32_t* s) {
+            *x = u32x4{0, 0, 0, 0};
+            *s = 0;
+            if (off < 0 || b >= A.D / 2) return;
+            if constexpr (LB == 16) {
+                *x = *reinterpret_cast<const u32x4*>(head + off + b);
+            } else {
+                const u32x2 y = *reinterpret_cast<const u32x2*>(head + off + b);
+                *x = u32x4{y.x, y.y, 0, 0};
+            }
+            *s = *reinterpret_cast<const uint8_t*>(shead + soff + b / 16);
+        };
+        const char* ks = A.k + kvh * A.s_head;
+        const char* vs = A.v + kvh * A.s_head;
+        load(kh, ks, koff, scales, sub * 64 + g * LB, &S->k[0], &S->ks);
+        const int row = sub * W::VR + lane / LPR;
+        load(vhd, vs, __shfl(S->off, row), __shfl(scales, row), lane % LPR * LB, &S->v[0], &S->vs);
     } else {
         using St = Stage<T, C>;
         constexpr int LPR = W::DP / 16, RPP = 64 / LPR;
@@ -1043,8 +1366,30 @@ __device__ inline u32x4 widen(uint32_t lo, uint32_t hi) {
                  Mma<T>::template from_fp8<false>(hi), Mma<T>::template from_fp8<true>(hi)};
 }
 
+// 8 4-bit numbers times a power of two.
+template <class T>
+__device__ inline u32x4 widen4(uint32_t w, float unit) {
+    return u32x4{Mma<T>::from_fp4(w, unit, 0), Mma<T>::from_fp4(w, unit, 1),
+                 Mma<T>::from_fp4(w, unit, 2), Mma<T>::from_fp4(w, unit, 3)};
+}
+
 template <class T, class C>
 __device__ inline void stage_store(const Stage<T, C>& S, int wave, char* buf) {
+    if constexpr (C::FP4) {
+        using W = Wide<C>;
+        constexpr int LB = W::DP == 64 ? 8 : 16, LPR = W::DP / 2 / LB;
+        const int lane = here_lane();
+        const int grp = wave / W::WPG, sub = wave % W::WPG;
+        const float ku = __builtin_bit_cast(float, S.ks << 23), vu = __builtin_bit_cast(float, S.vs << 23);
+        char* to = buf + (grp * C::KS + sub * W::KSW) * 1024 + lane * 16;
+        const int row = sub * W::VR + lane / LPR, c = lane % LPR * (LB / 4), sw = v_swizzle<C>(row);
+        char* at = buf + W::KF * 1024 + (grp * 16 + row) * W::RB;
+#pragma unroll
+        for (int x = 0; x < LB / 4; ++x) {
+            *reinterpret_cast<u32x4*>(to + x * 1024) = widen4<T>(S.k[0][x], ku);
+            *reinterpret_cast<u32x4*>(at + (((c + x) ^ sw) * 16)) = widen4<T>(S.v[0][x], vu);
+        }
+    }
     if constexpr (C::EB == 1) {
         using W = Wide<C>;
         using St = Stage<T, C>;
@@ -1190,7 +1535,7 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
     int32_t page = stage_page<C>(A, P, P.key0, wave);
     next.off = page_offset(A, P.lists, P.pg0, page, stage_key<C>(P.key0, wave), P.key1);
     page = stage_page<C>(A, P, P.key0 + W::KT, wave);
-    stage_load<T, C>(A, &next, kh, vhd, wave, buf0, flags);
+    stage_load<T, C>(A, &next, kh, vhd, wave, buf0, flags, P.key0, kvh);
 
     WideState<T, C> S;
     const int32_t at = P.tile * A.wide_tokens, past = P.seg.keys - P.seg.ntok;
@@ -1233,7 +1578,7 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
         auto stage_next = [&]() {
             next.off = page_offset(A, P.lists, P.pg0, page, stage_key<C>(tile0 + W::KT, wave), P.key1);
             page = stage_page<C>(A, P, tile0 + 2 * W::KT, wave);
-            stage_load<T, C>(A, &next, kh, vhd, wave, there, ft);
+            stage_load<T, C>(A, &next, kh, vhd, wave, there, ft, tile0 + W::KT, kvh);
         };
         if (more && wave < kWaves / 2) stage_next();
         // where some row of the workgroup does not see some key, values that are
@@ -1261,7 +1606,7 @@ __device__ void run_wide(const Args& A, const Piece& P, const Dest& to, char* bu
     if (S.first_odd >= 0) {
 #pragma unroll
         for (int t = 0; t < W::RT; ++t)
-            add_not_finite<T, C, true>(A, P.lists, P.pg0, vhd, S.first_odd, S.most, S.limit[t], &S.R[t]);
+            add_not_finite<T, C, true>(A, P.lists, P.pg0, kvh, S.first_odd, S.most, S.limit[t], &S.R[t]);
     }
 #pragma unroll
     for (int t = 0; t < W::RT; ++t) {
@@ -1447,18 +1792,18 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
 }
 
 // LINES: 1 thin, 2 wide, 3 both.
-template <class T, bool FP8, int DP, int LINES>
+template <class T, int BITS, int DP, int LINES>
 struct Shared {
-    using C = Cfg<T, FP8, DP>;
+    using C = Cfg<T, BITS, DP>;
     static constexpr int THIN = LINES & 1 ? (kWaves / 2) * 64 * (4 * C::NJ + 2) * 4 : 16;
     static constexpr int BUF = LINES == 1 ? 16 : Wide<C>::BUF;
     static constexpr int BUF0 = BUF > THIN ? BUF : THIN;
 };
 
-template <class T, bool FP8, int DP, int LINES>
+template <class T, int BITS, int DP, int LINES>
 __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
-    using C = Cfg<T, FP8, DP>;
-    using S = Shared<T, FP8, DP, LINES>;
+    using C = Cfg<T, BITS, DP>;
+    using S = Shared<T, BITS, DP, LINES>;
     __shared__ Plan plan;
     // separate arrays: reads of one need not wait for loads on their way to the other
     __shared__ __attribute__((aligned(16))) char buf0[S::BUF0];
@@ -1552,7 +1897,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
                 if (wide_line) run_wide<T, C>(A, P, to, buf0, buf1, flags, odds);
             }
             if constexpr (LINES & 1) {
-                if (!wide_line) run_thin<T, C>(A, P, to, reinterpret_cast<float*>(buf0));
+                float* joins = reinterpret_cast<float*>(buf0);
+                if constexpr (C::FP4) {
+                    if (!wide_line && A.tiled) run_thin4<T, C, true>(A, P, to, joins);
+                    if (!wide_line && !A.tiled) run_thin4<T, C, false>(A, P, to, joins);
+                } else {
+                    if (!wide_line) run_thin<T, C>(A, P, to, joins);
+                }
             }
         }
         seg_start += cost;

@@ -1,9 +1,11 @@
-// kvx_serve_host.hpp -- host side of include/kvx_serve.h: argument checks,
-// tilings and launches.  Part of kvx.hip's translation unit, whose checks of
-// layouts, pools, batches and tables it uses.
+// kvx_serve_host.hpp -- host side of include/kvx_serve.h and kvx_read.h:
+// argument checks, tilings and launches.  Part of kvx.hip's translation unit,
+// whose checks of layouts, pools, batches and tables it uses.
 #pragma once
 
 #include "kvx_attend.hpp"
+#include "kvx_dense.hpp"
+#include "kvx_read.h"
 #include "kvx_serve.h"
 #include "kvx_tables.hpp"
 
@@ -19,6 +21,7 @@ constexpr int32_t kMaxReqs = 1 << 24;          // requests (and groups) of a bat
 constexpr int64_t kMaxQueries = 1 << 23;       // query tokens of an attention call, exclusive
 
 bool positive(float x) { return std::isfinite(x) && x > 0.0f; }
+bool far_scale(float x) { return x < 0x1p-64f || x > 0x1p64f; }
 
 // The debug checks copy tables to host vectors: a failed allocation is a
 // status, and no exception passes the C entries.
@@ -139,12 +142,14 @@ kvx_status validate_build(int32_t n, int32_t page, const int32_t* have, const in
 
 // ------------------------------------------------------------ the layer --
 
-// The planes, strides and checks that kvx_append and kvx_attend share.
+// The planes, strides and checks that kvx_append, kvx_read and kvx_attend share.
 struct LayerRef {
     Geom g;
     char* k;
     char* v;
     int64_t row_stride, page_stride, head_stride;
+    // KVX_FP4: a head's scales of a row, from s_base of the page on
+    int64_t s_base, s_row, s_head, s_bytes;
 };
 
 kvx_status check_layer(const kvx_layout* layout, int32_t layer, const kvx_pool* pool,
@@ -172,7 +177,42 @@ kvx_status check_layer(const kvx_layout* layout, int32_t layer, const kvx_pool* 
         ref->row_stride = pool->slot_stride;
         ref->head_stride = g.Db;
     }
+    ref->s_base = ref->s_row = ref->s_head = ref->s_bytes = 0;
+    if (layout->dtype == KVX_FP4) {
+        ref->s_bytes = layout->head_dim / 32;
+        if (block_layout == KVX_HND) {
+            if (!mul_ok(g.H, ref->head_stride, &ref->s_base)) return KVX_E_RANGE;
+            ref->s_row = ref->s_bytes;
+            ref->s_head = pool->page_size * ref->s_bytes;       // less than head_stride
+        } else {
+            ref->s_base = g.H * g.Db;
+            ref->s_row = ref->row_stride;
+            ref->s_head = ref->s_bytes;
+        }
+    }
     return KVX_OK;
+}
+
+// f(address, bytes) for the runs of a slot's row in a plane: the whole row, or a
+// run (and with scales another) per head.
+template <class F>
+void row_runs(const LayerRef& ref, int32_t block_layout, const kvx_pool* pool, const char* plane,
+              int64_t slot, F f) {
+    const uint64_t page = reinterpret_cast<uint64_t>(plane) +
+                          static_cast<uint64_t>(slot / pool->page_size * ref.page_stride);
+    const int64_t row = slot % pool->page_size;
+    if (block_layout != KVX_HND) {
+        const int64_t bytes = ref.g.H * (ref.g.Db + ref.s_bytes);
+        f(page + static_cast<uint64_t>(row * ref.row_stride), static_cast<uint64_t>(bytes));
+        return;
+    }
+    for (int64_t h = 0; h < ref.g.H; ++h) {
+        f(page + static_cast<uint64_t>(row * ref.row_stride + h * ref.head_stride),
+          static_cast<uint64_t>(ref.g.Db));
+        if (ref.s_bytes > 0)
+            f(page + static_cast<uint64_t>(ref.s_base + row * ref.s_row + h * ref.s_head),
+              static_cast<uint64_t>(ref.s_bytes));
+    }
 }
 
 // KVX_VALIDATE=1: no slot of the pool is written twice, and no row of k or v
@@ -193,19 +233,14 @@ kvx_status validate_append(const LayerRef& ref, int32_t block_layout, const kvx_
                      static_cast<long long>(*twice));
         return KVX_E_DUPLICATE;
     }
-    const int64_t runs = block_layout == KVX_HND ? ref.g.H : 1;     // a head-major row is a run per head
     std::vector<Span> written, read;
     for (int64_t t = 0; t < rows->num_tokens; ++t) {
         const int64_t x = at[static_cast<size_t>(t)];
         if (skipped(x)) continue;
-        const uint64_t off = static_cast<uint64_t>(x / pool->page_size * ref.page_stride +
-                                                   x % pool->page_size * ref.row_stride);
         for (const char* plane : {ref.k, ref.v})
-            for (int64_t h = 0; h < runs; ++h) {
-                const uint64_t lo = reinterpret_cast<uint64_t>(plane) + off +
-                                    static_cast<uint64_t>(h * ref.head_stride);
-                written.push_back(Span{lo, lo + static_cast<uint64_t>(ref.g.R / runs), t});
-            }
+            row_runs(ref, block_layout, pool, plane, x, [&](uint64_t lo, uint64_t bytes) {
+                written.push_back(Span{lo, lo + bytes, t});
+            });
         const uint64_t k = reinterpret_cast<uint64_t>(rows->k) + static_cast<uint64_t>(t * rows->k_stride);
         const uint64_t v = reinterpret_cast<uint64_t>(rows->v) + static_cast<uint64_t>(t * rows->v_stride);
         read.push_back(Span{k, k + static_cast<uint64_t>(row), t});
@@ -217,6 +252,106 @@ kvx_status validate_append(const LayerRef& ref, int32_t block_layout, const kvx_
         std::fprintf(stderr, "kvx: KVX_VALIDATE: append: a row is %s (token %lld); nothing enqueued\n",
                      st == KVX_E_OVERLAP ? "read and written" : "written twice",
                      static_cast<long long>(bad));
+    return st;
+}
+
+// ---------------------------------------------------------- dense rows --
+
+uint32_t magic_of(uint32_t v) {
+    return v == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + v - 1) / v);
+}
+
+// Launches a kernel of kvx_dense.hpp whose threads take `values` values each.
+kvx_status launch_dense(const char* what, const void* fn, const LayerRef& ref, const kvx_layout* layout,
+                        const kvx_pool* pool, int32_t block_layout, const int64_t* slots,
+                        const kvx_rows_out& rows, int values, unsigned long long* skipped,
+                        hipStream_t stream) {
+    namespace tb = kvx::tables;
+    const Geom& g = ref.g;
+    const bool hnd = block_layout == KVX_HND;
+    tb::DenseArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.dense[0] = static_cast<char*>(rows.k);
+    a.dense[1] = static_cast<char*>(rows.v);
+    a.dense_stride[0] = rows.k_stride;
+    a.dense_stride[1] = rows.v_stride;
+    a.pool[0] = ref.k;
+    a.pool[1] = ref.v;
+    a.slots = slots;
+    a.T = rows.num_tokens;
+    a.num_pages = pool->num_pages;
+    a.page_stride = ref.page_stride;
+    a.row_stride = ref.row_stride;
+    a.page_size = pool->page_size;
+    a.page_shift = shift_of(pool->page_size);
+    // an NHD row is one run (of its numbers, and one of its scales); an HND row is a run per head
+    a.V = static_cast<uint32_t>(static_cast<int64_t>(g.H) * layout->head_dim / values);
+    a.VH = hnd ? static_cast<uint32_t>(layout->head_dim / values) : a.V;
+    a.head_stride = hnd ? ref.head_stride : 0;
+    a.s_base = ref.s_base;
+    a.s_row = ref.s_row;
+    a.s_head = hnd ? ref.s_head : 0;
+    a.v_magic = magic_of(a.V);
+    a.vh_magic = magic_of(a.VH);
+    a.scale[0] = rows.k_scale;
+    a.scale[1] = rows.v_scale;
+    a.inverse[0] = 1.0f / rows.k_scale;
+    a.inverse[1] = 1.0f / rows.v_scale;
+    a.skipped = skipped;
+    const int64_t per = tb::kAppendThreads;
+    const int64_t grid = (rows.num_tokens * 2 * a.V + per - 1) / per;
+    if (log_enabled())
+        std::fprintf(stderr, "kvx: %s tokens=%lld row=%lld grid=%lld\n", what,
+                     static_cast<long long>(a.T), static_cast<long long>(g.R),
+                     static_cast<long long>(grid));
+    return launch_one(fn, grid, tb::kAppendThreads, a, stream);
+}
+
+template <int FROM>
+const void* append_fp4_kernel(bool scaled) {
+    return scaled ? reinterpret_cast<const void*>(&kvx::tables::k_append_fp4<FROM, true>)
+                  : reinterpret_cast<const void*>(&kvx::tables::k_append_fp4<FROM, false>);
+}
+const void* append_fp4_kernel(int32_t dtype, bool scaled) {
+    namespace tb = kvx::tables;
+    return dtype == KVX_BF16  ? append_fp4_kernel<tb::kFromBf16>(scaled)
+           : dtype == KVX_F16 ? append_fp4_kernel<tb::kFromF16>(scaled)
+                              : append_fp4_kernel<tb::kFromF32>(scaled);
+}
+
+template <int HOW>
+const void* read_kernel(int32_t dtype) {
+    namespace tb = kvx::tables;
+    return dtype == KVX_BF16  ? reinterpret_cast<const void*>(&tb::k_read<HOW, tb::kFromBf16>)
+           : dtype == KVX_F16 ? reinterpret_cast<const void*>(&tb::k_read<HOW, tb::kFromF16>)
+                              : reinterpret_cast<const void*>(&tb::k_read<HOW, tb::kFromF32>);
+}
+
+// KVX_VALIDATE=1: no row of k or v (`row` bytes) lies in a slot that is read.
+kvx_status validate_read(const LayerRef& ref, int32_t block_layout, const kvx_pool* pool,
+                         const int64_t* slots, const kvx_rows_out* rows, int64_t row,
+                         hipStream_t stream) {
+    if (hipStreamSynchronize(stream) != hipSuccess) return KVX_E_HIP;
+    std::vector<int64_t> at;
+    KVX_TRY(to_host(slots, rows->num_tokens, &at));
+    std::vector<Span> written, read;
+    for (int64_t t = 0; t < rows->num_tokens; ++t) {
+        const int64_t x = at[static_cast<size_t>(t)];
+        if (x < 0 || x / pool->page_size >= pool->num_pages) continue;
+        for (const char* plane : {ref.k, ref.v})
+            row_runs(ref, block_layout, pool, plane, x, [&](uint64_t lo, uint64_t bytes) {
+                read.push_back(Span{lo, lo + bytes, t});
+            });
+        const uint64_t k = reinterpret_cast<uint64_t>(rows->k) + static_cast<uint64_t>(t * rows->k_stride);
+        const uint64_t v = reinterpret_cast<uint64_t>(rows->v) + static_cast<uint64_t>(t * rows->v_stride);
+        written.push_back(Span{k, k + static_cast<uint64_t>(row), t});
+        written.push_back(Span{v, v + static_cast<uint64_t>(row), t});
+    }
+    int64_t bad = 0;
+    const kvx_status st = spans_disjoint(&written, &read, &bad);
+    if (st != KVX_OK)
+        std::fprintf(stderr, "kvx: KVX_VALIDATE: read: a row is read and written (token %lld); nothing "
+                             "enqueued\n", static_cast<long long>(bad));
     return st;
 }
 
@@ -264,7 +399,7 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     s->DP = D <= 64 ? 64 : (D <= 128 ? 128 : 256);
     s->G = q_heads / g.H;
     const int64_t rows = tokens * s->G;
-    const bool all_wide = s->DP > 128 && layout->dtype != KVX_FP8;
+    const bool all_wide = s->DP > 128 && layout->dtype != KVX_FP8 && layout->dtype != KVX_FP4;
     s->own_wide = num_reqs > 0 && (all_wide || rows / num_reqs >= kWideRows);
     s->pre_wide = num_groups > 0 && (all_wide || rows / num_groups >= kWideRows);
     s->wide_rows = s->DP <= 128 ? 256 : 128;
@@ -297,24 +432,32 @@ struct AttendKernels {
     const void *main, *join, *join_shared, *join_items;
 };
 
-template <class T, bool FP8, int DP>
+// BITS: of a pool's values.
+template <class T, int BITS, int DP>
 AttendKernels attend_kernels(int lines) {
     const void* main;
-    if constexpr (DP > 128 && !FP8)
-        main = reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 2>);
+    if constexpr (DP > 128 && BITS == 16)
+        main = reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 2>);
     else
-        main = lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 1>)
-                          : reinterpret_cast<const void*>(&at::k_attend<T, FP8, DP, 3>);
+        main = lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 1>)
+                          : reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 3>);
     return {main, reinterpret_cast<const void*>(&at::k_attend_join<T, DP, false>),
             reinterpret_cast<const void*>(&at::k_attend_join<T, DP, true>),
             reinterpret_cast<const void*>(&at::k_attend_join_items<T, DP>)};
 }
 
-template <class T, bool FP8>
+template <class T, int BITS>
 AttendKernels attend_kernels(int DP, int lines) {
-    return DP == 64    ? attend_kernels<T, FP8, 64>(lines)
-           : DP == 128 ? attend_kernels<T, FP8, 128>(lines)
-                       : attend_kernels<T, FP8, 256>(lines);
+    return DP == 64    ? attend_kernels<T, BITS, 64>(lines)
+           : DP == 128 ? attend_kernels<T, BITS, 128>(lines)
+                       : attend_kernels<T, BITS, 256>(lines);
+}
+
+template <class T>
+AttendKernels attend_kernels(int32_t pool_dtype, int DP, int lines) {
+    return pool_dtype == KVX_FP4   ? attend_kernels<T, 4>(DP, lines)
+           : pool_dtype == KVX_FP8 ? attend_kernels<T, 8>(DP, lines)
+                                   : attend_kernels<T, 16>(DP, lines);
 }
 
 // n rows of `len` bytes, `stride` apart.
@@ -434,17 +577,18 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     KVX_TRY(check_layer(layout, layer, pool, block_layout, &ref));
     const Geom& g = ref.g;
     if (rows == nullptr) return KVX_E_NULL;
+    if (rows->dtype == KVX_FP4) return KVX_E_UNSUPPORTED;
     const int eb = elem_bytes(rows->dtype);
     if (eb == 0) return KVX_E_DTYPE;
     if (rows->num_tokens < 0) return KVX_E_SHAPE;
     if (rows->num_tokens >= (int64_t(1) << 31)) return KVX_E_RANGE;
-    const bool copies = rows->dtype == layout->dtype;
-    if (!copies && layout->dtype != KVX_FP8) return KVX_E_UNSUPPORTED;
+    const bool copies = rows->dtype == layout->dtype, fp4 = layout->dtype == KVX_FP4;
+    if (!copies && layout->dtype != KVX_FP8 && !fp4) return KVX_E_UNSUPPORTED;
+    if (fp4 && rows->dtype == KVX_FP8) return KVX_E_UNSUPPORTED;
     if (!positive(rows->k_scale) || !positive(rows->v_scale)) return KVX_E_SHAPE;
     // inside these the kernel's quotients by a rounded inverse are exact: no
-    // remainder of a value that e4m3 holds underflows
-    auto far = [](float x) { return x < 0x1p-64f || x > 0x1p64f; };
-    if (far(rows->k_scale) || far(rows->v_scale)) return KVX_E_RANGE;
+    // remainder of a value that e4m3 or a 4-bit block holds underflows
+    if (far_scale(rows->k_scale) || far_scale(rows->v_scale)) return KVX_E_RANGE;
     if (copies && (rows->k_scale != 1.0f || rows->v_scale != 1.0f)) return KVX_E_UNSUPPORTED;
     if (rows->num_tokens == 0) return KVX_OK;
     if (rows->k == nullptr || rows->v == nullptr || slots == nullptr) return KVX_E_NULL;
@@ -460,6 +604,13 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
         KVX_TRY(no_throw([&] {
             return validate_append(ref, block_layout, pool, slots, rows, row, stream);
         }));
+    if (fp4) {
+        const kvx_rows_out out{const_cast<void*>(rows->k), const_cast<void*>(rows->v), rows->k_stride,
+                               rows->v_stride, rows->num_tokens, rows->dtype, rows->k_scale, rows->v_scale};
+        const bool scaled = rows->k_scale != 1.0f || rows->v_scale != 1.0f;
+        return launch_dense("append", append_fp4_kernel(rows->dtype, scaled), ref, layout, pool,
+                            block_layout, slots, out, 8, skipped, stream);
+    }
     tb::AppendArgs a;
     std::memset(&a, 0, sizeof(a));
     a.src[0] = static_cast<const char*>(rows->k);
@@ -479,11 +630,8 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     // an NHD row is one run; an HND row is a run per head
     a.VH = block_layout == KVX_HND ? static_cast<uint32_t>(g.Db / 16) : a.V;
     a.head_stride = block_layout == KVX_HND ? ref.head_stride : 0;
-    auto magic = [](uint32_t v) {
-        return v == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + v - 1) / v);
-    };
-    a.v_magic = magic(a.V);
-    a.vh_magic = magic(a.VH);
+    a.v_magic = magic_of(a.V);
+    a.vh_magic = magic_of(a.VH);
     a.scale[0] = rows->k_scale;
     a.scale[1] = rows->v_scale;
     a.inverse[0] = 1.0f / rows->k_scale;
@@ -501,6 +649,48 @@ kvx_status kvx_append(const kvx_layout* layout, int32_t layer, const kvx_pool* p
                      static_cast<long long>(a.T), static_cast<long long>(g.R),
                      static_cast<long long>(grid));
     return launch_one(fn, grid, tb::kAppendThreads, a, stream);
+}
+
+kvx_status kvx_read(const kvx_layout* layout, int32_t layer, const kvx_pool* pool,
+                    int32_t block_layout, const int64_t* slots, const kvx_rows_out* rows,
+                    unsigned long long* skipped, hipStream_t stream) {
+    namespace tb = kvx::tables;
+    LayerRef ref;
+    KVX_TRY(check_layer(layout, layer, pool, block_layout, &ref));
+    if (rows == nullptr) return KVX_E_NULL;
+    if (rows->dtype == KVX_FP4) return KVX_E_UNSUPPORTED;
+    const int eb = elem_bytes(rows->dtype);
+    if (eb == 0) return KVX_E_DTYPE;
+    if (rows->num_tokens < 0) return KVX_E_SHAPE;
+    if (rows->num_tokens >= (int64_t(1) << 31)) return KVX_E_RANGE;
+    const bool copies = rows->dtype == layout->dtype;
+    if (!copies && ((layout->dtype != KVX_FP8 && layout->dtype != KVX_FP4) || rows->dtype == KVX_FP8))
+        return KVX_E_UNSUPPORTED;
+    if (!positive(rows->k_scale) || !positive(rows->v_scale)) return KVX_E_SHAPE;
+    if (far_scale(rows->k_scale) || far_scale(rows->v_scale)) return KVX_E_RANGE;
+    if (copies && (rows->k_scale != 1.0f || rows->v_scale != 1.0f)) return KVX_E_UNSUPPORTED;
+    if (rows->num_tokens == 0) return KVX_OK;
+    if (rows->k == nullptr || rows->v == nullptr || slots == nullptr) return KVX_E_NULL;
+    const int64_t row = static_cast<int64_t>(layout->kv_heads) * layout->head_dim * eb;
+    if (rows->k_stride < row || rows->v_stride < row) return KVX_E_SHAPE;
+    if (!aligned16(rows->k) || !aligned16(rows->v) || rows->k_stride % 16 != 0 ||
+        rows->v_stride % 16 != 0)
+        return KVX_E_ALIGN;
+    int64_t span = 0;
+    if (!mul_ok(rows->num_tokens, std::max(rows->k_stride, rows->v_stride), &span))
+        return KVX_E_RANGE;
+    const int64_t T = rows->num_tokens;
+    if (rows_meet({rows->k, rows->k_stride, row, T}, {rows->v, rows->v_stride, row, T}))
+        return KVX_E_OVERLAP;
+    if (validate_enabled())
+        KVX_TRY(no_throw([&] {
+            return validate_read(ref, block_layout, pool, slots, rows, row, stream);
+        }));
+    const void* fn = copies ? reinterpret_cast<const void*>(&tb::k_read<tb::kReadBytes, tb::kFromBf16>)
+                     : layout->dtype == KVX_FP8 ? read_kernel<tb::kReadFp8>(rows->dtype)
+                                                : read_kernel<tb::kReadFp4>(rows->dtype);
+    return launch_dense("read", fn, ref, layout, pool, block_layout, slots, *rows, copies ? 16 / eb : 8,
+                        skipped, stream);
 }
 
 kvx_status kvx_attend_workspace(const kvx_layout* layout, int32_t num_reqs, int32_t num_groups,
@@ -528,7 +718,8 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     if ((x.flags & ~KVX_ATTEND_CAUSAL) != 0) return KVX_E_UNSUPPORTED;
     if (x.dtype != KVX_F16 && x.dtype != KVX_BF16)
         return elem_bytes(x.dtype) == 0 ? KVX_E_DTYPE : KVX_E_UNSUPPORTED;
-    if (layout->dtype != x.dtype && layout->dtype != KVX_FP8) return KVX_E_UNSUPPORTED;
+    const bool fp4 = layout->dtype == KVX_FP4;
+    if (layout->dtype != x.dtype && layout->dtype != KVX_FP8 && !fp4) return KVX_E_UNSUPPORTED;
     const int32_t ng = prefix != nullptr ? prefix->num_groups : 0;
     AttendShape s;
     KVX_TRY(attend_shape(layout, g, reqs->num_reqs, ng, reqs->total_tokens, x.q_heads, &s));
@@ -573,9 +764,14 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.row_stride = ref.row_stride;
     a.page_stride = ref.page_stride;
     a.head_stride = ref.head_stride;
+    a.s_base = ref.s_base;
+    a.s_row = ref.s_row;
+    a.s_head = ref.s_head;
     a.num_pages = pool->num_pages;
     a.page_size = pool->page_size;
     a.page_shift = shift_of(pool->page_size);
+    // 16 rows of a tile in one page, their offsets from its first in 32 bits
+    a.tiled = fp4 && pool->page_size % 16 == 0 && ref.row_stride <= (1 << 26);
     a.tok_off = reqs->tok_off;
     a.ctx = ctx_len;
     a.own = at::Lists{table->pg_off, table->page_ids, table->num_ids};
@@ -627,7 +823,7 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     // a compute unit's time for a wide key (its products, 2350 a ns) over that
     // for a thin key (its bytes, 26 a ns): rates of the two loops alone
     const double wide_ns = 4.0 * s.wide_rows * s.DP / 2350.0;
-    const double thin_ns = 2.0 * a.hs * g.Db / a.parts / 26.0;
+    const double thin_ns = 2.0 * a.hs * static_cast<double>(g.Db + ref.s_bytes) / a.parts / 26.0;
     a.wide_weight = static_cast<float>(wide_ns / thin_ns);
     char* ws = static_cast<char*>(x.workspace);
     a.placed = reinterpret_cast<at::Placed*>(ws + s.placed);
@@ -640,12 +836,8 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.slot_rows = s.slot_rows;
 
     const int lines = s.own_wide || s.pre_wide ? 3 : 1;
-    const bool fp8 = layout->dtype == KVX_FP8;
-    const AttendKernels k = x.dtype == KVX_BF16
-                                ? (fp8 ? attend_kernels<__bf16, true>(s.DP, lines)
-                                       : attend_kernels<__bf16, false>(s.DP, lines))
-                                : (fp8 ? attend_kernels<_Float16, true>(s.DP, lines)
-                                       : attend_kernels<_Float16, false>(s.DP, lines));
+    const AttendKernels k = x.dtype == KVX_BF16 ? attend_kernels<__bf16>(layout->dtype, s.DP, lines)
+                                                : attend_kernels<_Float16>(layout->dtype, s.DP, lines);
     if (log_enabled())
         std::fprintf(stderr,
                      "kvx: attend reqs=%d groups=%d tokens=%lld heads=%d/%d dim=%d prefix=%s own=%s\n",
