@@ -81,6 +81,8 @@ constexpr int kWaves = 8;               // waves of an attention workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kKeys = 32;               // keys of one step of a wave
 constexpr int kThinRows = 16;
+constexpr int kTiles4 = 2;               // 16-key tiles of a thin step over 4-bit pools
+constexpr int kWaves4 = 2;               // waves of a SIMD where all tiles are such
 constexpr int32_t kMaxKeys = 1 << 30;    // of a context or a prefix: step indices stay in 32 bits
 constexpr int kJoinWaves = 8;
 constexpr int kJoinParts = 4;
@@ -139,7 +141,6 @@ struct Args {
     int64_t num_pages;
     int32_t page_size;
     int32_t page_shift;                 // log2(page_size), or -1
-    int32_t tiled;                      // 4 bits: a tile of 16 keys lies in one page
     const int64_t* tok_off;             // [num_reqs + 1]
     const int32_t* ctx;                 // [num_reqs]
     const int64_t* grp_off;             // [num_groups + 1]
@@ -929,26 +930,65 @@ __device__ void run_thin(const Args& A, const Piece& P, const Dest& to, float* l
     if (A.kp > 1) __syncthreads();
 }
 
-// ------------------------------------------------- thin, 4-bit pools --
-//
-// A step is 64 keys: 4 tiles of 16.  A lane (a, g) holds of K 16-byte pieces of
-// key a, one scale's 32 dims each (8 bytes below 128 dims), so that a piece
-// makes the operands of four products under one scale; of V the numbers of 8
-// dims (4 below 128 dims) of key 4 g + i, whose scale reaches it by a shuffle:
-// lane l loads the scales of key l.  Conversions multiply by the scale, and every
-// held value is exact in 16 bits, so nothing but the weights is rounded.
-//
-// TILED: a tile's keys lie in one page, whose offset is then in scalar
-// registers and each lane's own part is the same for all tiles.
+typedef __attribute__((address_space(3))) char lds_char;
 
-// Scale b of a lane's word(s) as a power of two: the conversions look at a
-// float's exponent alone, so the byte is rotated to it and the rest left there.
-__device__ inline int scale_turn(int b) { return (8 * (b & 3) + 9) & 31; }
-__device__ inline float scale_at(uint32_t w, int turn) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_alignbit(w, w, turn) & 0x7f800000u);
+// 16 bytes per lane from memory to base + 16 * lane of shared memory.
+__device__ inline void load_to_lds(const char* src, char* base) {
+    __builtin_amdgcn_global_load_lds(
+        (const __attribute__((address_space(1))) uint32_t*)src,
+        (__attribute__((address_space(3))) uint32_t*)base, 16, 0, 0);
 }
 
-// The scales of a row's head, D / 32 bytes; none past them.
+// ------------------------------------------------- thin, 4-bit pools --
+//
+// A step is X tiles of 16 keys.  A lane (a, g) holds of K 16-byte pieces of key
+// a, one scale's 32 dims each (8 bytes below 128 dims), so that a piece makes the
+// operands of four products under one scale; of V the numbers of 8 dims (4 below
+// 128 dims) of key 4 g + i, i < 4, and the scales of key 4 g + a % 4, which its row
+// of 16 lanes has from there by broadcasts without shared memory.  Conversions
+// multiply by the scale, and every held value is exact in 16 bits, so nothing but
+// the weights is rounded.
+//
+// TILED: pages are powers of two and a tile's keys lie in one.  A register holds the pages of the next
+// 64 tiles, one a lane; a tile's addresses are scalar and each lane's own part is
+// the same for all tiles.  Otherwise lane (a, g) looks up key 16 (a / 4 % X) + 4 g +
+// a % 4 of a step, and the offsets move between lanes.
+
+// x of lane n of the lane's 16 (n constant where it is inlined).
+template <int n>
+__device__ inline uint32_t of_row(uint32_t x) {
+    return __builtin_amdgcn_mov_dpp(x, 0x150 + n, 0xf, 0xf, true);
+}
+__device__ inline uint32_t of_row(uint32_t x, int n) {
+    switch (n) {
+        case 0: return of_row<0>(x);
+        case 1: return of_row<1>(x);
+        case 2: return of_row<2>(x);
+        case 3: return of_row<3>(x);
+        case 4: return of_row<4>(x);
+        case 5: return of_row<5>(x);
+        case 6: return of_row<6>(x);
+        case 7: return of_row<7>(x);
+        case 8: return of_row<8>(x);
+        case 9: return of_row<9>(x);
+        case 10: return of_row<10>(x);
+        case 11: return of_row<11>(x);
+        case 12: return of_row<12>(x);
+        case 13: return of_row<13>(x);
+        case 14: return of_row<14>(x);
+        default: return of_row<15>(x);
+    }
+}
+
+// Scale b of a word as a power of two: the conversions look at a float's exponent
+// alone, so the byte is rotated there and the rest left where it falls.
+__device__ inline int scale_turn(int b) { return (8 * (b & 3) + 9) & 31; }
+__device__ inline float scale_at(uint32_t w, int turn) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_alignbit(w, w, turn));
+}
+
+// The scales of a row's head, D / 32 bytes at p, and zeros behind them.  What a
+// word holds more is read from before p, where the page's numbers end.
 template <int DP>
 struct Scales {
     static constexpr int N = DP > 128 ? 2 : 1;
@@ -956,23 +996,19 @@ struct Scales {
 };
 
 template <int DP>
-__device__ inline Scales<DP> load_scales(const char* p, int D) {
+__device__ inline Scales<DP> load_scales(const char* p, uint32_t off, int pad) {
+    struct __attribute__((packed)) U2 { uint16_t x; };
+    struct __attribute__((packed)) U4 { uint32_t x; };
+    struct __attribute__((packed)) U8 { uint64_t x; };
+    const char* at = p - pad + off;
     Scales<DP> s;
-    if (D == DP) {
-        if constexpr (DP == 64) s.w[0] = *reinterpret_cast<const uint16_t*>(p);
-        if constexpr (DP == 128) s.w[0] = *reinterpret_cast<const uint32_t*>(p);
-        if constexpr (DP == 256) {
-            const u32x2 x = *reinterpret_cast<const u32x2*>(p);
-            s.w[0] = x.x;
-            s.w[1] = x.y;
-        }
-        return s;
+    if constexpr (DP == 64) s.w[0] = reinterpret_cast<const U2*>(at)->x >> (8 * pad);
+    if constexpr (DP == 128) s.w[0] = reinterpret_cast<const U4*>(at)->x >> (8 * pad);
+    if constexpr (DP == 256) {
+        const uint64_t x = reinterpret_cast<const U8*>(at)->x >> (8 * pad);
+        s.w[0] = static_cast<uint32_t>(x);
+        s.w[1] = static_cast<uint32_t>(x >> 32);
     }
-#pragma unroll
-    for (int i = 0; i < Scales<DP>::N; ++i) s.w[i] = 0;
-#pragma unroll
-    for (int b = 0; b < DP / 32; ++b)
-        if (b * 32 < D) s.w[b / 4] |= static_cast<uint32_t>(*reinterpret_cast<const uint8_t*>(p + b)) << (b % 4 * 8);
     return s;
 }
 
@@ -982,199 +1018,313 @@ __device__ inline uint32_t finite_scales(uint32_t w) {
     return w & ~((nan >> 7) * 0xffu);
 }
 
-template <class T, class C, bool TILED>
-__device__ void run_thin4(const Args& A, const Piece& P, const Dest& to, float* lds) {
-    constexpr int DP = C::KS * 32, X = 4, STEP = 16 * X;
-    constexpr int KP = DP > 128 ? 2 : 1;                  // pieces of K a lane holds of a key
-    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int h = wave % A.hs, part = wave / A.hs;
-    const int32_t vh = P.set * A.hs + h;                  // thin head
-    const int32_t kvh = vh / A.parts, sub = vh % A.parts;
-    const bool works = part < A.kp && vh < A.H * A.parts;
-    count_skipped(A, P, wave);
+// K and V of a step as loaded, or read from shared memory: scale bytes of K's
+// pieces, and V's scales as powers of two.
+template <class C>
+struct Step4 {
+    static constexpr int X = kTiles4;
+    static constexpr int KP = C::KS > 4 ? 2 : 1;          // pieces of K a lane holds of a key
+    u32x4 k[X][KP];
+    uint32_t ks[X][KP];
+    uint32_t v[X][4][C::NC];
+};
 
-    // this lane's query row
+template <class T, class C>
+__device__ inline void scores4(const Step4<C>& S, const u32x4 (&q)[C::KS], f32x4* s) {
+#pragma unroll
+    for (int x = 0; x < S.X; ++x) {
+        s[x] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < C::KS; ++k) {
+            const uint32_t w = S.k[x][k >> 2][k & 3];
+            const float u = __builtin_bit_cast(float, S.ks[x][k >> 2] << 23);
+            const u32x4 f = u32x4{Mma<T>::from_fp4(w, u, 0), Mma<T>::from_fp4(w, u, 1),
+                                  Mma<T>::from_fp4(w, u, 2), Mma<T>::from_fp4(w, u, 3)};
+            s[x] = Mma<T>::run(f, q[k], s[x]);
+        }
+    }
+}
+
+// The second product, unit(x, i, c) the scale of chunk c of key 16 x + 4 g + i.
+template <class T, class C, class F>
+__device__ inline void values4(const Step4<C>& S, const u32x4* pf, F unit, Rows<C>* R) {
+#pragma unroll
+    for (int u = 0; u < S.X / 2; ++u)
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+            float f8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f8[i] = unit(2 * u + (i >> 2), i & 3, c);
+#pragma unroll
+            for (int w = 0; w < C::VE / 2; ++w) {
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[i] = Mma<T>::from_fp4(S.v[2 * u + (i >> 2)][i & 3][c], f8[i], w);
+                u32x4 f[2];
+                v_transpose(y, &f[0], &f[1]);
+                const int j = c * C::VE + 2 * w;
+                R->o[j] = Mma<T>::run(f[0], pf[u], R->o[j]);
+                R->o[j + 1] = Mma<T>::run(f[1], pf[u], R->o[j + 1]);
+            }
+        }
+}
+
+// A lane's query row of a thin tile, and what it sees.
+struct ThinRow {
+    int32_t token, head;
+    int32_t limit, all_see;             // keys that this row sees, and the fewest that a row of the tile sees
+    int32_t kvh;
+    int h, part;
+    bool works, live;
+};
+
+__device__ inline ThinRow thin_row(const Args& A, const Piece& P, int wave) {
+    const int a = here_lane() & 15;
+    ThinRow r;
+    r.h = wave % A.hs;
+    r.part = wave / A.hs;
+    const int32_t vh = P.set * A.hs + r.h;                // thin head
+    r.kvh = vh / A.parts;
+    const int32_t sub = vh % A.parts;
+    r.works = r.part < A.kp && vh < A.H * A.parts;
     const int32_t local = P.tile * A.thin_tokens + a / A.gv;
     const int32_t hsub = sub * A.gv + a % A.gv;
-    const bool live = works && a < A.thin_tokens * A.gv && local < P.seg.ntok && hsub < A.G;
-    const int32_t token = P.seg.tok0 + local;
-    const int32_t head = kvh * A.G + hsub;
+    r.live = r.works && a < A.thin_tokens * A.gv && local < P.seg.ntok && hsub < A.G;
+    r.token = P.seg.tok0 + local;
+    r.head = r.kvh * A.G + hsub;
     const int32_t past = P.seg.keys - P.seg.ntok;
-    // keys that this row sees, and the fewest that a row of the tile sees
-    int32_t limit = P.key1, all_see = P.key1;
+    r.limit = r.all_see = P.key1;
     if (P.seg.causal) {
-        if (live && past + local + 1 < limit) limit = past + local + 1;
-        all_see = past + P.tile * A.thin_tokens + 1;
+        if (r.live && past + local + 1 < r.limit) r.limit = past + local + 1;
+        r.all_see = past + P.tile * A.thin_tokens + 1;
     }
+    return r;
+}
+
+template <class T, class C, bool TILED>
+__device__ void run_thin4(const Args& A, const Piece& P, const Dest& to, float* lds) {
+    constexpr int DP = C::KS * 32, X = kTiles4, STEP = 16 * X, KP = Step4<C>::KP;
+    constexpr uint32_t ALL = (1u << X) - 1;
+    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const ThinRow row = thin_row(A, P, wave);
+    const int32_t kvh = row.kvh, limit = row.limit, part = row.part;
+    count_skipped(A, P, wave);
 
     Rows<C> R;
     clear(&R);
-    if (works) {
+    if (row.works) {
         u32x4 q[C::KS];
-        load_q<T, C>(A, q, token, head, live);
+        load_q<T, C>(A, q, row.token, row.head, row.live);
         const char* kh = A.k + kvh * A.head_stride;
         const char* vhd = A.v + kvh * A.head_stride;
-        const char* ks = A.k + kvh * A.s_head;
-        const char* vs = A.v + kvh * A.s_head;
+        const char* ks = A.k + A.s_base + kvh * A.s_head;
+        const char* vs = A.v + A.s_base + kvh * A.s_head;
         const int32_t step = STEP * A.kp;
+        const int pad = DP / 32 - A.D / 32;
 
         // a lane's bytes in a row of K and of V, none past the head (such dims
         // meet zeros of the query, or are not stored; their scales are finite)
-        int kb[KP], vb[C::NC];
+        uint32_t kb[KP], vb[C::NC];
 #pragma unroll
         for (int x = 0; x < KP; ++x) {
             kb[x] = DP == 64 ? g * 8 : x * 64 + g * 16;
-            if (kb[x] >= A.D / 2) kb[x] = 0;
+            if (kb[x] >= static_cast<uint32_t>(A.D) / 2) kb[x] = 0;
         }
 #pragma unroll
         for (int c = 0; c < C::NC; ++c) {
             vb[c] = (c * 16 + a) * C::VE / 2;
-            if (vb[c] >= A.D / 2) vb[c] = 0;
+            if (vb[c] >= static_cast<uint32_t>(A.D) / 2) vb[c] = 0;
         }
-        // their scales: block of 32 dims, less 4 c of chunk c or piece x
-        const int kturn = scale_turn(DP == 64 ? g >> 1 : g), vturn = scale_turn(a * C::VE / 32);
-        const int row_bytes = static_cast<int>(A.row_stride);     // TILED: small
+        // V's scales: block of 32 dims, less 4 c of chunk c
+        const int vturn = scale_turn(a * C::VE / 32);
 
-        u32x4 kr[X][KP];
-        uint32_t vr[X][4][C::NC];
-        Scales<DP> ksc, vsc;
-
-        auto page_of = [&](int32_t key0) -> int32_t { return key_page(A, P.lists, P.pg0, key0 + lane); };
-        auto offset_of = [&](int32_t key0, int32_t page) -> int64_t {
-            return page_offset(A, P.lists, P.pg0, page, key0 + lane, P.key1);
-        };
-        // the row of tile x that this lane reads, `row` of 16
-        auto row_at = [&](const char* base, int64_t off, int x, int row) -> const char* {
-            if constexpr (TILED) {
-                // the offset of the tile's first key; all of a page's rows are there
-                const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(off), x * 16);
-                const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(off >> 32), x * 16);
-                int64_t first = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
-                if (first < 0) first = 0;
-                return base + first + row * row_bytes;
+        Step4<C> S;
+        Scales<DP> vsc[X];
+        auto load_k_piece = [&](int x, int y, const char* p, uint32_t off) {
+            if constexpr (DP == 64) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(p + off);
+                S.k[x][y] = u32x4{w.x, w.y, 0, 0};
             } else {
-                const int64_t o = __shfl(off, x * 16 + row);
-                return base + (o < 0 ? 0 : o);
+                S.k[x][y] = *reinterpret_cast<const u32x4*>(p + off);
             }
         };
-        auto load_keys = [&](int32_t key0, int64_t off) {
+        auto load_v_piece = [&](int x, int i, int c, const char* p, uint32_t off) {
+            if constexpr (C::VE == 4) S.v[x][i][c] = *reinterpret_cast<const uint16_t*>(p + off);
+            else S.v[x][i][c] = *reinterpret_cast<const uint32_t*>(p + off);
+        };
+
+        int32_t key0 = P.key0 + part * STEP;
+        // TILED: the pages of 64 / X steps (-1: none), those of the next ones as
+        // loaded, the present step of them, and its first key.
+        constexpr int SPAN = 64 / X;
+        int32_t pages = -1, ahead = -1, at = 0, from = key0;
+        auto tile_key = [&](int32_t first) { return first + lane / X * step + lane % X * 16; };
+        auto look = [&](int32_t first) { return key_page(A, P.lists, P.pg0, tile_key(first)); };
+        auto checked = [&](int32_t first, int32_t page) {
+            return page_offset(A, P.lists, P.pg0, page, tile_key(first), P.key1) < 0 ? -1 : page;
+        };
+        uint32_t kof[KP], ksof[KP], vof[C::NC], vsof = 0;
+        // otherwise: the offset of the key that this lane looks up, and a later one's page
+        int64_t off = -1;
+        int32_t page = -1;
+        const int mine = 16 * ((a >> 2) % X) + 4 * g + (a & 3);
+        auto page_of = [&](int32_t k0) { return key_page(A, P.lists, P.pg0, k0 + mine); };
+        auto offset_of = [&](int32_t k0, int32_t p) {
+            return page_offset(A, P.lists, P.pg0, p, k0 + mine, P.key1);
+        };
+        auto of_key = [&](int64_t o, int x, int key) {       // of the lane that looks up `key` of tile x
+            return __shfl(o, 16 * (key >> 2) + 4 * x + (key & 3));
+        };
+        if constexpr (TILED) {
+            const uint32_t rb = static_cast<uint32_t>(A.row_stride), sb = static_cast<uint32_t>(A.s_row);
+#pragma unroll
+            for (int y = 0; y < KP; ++y) {
+                kof[y] = a * rb + kb[y];
+                ksof[y] = a * sb + kb[y] / 16;
+            }
+#pragma unroll
+            for (int c = 0; c < C::NC; ++c) vof[c] = 4 * g * rb + vb[c];
+            vsof = (4 * g + (a & 3)) * sb;
+        }
+        // offsets of a tile's page and row, uniform
+        auto tile_at = [&](int32_t key, int32_t id, int64_t* scales) {
+            const uint32_t r = static_cast<uint32_t>(key) & (static_cast<uint32_t>(A.page_size) - 1);
+            const uint64_t p = static_cast<uint64_t>(static_cast<uint32_t>(id < 0 ? 0 : id)) *
+                               static_cast<uint32_t>(A.page_stride);
+            *scales = static_cast<int64_t>(p + r * static_cast<uint32_t>(A.s_row));
+            return static_cast<int64_t>(p + r * static_cast<uint32_t>(A.row_stride));
+        };
+        // the step at k0: tiles that are there, as bits (TILED; all others are seen to by key)
+        auto load_keys = [&](int32_t k0) -> uint32_t {
+            uint32_t there = ALL;
+            if constexpr (TILED) {
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+                    const int32_t id = __builtin_amdgcn_readlane(pages, at * X + x);
+                    if (id < 0) there &= ~(1u << x);
+                    int64_t so;
+                    const int64_t o = tile_at(k0 + 16 * x, id, &so);
+#pragma unroll
+                    for (int y = 0; y < KP; ++y) {
+                        load_k_piece(x, y, kh + o, kof[y]);
+                        S.ks[x][y] = *reinterpret_cast<const uint8_t*>(ks + so + ksof[y]);
+                    }
+                    vsc[x] = load_scales<DP>(vs + so, vsof, pad);
+                }
+            } else {
+                const int64_t so = off < 0 ? 0 : off + scales_from(A, k0 + mine) - A.s_base;
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+                    const int64_t o = of_key(off, x, a), s = of_key(so, x, a);
+#pragma unroll
+                    for (int y = 0; y < KP; ++y) {
+                        load_k_piece(x, y, kh + (o < 0 ? 0 : o), kb[y]);
+                        S.ks[x][y] = *reinterpret_cast<const uint8_t*>(ks + s + kb[y] / 16);
+                    }
+                    vsc[x] = load_scales<DP>(vs + of_key(so, x, 4 * g + (a & 3)), 0, pad);
+                }
+            }
+            return there;
+        };
+        auto load_values = [&](int32_t k0) {
 #pragma unroll
             for (int x = 0; x < X; ++x) {
-                const char* row = row_at(kh, off, x, a);
-#pragma unroll
-                for (int y = 0; y < KP; ++y) {
-                    if constexpr (DP == 64) {
-                        const u32x2 w = *reinterpret_cast<const u32x2*>(row + kb[y]);
-                        kr[x][y] = u32x4{w.x, w.y, 0, 0};
-                    } else {
-                        kr[x][y] = *reinterpret_cast<const u32x4*>(row + kb[y]);
-                    }
-                }
-            }
-        };
-        auto load_values = [&](int64_t off) {
-#pragma unroll
-            for (int x = 0; x < X; ++x)
+                int64_t o = 0, so;
+                if constexpr (TILED) o = tile_at(k0 + 16 * x, __builtin_amdgcn_readlane(pages, at * X + x), &so);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const char* row = row_at(vhd, off, x, 4 * g + i);
-#pragma unroll
-                    for (int c = 0; c < C::NC; ++c) {
-                        if constexpr (C::VE == 4) vr[x][i][c] = *reinterpret_cast<const uint16_t*>(row + vb[c]);
-                        else vr[x][i][c] = *reinterpret_cast<const uint32_t*>(row + vb[c]);
+                    const char* p;
+                    if constexpr (TILED) {
+                        p = vhd + o + i * static_cast<uint32_t>(A.row_stride);
+                    } else {
+                        const uint32_t lo = of_row(static_cast<uint32_t>(off), 4 * x + i);
+                        const uint32_t hi = of_row(static_cast<uint32_t>(off >> 32), 4 * x + i);
+                        o = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+                        p = vhd + (o < 0 ? 0 : o);
                     }
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c) load_v_piece(x, i, c, p, TILED ? vof[c] : vb[c]);
                 }
-        };
-        // the scales of this lane's key
-        auto load_both_scales = [&](int32_t key0, int64_t off) {
-            const int64_t o = off < 0 ? A.s_base : off + scales_from(A, key0 + lane);
-            ksc = load_scales<DP>(ks + o, A.D);
-            vsc = load_scales<DP>(vs + o, A.D);
+            }
         };
 
         int32_t first_odd = -1;         // this wave's first step whose product left values out
-        int32_t key0 = P.key0 + part * STEP;
-        int32_t page = -1;
-        int64_t off = -1;
+        uint32_t there = ALL, there_next = ALL;
         if (key0 < P.key1) {
-            off = offset_of(key0, page_of(key0));
-            page = page_of(key0 + step);
-            load_keys(key0, off);
-            load_both_scales(key0, off);
-            load_values(off);
+            if constexpr (TILED) {
+                pages = checked(from, look(from));
+                ahead = look(from + SPAN * step);
+            } else {
+                off = offset_of(key0, page_of(key0));
+                page = page_of(key0 + step);
+            }
+            there = load_keys(key0);
+            load_values(key0);
         }
         for (; key0 < P.key1; key0 += step) {
-            const uint64_t valid = __ballot(off >= 0);
             const bool more = key0 + step < P.key1;
+            const int64_t off_here = off;
             f32x4 s[X];
+            scores4<T, C>(S, q, s);
+            Scales<DP> here[X];
 #pragma unroll
-            for (int x = 0; x < X; ++x) {
-                s[x] = f32x4{0, 0, 0, 0};
-                float unit[KP];
-#pragma unroll
-                for (int y = 0; y < KP; ++y) unit[y] = scale_at(__shfl(ksc.w[y], x * 16 + a), kturn);
-#pragma unroll
-                for (int k = 0; k < C::KS; ++k) {
-                    const uint32_t w = kr[x][k >> 2][k & 3];
-                    const float u = unit[k >> 2];
-                    const u32x4 f = u32x4{Mma<T>::from_fp4(w, u, 0), Mma<T>::from_fp4(w, u, 1),
-                                          Mma<T>::from_fp4(w, u, 2), Mma<T>::from_fp4(w, u, 3)};
-                    s[x] = Mma<T>::run(f, q[k], s[x]);
+            for (int x = 0; x < X; ++x) here[x] = vsc[x];
+            if constexpr (TILED) {
+                if (++at == SPAN) {
+                    at = 0;
+                    from += SPAN * step;
+                    pages = checked(from, ahead);
+                    ahead = look(from + SPAN * step);
                 }
+            } else {
+                off = offset_of(key0 + step, page);
+                page = page_of(key0 + 2 * step);
             }
-            const bool partial = all_see < key0 + STEP;
-            Scales<DP> here = vsc;
-            const int64_t off_next = offset_of(key0 + step, page);
-            page = page_of(key0 + 2 * step);
-            if (more) {
-                load_keys(key0 + step, off_next);
-                load_both_scales(key0 + step, off_next);
-            }
-            if (valid != ~0ull || partial) {
-                mask_scores(&s[0], key0, limit, static_cast<uint32_t>(valid));
-                mask_scores(&s[2], key0 + 32, limit, static_cast<uint32_t>(valid >> 32));
+            if (more) there_next = load_keys(key0 + step);
+            const bool partial = row.all_see < key0 + STEP;
+            const bool odd_step = partial || (TILED ? there != ALL : __any(off_here < 0));
+            if (odd_step) {
+                // by key of this lane's row, and of the scales that it holds
+                uint32_t bits = 0;                              // bit 4 x + i: key 16 x + 4 g + i is there
+                if constexpr (TILED) {
+#pragma unroll
+                    for (int x = 0; x < X; ++x) bits |= (there >> x & 1) * (0xfu << (4 * x));
+                } else {
+                    bits = static_cast<uint32_t>(__ballot(off_here >= 0) >> (16 * g)) & 0xffffu;
+                }
+                bool odd = false;
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool seen = (key0 + 16 * x + 4 * g + i < limit) & ((bits >> (4 * x + i) & 1) != 0);
+                        s[x][i] = seen ? s[x][i] : -INFINITY;
+                    }
+                    // keys that are not there, and where a row does not see one blocks
+                    // of NaN (see add_not_finite), leave the second product
+                    const int i = a & 3;
+                    const bool gone = (key0 + 16 * x + 4 * g + i >= P.key1) | ((bits >> (4 * x + i) & 1) == 0);
+#pragma unroll
+                    for (int y = 0; y < Scales<DP>::N; ++y) {
+                        if (gone) here[x].w[y] = 0;
+                        if (partial && P.seg.causal) {
+                            const uint32_t w = finite_scales(here[x].w[y]);
+                            odd = odd || w != here[x].w[y];
+                            here[x].w[y] = w;
+                        }
+                    }
+                }
+                if (first_odd < 0 && __any(odd)) first_odd = key0;
             }
             u32x4 pf[X / 2];
             float sum = take_weights<T, C, X / 2>(R, s, A.scale, pf);
             if (too_much<T>(sum)) sum = move_maximum<T, C, X / 2>(&R, s, A.scale, pf);
             R.l += sum;
-            // keys that are not there, and in steps with unseen keys blocks of NaN
-            // (see add_not_finite), leave the product
-            bool mine = false;
-#pragma unroll
-            for (int y = 0; y < Scales<DP>::N; ++y) {
-                if (off < 0) here.w[y] = 0;
-                if (partial && P.seg.causal) {
-                    const uint32_t w = finite_scales(here.w[y]);
-                    mine = mine || w != here.w[y];
-                    here.w[y] = w;
-                }
-            }
-            if (partial && P.seg.causal && first_odd < 0 && __any(mine)) first_odd = key0;
-#pragma unroll
-            for (int u = 0; u < X / 2; ++u)
-#pragma unroll
-                for (int c = 0; c < C::NC; ++c) {
-                    float unit[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        unit[i] = scale_at(__shfl(here.w[c], (2 * u + (i >> 2)) * 16 + 4 * g + (i & 3)), vturn);
-#pragma unroll
-                    for (int w = 0; w < C::VE / 2; ++w) {
-                        uint32_t y[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            y[i] = Mma<T>::from_fp4(vr[2 * u + (i >> 2)][i & 3][c], unit[i], w);
-                        u32x4 f[2];
-                        v_transpose(y, &f[0], &f[1]);
-                        const int j = c * C::VE + 2 * w;
-                        R.o[j] = Mma<T>::run(f[0], pf[u], R.o[j]);
-                        R.o[j + 1] = Mma<T>::run(f[1], pf[u], R.o[j + 1]);
-                    }
-                }
-            if (more) load_values(off_next);
-            off = off_next;
+            values4<T, C>(S, pf, [&](int x, int i, int c) { return scale_at(of_row(here[x].w[c], i), vturn); }, &R);
+            if (more) load_values(key0 + step);
+            there = there_next;
         }
         if (first_odd >= 0) {
             // the wave's own steps only: `step` apart
@@ -1183,8 +1333,244 @@ __device__ void run_thin4(const Args& A, const Piece& P, const Dest& to, float* 
                                             t + STEP < P.key1 ? t + STEP : P.key1, limit, &R);
         }
     }
-    join_parts<C>(A, &R, lds, h, part, works);
-    if (works && part == 0) store_rows<T, C, false>(A, to, R, h * kThinRows + a, token, head, live);
+    join_parts<C>(A, &R, lds, row.h, part, row.works);
+    if (row.works && part == 0)
+        store_rows<T, C, false>(A, to, R, row.h * kThinRows + a, row.token, row.head, row.live);
+    if (A.kp > 1) __syncthreads();
+}
+
+// NHD rows.  A wave that loads its own head of 16 rows touches 16 lines of which
+// it uses a half, and the scales' lines once more for every head: that pattern
+// alone moves rows of 544 bytes at 3.5 TB/s where whole pages move at 6.0.  So
+// here the workgroup loads whole rows, K's and V's of 32 keys per part at a time,
+// to shared memory without registers, NB stages in a ring, and each wave reads its
+// head from there.  (One head a set makes rows that are little more than what
+// the wave needs, and is loaded as above.)
+//
+// A stage is 64 kp rows, K's and then V's, of R pieces of 16 bytes each (the
+// set's heads' numbers, then the pieces that hold their scales), one behind the
+// other.  Its loads, of 64 pieces, are dealt to the waves in runs of NJ or NJ + 1;
+// those past the last load row 0 to a place of their own, so that at least NJ a
+// wave are under way everywhere.  Stages past the last load row 0.  Page ids are
+// loaded NB stages before their use: loads return in order.
+template <class C>
+struct Stage4 {
+    static constexpr int DP = C::KS * 32;
+    static constexpr int NJ = DP == 64 ? 2 : (DP == 128 ? 4 : 8);       // the fewest loads of a wave
+    static constexpr int LOADS = DP == 64 ? 20 : (DP == 128 ? 36 : 70); // the most of a stage
+    static constexpr int BUF = (LOADS + 1) * 1024;
+};
+
+// Waits until at most N vector memory operations are under way and the wave's
+// shared memory operations are done, and for the workgroup's waves.
+template <int N>
+__device__ inline void stage_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// NB buffers (b2 and b3 only where there are so many); there: 128 bytes for each,
+// one a key, 1 where it is there.
+template <class T, class C, int NB>
+__device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, char* b0, char* b1, char* b2,
+                               char* b3, char* there) {
+    using G = Stage4<C>;
+    constexpr int DP = G::DP, X = 2, KP = Step4<C>::KP, NJ = G::NJ;
+    static_assert(X == kTiles4, "a stage is two tiles");
+    const int lane = here_lane(), a = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const ThinRow row = thin_row(A, P, wave);
+    const int32_t limit = row.limit, part = row.part;
+    const int kp = A.kp, keys = 32 * kp;                    // of a stage; 1, 2 or 4 parts
+    count_skipped(A, P, wave);
+
+    // the set's kv heads, and the pieces of a row
+    const int32_t kv0 = P.set * A.hs / A.parts;
+    int32_t kvl = (P.set * A.hs + A.hs - 1) / A.parts;
+    if (kvl > A.H - 1) kvl = A.H - 1;
+    const int nkv = kvl - kv0 + 1, numbers = nkv * A.D / 32;
+    const int32_t s0 = static_cast<int32_t>(A.s_base) + kv0 * (A.D / 32);       // of the row
+    const int pieces = numbers + ((s0 & 15) + nkv * (A.D / 32) + 15) / 16, row_bytes = pieces * 16;
+
+    // this wave's loads, and this lane's pieces: of which row behind the wave's
+    // first, and from where in it
+    const int loads = keys * pieces / 32, extra = loads > NJ * kWaves ? loads - NJ * kWaves : 0;
+    const int load0 = wave * NJ + (wave < extra ? wave : extra);
+    const bool more = wave < extra;
+    const int row0 = load0 * 64 / pieces;
+    int from_row[NJ + 1];
+    int64_t from[NJ + 1];
+    const int64_t to_v = A.v - A.k;
+#pragma unroll
+    for (int j = 0; j <= NJ; ++j) {
+        const int p = (load0 + j) * 64 + lane, r = p / pieces, x = p - r * pieces;
+        const bool in = r < 2 * keys;
+        from_row[j] = in ? r - row0 : 0;
+        from[j] = !in ? 0
+                      : (x < numbers ? kv0 * A.D / 2 + x * 16 : (s0 & ~15) + (x - numbers) * 16) +
+                            (r < keys ? 0 : to_v);
+    }
+    // the key of a stage that this lane looks up
+    const int32_t mine = (row0 + lane) & (keys - 1);
+    const bool tells = row0 + lane < keys;
+    auto look = [&](int32_t k0) { return key_page(A, P.lists, P.pg0, k0 + mine); };
+    auto load_stage = [&](int32_t k0, int32_t page, char* buf, char* flags) {
+        const int64_t off = page_offset(A, P.lists, P.pg0, page, k0 + mine, P.key1);
+        const int64_t safe = off < 0 ? 0 : off;
+        const char* at[NJ + 1];
+#pragma unroll
+        for (int j = 0; j <= NJ; ++j) at[j] = A.k + __shfl(safe, from_row[j]) + from[j];
+        char* base = buf + load0 * 1024;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            load_to_lds(at[j], load0 + j < loads ? base + j * 1024 : buf + G::LOADS * 1024);
+        if (more) load_to_lds(at[NJ], base + NJ * 1024);
+        if (tells) flags[mine] = off >= 0 ? 1 : 0;
+    };
+
+    // this lane's places in a buffer, of numbers and scales: key a of K, 4 g of V
+    const int hn = (row.kvh - kv0) * (A.D / 2), hs = numbers * 16 + (s0 & 15) + (row.kvh - kv0) * (A.D / 32);
+    int kn[KP], kc[KP], vn[C::NC], vc[C::NC];
+#pragma unroll
+    for (int y = 0; y < KP; ++y) {
+        int b = DP == 64 ? g * 8 : y * 64 + g * 16;
+        if (b >= A.D / 2) b = 0;
+        kn[y] = (part * 32 + a) * row_bytes + hn + b;
+        kc[y] = (part * 32 + a) * row_bytes + hs + b / 16;
+    }
+#pragma unroll
+    for (int c = 0; c < C::NC; ++c) {
+        int b = (c * 16 + a) * C::VE / 2;
+        if (b >= A.D / 2) b = 0;
+        vn[c] = (keys + part * 32 + 4 * g) * row_bytes + hn + b;
+        vc[c] = (keys + part * 32 + 4 * g) * row_bytes + hs + b / 16;
+    }
+
+    Rows<C> R;
+    clear(&R);
+    u32x4 q[C::KS];
+    load_q<T, C>(A, q, row.token, row.head, row.live);
+    int32_t first_odd = -1;             // this wave's first step whose product left values out
+
+    auto compute = [&](int32_t k0, const char* buf, const char* flags) {
+        const int32_t key0 = k0 + part * 32;
+        if (!row.works || key0 >= P.key1) return;
+        const uint32_t valid = static_cast<uint32_t>(__ballot(flags[part * 32 + (lane & 31)] != 0));
+        Step4<C> S;
+        uint32_t vs[X][4][C::NC];
+        // (values that the compiler does not carry around the loop for every buffer)
+#pragma unroll
+        for (int y = 0; y < KP; ++y) {
+            int n = kn[y], c = kc[y];
+            asm volatile("" : "+v"(n), "+v"(c));
+#pragma unroll
+            for (int x = 0; x < X; ++x) {
+                if constexpr (DP == 64) {
+                    const u32x2 w = *reinterpret_cast<const u32x2*>(buf + n + x * 16 * row_bytes);
+                    S.k[x][y] = u32x4{w.x, w.y, 0, 0};
+                } else {
+                    S.k[x][y] = *reinterpret_cast<const u32x4*>(buf + n + x * 16 * row_bytes);
+                }
+                S.ks[x][y] = *reinterpret_cast<const uint8_t*>(buf + c + x * 16 * row_bytes);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C::NC; ++c) {
+            int n = vn[c], m = vc[c];
+            asm volatile("" : "+v"(n), "+v"(m));
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (16 * x + i) * row_bytes;
+                    if constexpr (C::VE == 4) S.v[x][i][c] = *reinterpret_cast<const uint16_t*>(buf + n + r);
+                    else S.v[x][i][c] = *reinterpret_cast<const uint32_t*>(buf + n + r);
+                    vs[x][i][c] = *reinterpret_cast<const uint8_t*>(buf + m + r);
+                }
+        }
+        f32x4 s[X];
+        scores4<T, C>(S, q, s);
+        const bool partial = row.all_see < key0 + 32;
+        if (valid != 0xffffffffu || partial) {
+            uint32_t bits = valid;
+            asm volatile("" : "+s"(bits));      // what follows stays in this branch
+            mask_scores(s, key0, limit, bits);
+            // keys that are not there, and where a row does not see one blocks of NaN
+            // (see add_not_finite), leave the second product
+            bool odd = false;
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < C::NC; ++c) {
+                        const bool gone = ((bits >> (16 * x + 4 * g + i)) & 1) == 0;
+                        const bool nan = partial && P.seg.causal && vs[x][i][c] == 255;
+                        odd = odd || (nan && !gone);
+                        if (gone || nan) vs[x][i][c] = 0;
+                    }
+            if (first_odd < 0 && __any(odd)) first_odd = key0;
+        }
+        u32x4 pf[1];
+        float sum = take_weights<T, C, 1>(R, s, A.scale, pf);
+        if (too_much<T>(sum)) sum = move_maximum<T, C, 1>(&R, s, A.scale, pf);
+        R.l += sum;
+        values4<T, C>(S, pf, [&](int x, int i, int c) { return __builtin_bit_cast(float, vs[x][i][c] << 23); }, &R);
+    };
+
+    const int32_t step = keys;
+    int32_t k0 = P.key0;
+    auto buffer = [&](int n) { return n == 0 ? b0 : (n == 1 ? b1 : (n == 2 ? b2 : b3)); };
+    // stages 0 .. NB - 2 first, each with the page ids of one NB stages later behind it
+    int32_t ids[NB], first[NB - 1];
+#pragma unroll
+    for (int n = 0; n < NB - 1; ++n) first[n] = look(k0 + n * step);
+    ids[0] = look(k0 + (NB - 1) * step);
+    // none of these loads behind a stage's
+#pragma unroll
+    for (int n = 0; n < NB - 1; ++n) asm volatile("" : "+v"(first[n]));
+    asm volatile("" : "+v"(ids[0]));
+#pragma unroll
+    for (int k = 0; k < C::KS; ++k) asm volatile("" : "+v"(q[k]));
+#pragma unroll
+    for (int n = 0; n < NB - 1; ++n) {
+        load_stage(k0 + n * step, first[n], buffer(n), there + 128 * n);
+        asm volatile("" ::: "memory");
+        ids[n + 1] = look(k0 + (NB + n) * step);
+    }
+    // One stage: the one NB - 1 later is on its way to the buffer that was read
+    // last.  Behind the last of a stage's loads there are at least those of NB - 2
+    // stages and a page id with each when its turn comes.
+    auto turn = [&](int n) {
+        constexpr int N = NB - 1;
+        stage_barrier<(NB - 2) * (NJ + 1)>();
+        load_stage(k0 + N * step, ids[n], buffer((n + N) % NB), there + 128 * ((n + N) % NB));
+        ids[n] = look(k0 + (N + NB) * step);
+        compute(k0, buffer(n), there + 128 * n);
+        k0 += step;
+    };
+    // whole rounds of the ring without a branch, so that the loads under way are
+    // counted alike on every path to a wait, and what is left behind them
+    const int32_t rounds = P.key1 - (NB - 1) * step;
+    while (k0 < rounds) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) turn(n);
+    }
+#pragma unroll
+    for (int n = 0; n < NB - 1; ++n)
+        if (k0 < P.key1) turn(n);
+    stage_barrier<0>();                 // nothing is on its way to the buffers
+    if (first_odd >= 0) {
+        // the wave's own steps only: `step` apart
+        for (int32_t t = first_odd; t < P.key1; t += step)
+            add_not_finite<T, C, false>(A, P.lists, P.pg0, row.kvh, t, t + 32 < P.key1 ? t + 32 : P.key1,
+                                        limit, &R);
+    }
+    join_parts<C>(A, &R, reinterpret_cast<float*>(b0), row.h, part, row.works);
+    if (row.works && part == 0)
+        store_rows<T, C, false>(A, to, R, row.h * kThinRows + a, row.token, row.head, row.live);
     if (A.kp > 1) __syncthreads();
 }
 
@@ -1207,15 +1593,6 @@ struct Wide {
     static constexpr int RB = DP * 2;                   // bytes of a V row
     static constexpr int BUF = KF * 1024 + KT * RB;
 };
-
-typedef __attribute__((address_space(3))) char lds_char;
-
-// 16 bytes per lane from memory to base + 16 * lane of shared memory.
-__device__ inline void load_to_lds(const char* src, char* base) {
-    __builtin_amdgcn_global_load_lds(
-        (const __attribute__((address_space(1))) uint32_t*)src,
-        (__attribute__((address_space(3))) uint32_t*)base, 16, 0, 0);
-}
 
 // V stands in shared memory row by row, its 32-byte pairs of 16-byte chunks
 // permuted by row so that the 4 rows x 32 bytes that 16 lanes read together,
@@ -1791,28 +2168,37 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
     return M;
 }
 
-// LINES: 1 thin, 2 wide, 3 both.
+// LINES: 1 thin, 2 wide, 3 both; and of thin 4-bit tiles, 4 more: pages hold whole tiles of 16 keys, 8
+// more: rows by way of shared memory.
 template <class T, int BITS, int DP, int LINES>
 struct Shared {
     using C = Cfg<T, BITS, DP>;
     static constexpr int THIN = LINES & 1 ? (kWaves / 2) * 64 * (4 * C::NJ + 2) * 4 : 16;
-    static constexpr int BUF = LINES == 1 ? 16 : Wide<C>::BUF;
+    static constexpr int WIDE = LINES & 2 ? Wide<C>::BUF : 16;
+    static constexpr int ROWS = LINES & 8 ? Stage4<C>::BUF : 16;
+    static constexpr int BUF = WIDE > ROWS ? WIDE : ROWS;
     static constexpr int BUF0 = BUF > THIN ? BUF : THIN;
+    // more buffers for rows where wide tiles leave the room
+    static constexpr int NB = (LINES & 10) == 8 && DP <= 128 ? 4 : 2;
+    static constexpr int MORE = NB == 4 ? ROWS : 16;
 };
 
 template <class T, int BITS, int DP, int LINES>
-__global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
+__global__ __launch_bounds__(kThreads, BITS == 4 && !(LINES & 2) ? kWaves4 : 2) void k_attend(const Args A) {
     using C = Cfg<T, BITS, DP>;
     using S = Shared<T, BITS, DP, LINES>;
     __shared__ Plan plan;
     // separate arrays: reads of one need not wait for loads on their way to the other
     __shared__ __attribute__((aligned(16))) char buf0[S::BUF0];
     __shared__ __attribute__((aligned(16))) char buf1[S::BUF];
+    __shared__ __attribute__((aligned(16))) char buf2[S::MORE];
+    __shared__ __attribute__((aligned(16))) char buf3[S::MORE];
+    __shared__ char there[LINES & 8 ? 128 * S::NB : 16];
     __shared__ uint32_t flags[2 * Wide<C>::NB];
     __shared__ uint32_t odds[kWaves];
-    const Mine M = plan_work<LINES>(A, &plan, blockIdx.x, gridDim.x);
+    const Mine M = plan_work<LINES & 3>(A, &plan, blockIdx.x, gridDim.x);
     if (M.lo >= M.hi) return;
-    const bool wide_line = LINES == 2 || (LINES == 3 && M.line == 1);
+    const bool wide_line = (LINES & 3) == 2 || ((LINES & 3) == 3 && M.line == 1);
     const int32_t nseg = A.num_groups + A.num_reqs;
     const int step_log2 = wide_line ? (Wide<C>::KT == 128 ? 7 : 6) : 5;
 
@@ -1899,8 +2285,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
             if constexpr (LINES & 1) {
                 float* joins = reinterpret_cast<float*>(buf0);
                 if constexpr (C::FP4) {
-                    if (!wide_line && A.tiled) run_thin4<T, C, true>(A, P, to, joins);
-                    if (!wide_line && !A.tiled) run_thin4<T, C, false>(A, P, to, joins);
+                    if constexpr (LINES & 8) {
+                        if (!wide_line) run_thin4_rows<T, C, S::NB>(A, P, to, buf0, buf1, buf2, buf3, there);
+                    } else {
+                        if (!wide_line) run_thin4<T, C, (LINES & 4) != 0>(A, P, to, joins);
+                    }
                 } else {
                     if (!wide_line) run_thin<T, C>(A, P, to, joins);
                 }

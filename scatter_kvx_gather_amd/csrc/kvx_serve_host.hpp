@@ -384,7 +384,8 @@ kvx_status validate_read(const LayerRef& ref, int32_t block_layout, const kvx_po
 
 namespace at = kvx::attend;
 
-constexpr int64_t kAttendGrid = 256;    // one workgroup per compute unit of an MI355X
+constexpr int64_t kUnits = 256;         // compute units of an MI355X
+constexpr int64_t kMostGrid = 2 * kUnits;
 constexpr int64_t kJoinPlaces = 2048;   // waves of a join that shares rows among waves
 
 // The average query rows per kv head of a batch's contexts (and those of its
@@ -408,6 +409,7 @@ struct AttendShape {
     bool pre_wide, own_wide;
     int32_t wide_rows;
     int32_t slot_rows;
+    int32_t grid;                       // workgroups of k_attend
     int64_t placed, plan, splits, slot_ml, slot_o, row_ml, row_o, bytes;    // offsets into the workspace
 };
 
@@ -430,6 +432,10 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     s->wide_rows = s->DP <= 128 ? 256 : 128;
     // of the larger tile whichever this batch takes, so that a smaller batch needs no more
     s->slot_rows = std::max(s->wide_rows, at::kWaves * at::kThinRows);
+    // one workgroup per compute unit, and as many as its registers hold of 4-bit thin tiles alone
+    const bool fp4 = layout->dtype == KVX_FP4;
+    s->grid = static_cast<int32_t>(kUnits * (fp4 && !s->own_wide && !s->pre_wide ? at::kWaves4 / 2 : 1));
+    const int64_t most = fp4 ? kMostGrid : kUnits;
     int64_t end = 0;
     auto take = [&](int64_t count, int64_t size) {
         const int64_t at0 = end;
@@ -440,9 +446,9 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     };
     s->placed = take(static_cast<int64_t>(num_reqs) + num_groups, sizeof(at::Placed));
     s->plan = take(6, 8);
-    s->splits = take(kAttendGrid, sizeof(at::Split));
-    s->slot_ml = take(2 * kAttendGrid * s->slot_rows, 8);
-    s->slot_o = take(2 * kAttendGrid * s->slot_rows, 4 * static_cast<int64_t>(D));
+    s->splits = take(most, sizeof(at::Split));
+    s->slot_ml = take(2 * most * s->slot_rows, 8);
+    s->slot_o = take(2 * most * s->slot_rows, 4 * static_cast<int64_t>(D));
     int64_t out_rows = 0;
     if (!mul_ok(tokens, q_heads, &out_rows)) return KVX_E_RANGE;
     if (num_groups == 0) out_rows = 0;
@@ -457,11 +463,18 @@ struct AttendKernels {
     const void *main, *join, *join_shared, *join_items;
 };
 
-// BITS: of a pool's values.
+// BITS: of a pool's values; lines: k_attend's LINES.
 template <class T, int BITS, int DP>
 AttendKernels attend_kernels(int lines) {
     const void* main;
-    if constexpr (DP > 128 && BITS == 16)
+    if constexpr (BITS == 4)
+        main = lines == 1    ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 1>)
+               : lines == 3  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 3>)
+               : lines == 5  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 5>)
+               : lines == 7  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 7>)
+               : lines == 9  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 9>)
+                             : reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 11>);
+    else if constexpr (DP > 128 && BITS == 16)
         main = reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 2>);
     else
         main = lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 1>)
@@ -797,8 +810,6 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.num_pages = pool->num_pages;
     a.page_size = pool->page_size;
     a.page_shift = shift_of(pool->page_size);
-    // 16 rows of a tile in one page, their offsets from its first in 32 bits
-    a.tiled = fp4 && pool->page_size % 16 == 0 && ref.row_stride <= (1 << 26);
     a.tok_off = reqs->tok_off;
     a.ctx = ctx_len;
     a.own = at::Lists{table->pg_off, table->page_ids, table->num_ids};
@@ -862,7 +873,12 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.row_o = reinterpret_cast<float*>(ws + s.row_o);
     a.slot_rows = s.slot_rows;
 
-    const int lines = s.own_wide || s.pre_wide ? 3 : 1;
+    int lines = s.own_wide || s.pre_wide ? 3 : 1;
+    // 4 bits: rows by way of shared memory, or the 16 rows of a tile in one page,
+    // their offsets inside it in 32 bits
+    if (fp4 && block_layout == KVX_NHD && a.hs > 1)
+        lines |= 8;
+    else if (fp4 && pool->page_size % 16 == 0 && a.page_shift >= 0 && ref.page_stride < (int64_t(1) << 31)) lines |= 4;
     const AttendKernels k = x.dtype == KVX_BF16 ? attend_kernels<__bf16>(layout->dtype, s.DP, lines)
                                                 : attend_kernels<_Float16>(layout->dtype, s.DP, lines);
     if (log_enabled())
@@ -870,7 +886,7 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
                      "kvx: attend reqs=%d groups=%d tokens=%lld heads=%d/%d dim=%d prefix=%s own=%s\n",
                      a.num_reqs, ng, static_cast<long long>(a.T), x.q_heads, g.H, a.D,
                      ng == 0 ? "none" : (s.pre_wide ? "wide" : "thin"), s.own_wide ? "wide" : "thin");
-    KVX_TRY(launch_one(k.main, kAttendGrid, at::kThreads, a, stream));
+    KVX_TRY(launch_one(k.main, s.grid, at::kThreads, a, stream));
     if (ng > 0) {
         const int32_t per_head = (a.gv + 256 / s.DP - 1) / (256 / s.DP);
         const int32_t units = heads * per_head;
@@ -887,8 +903,8 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
                    ? KVX_OK
                    : KVX_E_HIP;
     }
-    int32_t pieces = static_cast<int32_t>(kAttendGrid);
-    const int64_t grid = pieces * at::kJoinParts +
+    int32_t pieces = s.grid;
+    const int64_t grid = int64_t(pieces) * at::kJoinParts +
                          (a.num_reqs + 64 * at::kJoinWaves - 1) / (64 * at::kJoinWaves);
     void* params[] = {&a, &pieces};
     return hipLaunchKernel(k.join_items, dim3(static_cast<uint32_t>(grid)), dim3(64 * at::kJoinWaves), params,
