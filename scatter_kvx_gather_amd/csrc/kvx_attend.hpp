@@ -85,7 +85,7 @@ constexpr int kTiles4 = 2;               // 16-key tiles of a thin step over 4-b
 constexpr int kWaves4 = 2;               // waves of a SIMD where all tiles are such
 constexpr int32_t kMaxKeys = 1 << 30;    // of a context or a prefix: step indices stay in 32 bits
 constexpr int kJoinWaves = 8;
-constexpr int kJoinParts = 4;
+constexpr int kJoinParts = 4;              // at most
 
 // Weights are taken against a reference, which is a row's maximum less kRoom
 // when it moves and may lag it while a lane's weights of one step sum to no
@@ -169,6 +169,8 @@ struct Args {
     int32_t hs;                         // thin heads per set
     int32_t kp;                         // waves that share a thin head's keys
     int32_t thin_tokens;                // tokens per thin tile
+    int32_t pieces;                     // 16-byte pieces of a set's row of a 4-bit NHD pool, at most
+    uint32_t by_hs, by_parts, by_gv, by_pieces;     // magics of these
     int32_t wide_tokens;                // tokens per wide tile
     int32_t pre_wide;                   // prefixes run in wide tiles
     int32_t own_wide;                   // own contexts run in wide tiles
@@ -279,6 +281,11 @@ __device__ inline int32_t cut_key(const Seg& g, int64_t x, int step_log2, int32_
     if (x <= g.extra) return 0;
     const int64_t k = (x - g.extra) >> step_log2 << step_log2;
     return k < keys ? static_cast<int32_t>(k) : keys;
+}
+
+// x / d by magic_of(d) = ceil(2^32 / d) (0 for d = 1), exact while x d < 2^32.
+__device__ inline int32_t by(int32_t x, uint32_t magic) {
+    return magic == 0 ? x : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(x), magic));
 }
 
 // A line of n units cut into `wgs` pieces whose lengths differ by one at most.
@@ -1082,14 +1089,15 @@ struct ThinRow {
 __device__ inline ThinRow thin_row(const Args& A, const Piece& P, int wave) {
     const int a = here_lane() & 15;
     ThinRow r;
-    r.h = wave % A.hs;
-    r.part = wave / A.hs;
+    r.part = by(wave, A.by_hs);
+    r.h = wave - r.part * A.hs;
     const int32_t vh = P.set * A.hs + r.h;                // thin head
-    r.kvh = vh / A.parts;
-    const int32_t sub = vh % A.parts;
+    r.kvh = by(vh, A.by_parts);
+    const int32_t sub = vh - r.kvh * A.parts;
     r.works = r.part < A.kp && vh < A.H * A.parts;
-    const int32_t local = P.tile * A.thin_tokens + a / A.gv;
-    const int32_t hsub = sub * A.gv + a % A.gv;
+    const int32_t at = by(a, A.by_gv);
+    const int32_t local = P.tile * A.thin_tokens + at;
+    const int32_t hsub = sub * A.gv + a - at * A.gv;
     r.live = r.works && a < A.thin_tokens * A.gv && local < P.seg.ntok && hsub < A.G;
     r.token = P.seg.tok0 + local;
     r.head = r.kvh * A.G + hsub;
@@ -1353,11 +1361,13 @@ __device__ void run_thin4(const Args& A, const Piece& P, const Dest& to, float* 
 // those past the last load row 0 to a place of their own, so that at least NJ a
 // wave are under way everywhere.  Stages past the last load row 0.  Page ids are
 // loaded NB stages before their use: loads return in order.
+constexpr int stage4_loads(int DP) { return DP == 64 ? 20 : (DP == 128 ? 36 : 70); }
+
 template <class C>
 struct Stage4 {
     static constexpr int DP = C::KS * 32;
     static constexpr int NJ = DP == 64 ? 2 : (DP == 128 ? 4 : 8);       // the fewest loads of a wave
-    static constexpr int LOADS = DP == 64 ? 20 : (DP == 128 ? 36 : 70); // the most of a stage
+    static constexpr int LOADS = stage4_loads(DP);                      // the most of a stage
     static constexpr int BUF = (LOADS + 1) * 1024;
 };
 
@@ -1371,53 +1381,64 @@ __device__ inline void stage_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// NB buffers (b2 and b3 only where there are so many); there: 128 bytes for each,
+// NB buffers (b2 only where there are three); there: 128 bytes for each,
 // one a key, 1 where it is there.
 template <class T, class C, int NB>
 __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, char* b0, char* b1, char* b2,
-                               char* b3, char* there) {
+                               char* there) {
     using G = Stage4<C>;
     constexpr int DP = G::DP, X = 2, KP = Step4<C>::KP, NJ = G::NJ;
     static_assert(X == kTiles4, "a stage is two tiles");
     const int lane = here_lane(), a = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const ThinRow row = thin_row(A, P, wave);
-    const int32_t limit = row.limit, part = row.part;
     const int kp = A.kp, keys = 32 * kp;                    // of a stage; 1, 2 or 4 parts
-    count_skipped(A, P, wave);
+    const int pieces = A.pieces, row_bytes = pieces * 16;
 
-    // the set's kv heads, and the pieces of a row
-    const int32_t kv0 = P.set * A.hs / A.parts;
-    int32_t kvl = (P.set * A.hs + A.hs - 1) / A.parts;
-    if (kvl > A.H - 1) kvl = A.H - 1;
-    const int nkv = kvl - kv0 + 1, numbers = nkv * A.D / 32;
-    const int32_t s0 = static_cast<int32_t>(A.s_base) + kv0 * (A.D / 32);       // of the row
-    const int pieces = numbers + ((s0 & 15) + nkv * (A.D / 32) + 15) / 16, row_bytes = pieces * 16;
-
-    // this wave's loads, and this lane's pieces: of which row behind the wave's
-    // first, and from where in it
+    // this wave's loads, and their first row
     const int loads = keys * pieces / 32, extra = loads > NJ * kWaves ? loads - NJ * kWaves : 0;
     const int load0 = wave * NJ + (wave < extra ? wave : extra);
     const bool more = wave < extra;
-    const int row0 = load0 * 64 / pieces;
+    const int row0 = by(load0 * 64, A.by_pieces);
+    // the key of a stage that this lane looks up; the first stages' pages
+    const int32_t mine = (row0 + lane) & (keys - 1), step = keys;
+    const bool tells = row0 + lane < keys;
+    auto look = [&](int32_t k) { return key_page(A, P.lists, P.pg0, k + mine); };
+    int32_t k0 = P.key0, ids[NB], first[NB - 1];
+#pragma unroll
+    for (int n = 0; n < NB - 1; ++n) first[n] = look(k0 + n * step);
+    ids[0] = look(k0 + (NB - 1) * step);
+
+    const ThinRow row = thin_row(A, P, wave);
+    const int32_t limit = row.limit, part = row.part;
+    count_skipped(A, P, wave);
+    Rows<C> R;
+    clear(&R);
+    u32x4 q[C::KS];
+    load_q<T, C>(A, q, row.token, row.head, row.live);
+    int32_t first_odd = -1;             // this wave's first step whose product left values out
+
+    // the set's kv heads, and this lane's pieces: of which row behind the wave's
+    // first, and from where in it
+    const int32_t kv0 = by(P.set * A.hs, A.by_parts);
+    int32_t kvl = by(P.set * A.hs + A.hs - 1, A.by_parts);
+    if (kvl > A.H - 1) kvl = A.H - 1;
+    const int nkv = kvl - kv0 + 1, numbers = nkv * A.D / 32;
+    const int32_t s0 = static_cast<int32_t>(A.s_base) + kv0 * (A.D / 32);       // of the row
+    const int used = numbers + ((s0 & 15) + nkv * (A.D / 32) + 15) / 16;
     int from_row[NJ + 1];
     int64_t from[NJ + 1];
     const int64_t to_v = A.v - A.k;
 #pragma unroll
     for (int j = 0; j <= NJ; ++j) {
-        const int p = (load0 + j) * 64 + lane, r = p / pieces, x = p - r * pieces;
-        const bool in = r < 2 * keys;
-        from_row[j] = in ? r - row0 : 0;
+        const int p = (load0 + j) * 64 + lane, r = by(p, A.by_pieces), x = p - r * pieces;
+        const bool in = r < 2 * keys && x < used;
+        from_row[j] = r < 2 * keys ? r - row0 : 0;
         from[j] = !in ? 0
                       : (x < numbers ? kv0 * A.D / 2 + x * 16 : (s0 & ~15) + (x - numbers) * 16) +
                             (r < keys ? 0 : to_v);
     }
-    // the key of a stage that this lane looks up
-    const int32_t mine = (row0 + lane) & (keys - 1);
-    const bool tells = row0 + lane < keys;
-    auto look = [&](int32_t k0) { return key_page(A, P.lists, P.pg0, k0 + mine); };
-    auto load_stage = [&](int32_t k0, int32_t page, char* buf, char* flags) {
-        const int64_t off = page_offset(A, P.lists, P.pg0, page, k0 + mine, P.key1);
+    auto load_stage = [&](int32_t k, int32_t page, char* buf, char* flags) {
+        const int64_t off = page_offset(A, P.lists, P.pg0, page, k + mine, P.key1);
         const int64_t safe = off < 0 ? 0 : off;
         const char* at[NJ + 1];
 #pragma unroll
@@ -1447,12 +1468,6 @@ __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, ch
         vn[c] = (keys + part * 32 + 4 * g) * row_bytes + hn + b;
         vc[c] = (keys + part * 32 + 4 * g) * row_bytes + hs + b / 16;
     }
-
-    Rows<C> R;
-    clear(&R);
-    u32x4 q[C::KS];
-    load_q<T, C>(A, q, row.token, row.head, row.live);
-    int32_t first_odd = -1;             // this wave's first step whose product left values out
 
     auto compute = [&](int32_t k0, const char* buf, const char* flags) {
         const int32_t key0 = k0 + part * 32;
@@ -1520,15 +1535,9 @@ __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, ch
         values4<T, C>(S, pf, [&](int x, int i, int c) { return __builtin_bit_cast(float, vs[x][i][c] << 23); }, &R);
     };
 
-    const int32_t step = keys;
-    int32_t k0 = P.key0;
-    auto buffer = [&](int n) { return n == 0 ? b0 : (n == 1 ? b1 : (n == 2 ? b2 : b3)); };
-    // stages 0 .. NB - 2 first, each with the page ids of one NB stages later behind it
-    int32_t ids[NB], first[NB - 1];
-#pragma unroll
-    for (int n = 0; n < NB - 1; ++n) first[n] = look(k0 + n * step);
-    ids[0] = look(k0 + (NB - 1) * step);
-    // none of these loads behind a stage's
+    auto buffer = [&](int n) { return n == 0 ? b0 : (n == 1 ? b1 : b2); };
+    // stages 0 .. NB - 2 first, each with the page ids of one NB stages later behind it;
+    // none of the loads so far behind a stage's
 #pragma unroll
     for (int n = 0; n < NB - 1; ++n) asm volatile("" : "+v"(first[n]));
     asm volatile("" : "+v"(ids[0]));
@@ -2179,8 +2188,8 @@ struct Shared {
     static constexpr int BUF = WIDE > ROWS ? WIDE : ROWS;
     static constexpr int BUF0 = BUF > THIN ? BUF : THIN;
     // more buffers for rows where wide tiles leave the room
-    static constexpr int NB = (LINES & 10) == 8 && DP <= 128 ? 4 : 2;
-    static constexpr int MORE = NB == 4 ? ROWS : 16;
+    static constexpr int NB = (LINES & 10) == 8 && DP <= 128 ? 3 : 2;
+    static constexpr int MORE = NB == 3 ? ROWS : 16;
 };
 
 template <class T, int BITS, int DP, int LINES>
@@ -2192,7 +2201,6 @@ __global__ __launch_bounds__(kThreads, BITS == 4 && !(LINES & 2) ? kWaves4 : 2) 
     __shared__ __attribute__((aligned(16))) char buf0[S::BUF0];
     __shared__ __attribute__((aligned(16))) char buf1[S::BUF];
     __shared__ __attribute__((aligned(16))) char buf2[S::MORE];
-    __shared__ __attribute__((aligned(16))) char buf3[S::MORE];
     __shared__ char there[LINES & 8 ? 128 * S::NB : 16];
     __shared__ uint32_t flags[2 * Wide<C>::NB];
     __shared__ uint32_t odds[kWaves];
@@ -2286,7 +2294,7 @@ __global__ __launch_bounds__(kThreads, BITS == 4 && !(LINES & 2) ? kWaves4 : 2) 
                 float* joins = reinterpret_cast<float*>(buf0);
                 if constexpr (C::FP4) {
                     if constexpr (LINES & 8) {
-                        if (!wide_line) run_thin4_rows<T, C, S::NB>(A, P, to, buf0, buf1, buf2, buf3, there);
+                        if (!wide_line) run_thin4_rows<T, C, S::NB>(A, P, to, buf0, buf1, buf2, there);
                     } else {
                         if (!wide_line) run_thin4<T, C, (LINES & 4) != 0>(A, P, to, joins);
                     }
@@ -2348,29 +2356,55 @@ struct Sum {
 
 // Adds row `slot_row` of the pieces w0 + way, w0 + way + ways .. w1 of an item
 // that begins at unit `item`; a workgroup has left its slot if its piece has a
-// step of keys.
+// step of keys.  With many pieces each lane finds that out for one of them (131071
+// keys in 256 pieces: 17.2 us, one after the other 18.6; of four it takes longer).
+// All but slot_row and d are the wave's, and all its lanes come here.
 __device__ inline void add_slots(const Args& A, Sum* sum, const Seg& g, const Cuts& cuts, int64_t item,
                                  int32_t keys, int32_t w0, int32_t w1, int32_t slot0, int slot_row,
                                  int d, int step_log2, int way, int ways) {
-    constexpr int B = 4;                    // slots under way at once
-    for (int32_t w = w0 + way; w <= w1; w += B * ways) {
-        float2 ml[B];
-        f32x4 x[B];
+    const int64_t row = slot0 * static_cast<int64_t>(A.slot_rows) + slot_row;
+    if (w1 - w0 < 4 * ways) {               // few: each looked at in turn
+        float2 ml[4];
+        f32x4 x[4];
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
+        for (int i = 0; i < 4; ++i) {
             ml[i] = make_float2(0.0f, 0.0f);
             x[i] = f32x4{0, 0, 0, 0};
-            const int32_t v = w + i * ways;
+            const int32_t v = w0 + way + i * ways;
             if (v > w1) continue;
             const int32_t k0 = v == w0 ? 0 : cut_key(g, cuts.start(v) - item, step_log2, keys);
             const int32_t k1 = v == w1 ? keys : cut_key(g, cuts.start(v + 1) - item, step_log2, keys);
             if (k0 >= k1) continue;
-            const int64_t at = static_cast<int64_t>(slot0 + 2 * v + (v == w0 ? 1 : 0)) * A.slot_rows + slot_row;
+            const int64_t at = row + static_cast<int64_t>(2 * v + (v == w0 ? 1 : 0)) * A.slot_rows;
             ml[i] = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);
             if (d < A.D) x[i] = *reinterpret_cast<const f32x4*>(A.slot_o + at * A.D + d);
         }
 #pragma unroll
-        for (int i = 0; i < B; ++i) sum->add(ml[i], x[i]);
+        for (int i = 0; i < 4; ++i) sum->add(ml[i], x[i]);
+        return;
+    }
+    constexpr int B = 8;                    // slots under way at once
+    const int lane = threadIdx.x & 63;
+    for (int32_t w = w0 + way; w <= w1; w += 64 * ways) {
+        const int32_t v = w + lane * ways;
+        const int32_t k0 = v == w0 ? 0 : cut_key(g, cuts.start(v) - item, step_log2, keys);
+        const int32_t k1 = v == w1 ? keys : cut_key(g, cuts.start(v + 1) - item, step_log2, keys);
+        uint64_t left = __ballot(v <= w1 && k0 < k1);
+        for (int32_t u = w; left != 0; u += B * ways, left >>= B) {
+            float2 ml[B];
+            f32x4 x[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const int32_t s = u + i * ways < w1 ? u + i * ways : w1;        // a slot of the workspace
+                const int64_t at = row + static_cast<int64_t>(2 * s + (s == w0 ? 1 : 0)) * A.slot_rows;
+                ml[i] = *reinterpret_cast<const float2*>(A.slot_ml + at * 2);
+                x[i] = f32x4{0, 0, 0, 0};
+                if (d < A.D) x[i] = *reinterpret_cast<const f32x4*>(A.slot_o + at * A.D + d);
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+                if (left >> i & 1) sum->add(ml[i], x[i]);
+        }
     }
 }
 
@@ -2394,13 +2428,13 @@ __device__ inline void join_ways(Sum* sum, float (*lds)[6][64], int wave, int wa
                  f32x4{lds[w][2][lane], lds[w][3][lane], lds[w][4][lane], lds[w][5][lane]});
 }
 
-// Without prefixes: an item that lies in n pieces is joined by kJoinParts
+// Without prefixes: an item that lies in n pieces is joined by `parts`
 // workgroups for each of the first n - 1, its rows dealt to their waves; with
 // many pieces, `ways` waves share a row's.  (One wave for all pieces of a row
 // took 26 us for 4 requests behind 2048 tokens, most of the call.)  Workgroups
 // behind those write the rows of requests without keys, 64 requests a wave.
 template <class T, int DP>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Args A, int32_t pieces) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Args A, int32_t pieces, int32_t parts) {
     constexpr int LPR = DP / 4, RPW = 64 / LPR;
     __shared__ float sums[kJoinWaves][6][64];
     const int lane = threadIdx.x & 63;
@@ -2408,8 +2442,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Arg
     const int d = lane % LPR * 4, sub_row = lane / LPR;
     const int32_t hq = A.H * A.G;
     const int32_t block = blockIdx.x;
-    if (block >= pieces * kJoinParts) {
-        const int32_t r0 = ((block - pieces * kJoinParts) * kJoinWaves + wave) * 64;
+    if (block >= pieces * parts) {
+        const int32_t r0 = ((block - pieces * parts) * kJoinWaves + wave) * 64;
         int32_t t0 = 0, n = 0;
         if (r0 + lane < A.num_reqs && A.ctx[r0 + lane] <= 0) {
             t0 = clamp_to(A.tok_off[r0 + lane], 0, A.T);
@@ -2424,39 +2458,45 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attend_join_items(const Arg
         }
         return;
     }
-    const int32_t piece = block / kJoinParts;
+    const int32_t piece = block / parts;
     const Split S = A.splits[piece];
     if (piece >= A.plan[4] + A.plan[5] || S.last < 0) return;
     const int32_t n = uniform(S.last - S.w);            // pieces less one
     const int ways = n < 4 ? 1 : (n < 8 ? 2 : (n < 16 ? 4 : 8));
     const int way = wave % ways, teams = kJoinWaves / ways;
-    const int32_t me = uniform((piece - S.slot0 / 2 - S.w) * kJoinParts) + block % kJoinParts;
+    const int32_t me = uniform((piece - S.slot0 / 2 - S.w) * parts) + block % parts;
     Cuts cuts;
     cuts.q = A.plan[S.wide ? 2 : 0];
     cuts.r = A.plan[S.wide ? 3 : 1];
     Seg g;
     g.extra = S.extra;
     const int step_log2 = S.wide ? (DP <= 128 ? 7 : 6) : 5;
-    const int rows = uniform(S.wide ? A.wide_tokens * A.G : A.hs * kThinRows);
-    for (int row0 = me * teams * RPW; row0 < rows; row0 += kJoinParts * n * teams * RPW) {
-        const int row = row0 + wave / ways * RPW + sub_row;
+    // the item's rows that have a query: of a thin head the first `each` of 16
+    const int32_t tokens = S.wide ? A.wide_tokens : A.thin_tokens;
+    const int32_t left = uniform(S.ntok - S.tile * tokens);
+    const int each = (left < tokens ? left : tokens) * (S.wide ? A.G : A.gv);
+    const int rows = uniform(S.wide ? each : A.hs * each);
+    for (int row0 = me * teams * RPW; row0 < rows; row0 += parts * n * teams * RPW) {
+        const int x = row0 + wave / ways * RPW + sub_row;
+        int row = x;
         int32_t local, head;
-        bool live = row < rows;
+        bool live = x < rows;
         if (S.wide) {
             local = S.tile * A.wide_tokens + row / A.G;
             head = S.set * A.G + row % A.G;
         } else {
-            const int a = row % kThinRows;
-            const int32_t vh = S.set * A.hs + row / kThinRows;
+            const int h = x / each, a = x - h * each;
+            const int32_t vh = S.set * A.hs + h;
             const int32_t kvh = vh / A.parts, hin = vh % A.parts * A.gv + a % A.gv;
+            row = h * kThinRows + a;
             local = S.tile * A.thin_tokens + a / A.gv;
             head = kvh * A.G + hin;
-            live = live && a < A.thin_tokens * A.gv && kvh < A.H && hin < A.G;
+            live = live && kvh < A.H && hin < A.G;
         }
         live = live && local < S.ntok;
         Sum sum;
-        if (live)
-            add_slots(A, &sum, g, cuts, S.item, S.keys, S.w, S.last, S.slot0, row, d, step_log2, way, ways);
+        add_slots(A, &sum, g, cuts, S.item, S.keys, S.w, S.last, S.slot0, live ? row : 0, d, step_log2, way,
+                  ways);
         join_ways(&sum, sums, wave, way, ways);
         if (live && way == 0) sum.store<T>(A, S.tok0 + local, head, d);
     }

@@ -524,6 +524,19 @@ bool rows_meet(const StridedRows& a, const StridedRows& b) {
     return false;
 }
 
+// The most 16-byte pieces that a set of thin heads has of a 4-bit NHD row: its
+// numbers, and the pieces that hold its scales.
+int32_t row_pieces(const at::Args& a, int64_t s_base, int32_t D) {
+    int32_t most = 1;
+    for (int32_t set = 0; set < a.sets; ++set) {
+        const int32_t kv0 = set * a.hs / a.parts;
+        const int32_t n = std::min((set * a.hs + a.hs - 1) / a.parts, a.H - 1) - kv0 + 1;
+        const int64_t at0 = (s_base + int64_t(kv0) * (D / 32)) % 16;
+        most = std::max<int32_t>(most, n * D / 32 + static_cast<int32_t>((at0 + n * (D / 32) + 15) / 16));
+    }
+    return most;
+}
+
 kvx_status validate_attend(const kvx_reqs* reqs, const int32_t* ctx, const kvx_prefix* prefix,
                            hipStream_t stream) {
     if (hipStreamSynchronize(stream) != hipSuccess) return KVX_E_HIP;
@@ -843,6 +856,11 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.sets = (heads + a.hs - 1) / a.hs;
     a.kp = at::kWaves / a.hs;
     a.thin_tokens = at::kThinRows / a.gv;
+    a.by_hs = magic_of(a.hs);
+    a.by_parts = magic_of(a.parts);
+    a.by_gv = magic_of(a.gv);
+    a.pieces = fp4 ? row_pieces(a, ref.s_base, layout->head_dim) : 1;
+    a.by_pieces = magic_of(a.pieces);
     a.wide_tokens = s.wide_rows / s.G;
     a.pre_wide = s.pre_wide;
     a.own_wide = s.own_wide;
@@ -856,7 +874,7 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     // with many short items end last.
     a.thin_min_log2 = 6;
     a.wide_min_log2 = 8;
-    a.thin_item = 64;
+    a.thin_item = fp4 ? 128 : 64;
     a.wide_item = 450;
     // a compute unit's time for a wide key (its products, 2350 a ns) over that
     // for a thin key (its bytes, 26 a ns): rates of the two loops alone
@@ -876,7 +894,7 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     int lines = s.own_wide || s.pre_wide ? 3 : 1;
     // 4 bits: rows by way of shared memory, or the 16 rows of a tile in one page,
     // their offsets inside it in 32 bits
-    if (fp4 && block_layout == KVX_NHD && a.hs > 1)
+    if (fp4 && block_layout == KVX_NHD && a.hs > 1 && a.kp * a.pieces <= at::stage4_loads(s.DP))
         lines |= 8;
     else if (fp4 && pool->page_size % 16 == 0 && a.page_shift >= 0 && ref.page_stride < (int64_t(1) << 31)) lines |= 4;
     const AttendKernels k = x.dtype == KVX_BF16 ? attend_kernels<__bf16>(layout->dtype, s.DP, lines)
@@ -903,10 +921,10 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
                    ? KVX_OK
                    : KVX_E_HIP;
     }
-    int32_t pieces = s.grid;
-    const int64_t grid = int64_t(pieces) * at::kJoinParts +
+    int32_t pieces = s.grid, parts = lines & 2 ? at::kJoinParts : 2;
+    const int64_t grid = int64_t(pieces) * parts +
                          (a.num_reqs + 64 * at::kJoinWaves - 1) / (64 * at::kJoinWaves);
-    void* params[] = {&a, &pieces};
+    void* params[] = {&a, &pieces, &parts};
     return hipLaunchKernel(k.join_items, dim3(static_cast<uint32_t>(grid)), dim3(64 * at::kJoinWaves), params,
                            0, stream) == hipSuccess
                ? KVX_OK
