@@ -44,6 +44,10 @@
 // softmax, and half of the waves staging after their first step beat one step
 // (664 -> 442 us with the split items' join, 410 -> 397).
 //
+// Over 4-bit pools thin tiles read whole rows by way of shared memory where that
+// pays (run_thin4_rows) and wide tiles widen the numbers as they stage them; a scale
+// multiplies in the conversion itself, and every held value is exact in 16 bits.
+//
 // The second launch joins what is split: 3 to 10 us where that is a chain of its
 // launch and three dependent loads, more where its bytes count: behind a prefix
 // every row has two parts, of which it reads 32-bit partial rows (256 requests
@@ -82,7 +86,6 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kKeys = 32;               // keys of one step of a wave
 constexpr int kThinRows = 16;
 constexpr int kTiles4 = 2;               // 16-key tiles of a thin step over 4-bit pools
-constexpr int kWaves4 = 2;               // waves of a SIMD where all tiles are such
 constexpr int32_t kMaxKeys = 1 << 30;    // of a context or a prefix: step indices stay in 32 bits
 constexpr int kJoinWaves = 8;
 constexpr int kJoinParts = 4;              // at most
@@ -170,7 +173,9 @@ struct Args {
     int32_t kp;                         // waves that share a thin head's keys
     int32_t thin_tokens;                // tokens per thin tile
     int32_t pieces;                     // 16-byte pieces of a set's row of a 4-bit NHD pool, at most
-    uint32_t by_hs, by_parts, by_gv, by_pieces;     // magics of these
+    int32_t set_heads;                  // kv heads of a set, at most
+    uint32_t by_hs, by_parts, by_gv, by_pieces, by_set_heads;   // magics of these,
+    uint32_t by_blocks, by_half;        // of D / 32 and of D / 2
     int32_t wide_tokens;                // tokens per wide tile
     int32_t pre_wide;                   // prefixes run in wide tiles
     int32_t own_wide;                   // own contexts run in wide tiles
@@ -1352,12 +1357,18 @@ __device__ void run_thin4(const Args& A, const Piece& P, const Dest& to, float* 
 // alone moves rows of 544 bytes at 3.5 TB/s where whole pages move at 6.0.  So
 // here the workgroup loads whole rows, K's and V's of 32 keys per part at a time,
 // to shared memory without registers, NB stages in a ring, and each wave reads its
-// head from there.  (One head a set makes rows that are little more than what
+// head from there (256 requests of 256 to 8192 tokens, 8 kv heads of 128 dims: 241
+// us, 4.9 TB/s, where the bytes alone take 200; with two stages 10% more, with four
+// the same).  (One head a set makes rows that are little more than what
 // the wave needs, and is loaded as above.)
 //
 // A stage is 64 kp rows, K's and then V's, of R pieces of 16 bytes each (the
 // set's heads' numbers, then the pieces that hold their scales), one behind the
-// other.  Its loads, of 64 pieces, are dealt to the waves in runs of NJ or NJ + 1;
+// other.  HEADS: head-major blocks whose pages hold whole tiles; a stage is then
+// [plane][tile][head] units of 16 keys' numbers, each in one run of its page, and
+// behind them the same of scales, and takes as many loads (256 requests of 256 to
+// 8192 tokens 257 us, through registers 301).
+// Its loads, of 64 pieces, are dealt to the waves in runs of NJ or NJ + 1;
 // those past the last load row 0 to a place of their own, so that at least NJ a
 // wave are under way everywhere.  Stages past the last load row 0.  Page ids are
 // loaded NB stages before their use: loads return in order.
@@ -1383,7 +1394,7 @@ __device__ inline void stage_barrier() {
 
 // NB buffers (b2 only where there are three); there: 128 bytes for each,
 // one a key, 1 where it is there.
-template <class T, class C, int NB>
+template <class T, class C, int NB, bool HEADS>
 __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, char* b0, char* b1, char* b2,
                                char* there) {
     using G = Stage4<C>;
@@ -1394,14 +1405,15 @@ __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, ch
     const int kp = A.kp, keys = 32 * kp;                    // of a stage; 1, 2 or 4 parts
     const int pieces = A.pieces, row_bytes = pieces * 16;
 
-    // this wave's loads, and their first row
-    const int loads = keys * pieces / 32, extra = loads > NJ * kWaves ? loads - NJ * kWaves : 0;
+    // this wave's loads, and their first row; HEADS: from load `tiles0` on they are scales
+    const int tiles0 = kp * pieces;
+    const int loads = HEADS ? (17 * kp * pieces + 15) / 16 : tiles0, extra = loads > NJ * kWaves ? loads - NJ * kWaves : 0;
     const int load0 = wave * NJ + (wave < extra ? wave : extra);
     const bool more = wave < extra;
-    const int row0 = by(load0 * 64, A.by_pieces);
+    const int row0 = HEADS ? 0 : by(load0 * 64, A.by_pieces);
     // the key of a stage that this lane looks up; the first stages' pages
     const int32_t mine = (row0 + lane) & (keys - 1), step = keys;
-    const bool tells = row0 + lane < keys;
+    const bool tells = HEADS ? wave == 0 && lane < keys : row0 + lane < keys;
     auto look = [&](int32_t k) { return key_page(A, P.lists, P.pg0, k + mine); };
     int32_t k0 = P.key0, ids[NB], first[NB - 1];
 #pragma unroll
@@ -1422,27 +1434,43 @@ __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, ch
     const int32_t kv0 = by(P.set * A.hs, A.by_parts);
     int32_t kvl = by(P.set * A.hs + A.hs - 1, A.by_parts);
     if (kvl > A.H - 1) kvl = A.H - 1;
-    const int nkv = kvl - kv0 + 1, numbers = nkv * A.D / 32;
-    const int32_t s0 = static_cast<int32_t>(A.s_base) + kv0 * (A.D / 32);       // of the row
-    const int used = numbers + ((s0 & 15) + nkv * (A.D / 32) + 15) / 16;
+    const int nkv = kvl - kv0 + 1, blocks = A.D / 32, numbers = nkv * blocks;
+    const int32_t s0 = static_cast<int32_t>(A.s_base) + kv0 * blocks;           // of an NHD row
+    const int used = HEADS ? numbers : numbers + ((s0 & 15) + numbers + 15) / 16;
     int from_row[NJ + 1];
     int64_t from[NJ + 1];
     const int64_t to_v = A.v - A.k;
 #pragma unroll
     for (int j = 0; j <= NJ; ++j) {
-        const int p = (load0 + j) * 64 + lane, r = by(p, A.by_pieces), x = p - r * pieces;
-        const bool in = r < 2 * keys && x < used;
-        from_row[j] = r < 2 * keys ? r - row0 : 0;
-        from[j] = !in ? 0
-                      : (x < numbers ? kv0 * A.D / 2 + x * 16 : (s0 & ~15) + (x - numbers) * 16) +
-                            (r < keys ? 0 : to_v);
+        const int p = (load0 + j) * 64 + lane;
+        from_row[j] = 0;
+        from[j] = 0;
+        if constexpr (HEADS) {
+            // unit: numbers or scales of a tile and a head, 16 keys one behind the other
+            const bool scale = load0 + j >= tiles0;
+            const int n = scale ? blocks : A.D / 2, at = scale ? p - tiles0 * 64 : p;
+            const int unit = by(at, scale ? A.by_blocks : A.by_half), x = at - unit * n;
+            const int tile = by(unit, A.by_set_heads), h = unit - tile * A.set_heads;
+            if (tile < 4 * kp && h < nkv) {
+                from_row[j] = tile * 16 & (keys - 1);
+                from[j] = x * 16 + (kv0 + h) * (scale ? A.s_head : A.head_stride) + (tile < 2 * kp ? 0 : to_v);
+            }
+        } else {
+            const int r = by(p, A.by_pieces), x = p - r * pieces;
+            if (r < 2 * keys) from_row[j] = r - row0;
+            if (r < 2 * keys && x < used)
+                from[j] = (x < numbers ? kv0 * A.D / 2 + x * 16 : (s0 & ~15) + (x - numbers) * 16) +
+                          (r < keys ? 0 : to_v);
+        }
     }
     auto load_stage = [&](int32_t k, int32_t page, char* buf, char* flags) {
         const int64_t off = page_offset(A, P.lists, P.pg0, page, k + mine, P.key1);
         const int64_t safe = off < 0 ? 0 : off;
+        const int64_t scales = !HEADS ? 0 : (off < 0 ? A.s_base : off + scales_from(A, k + mine));
         const char* at[NJ + 1];
 #pragma unroll
-        for (int j = 0; j <= NJ; ++j) at[j] = A.k + __shfl(safe, from_row[j]) + from[j];
+        for (int j = 0; j <= NJ; ++j)
+            at[j] = A.k + __shfl(HEADS && load0 + j >= tiles0 ? scales : safe, from_row[j]) + from[j];
         char* base = buf + load0 * 1024;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
@@ -1452,21 +1480,27 @@ __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, ch
     };
 
     // this lane's places in a buffer, of numbers and scales: key a of K, 4 g of V
-    const int hn = (row.kvh - kv0) * (A.D / 2), hs = numbers * 16 + (s0 & 15) + (row.kvh - kv0) * (A.D / 32);
+    // (HEADS: [plane][tile][head][key], numbers and behind them scales; a tile takes
+    // as much as 16 rows)
+    const int hd = row.kvh - kv0, tile_n = 16 * row_bytes, tile_s = HEADS ? row_bytes : tile_n;
+    const int key_n = HEADS ? A.D / 2 : row_bytes, key_s = HEADS ? blocks : row_bytes;
+    const int first_n = part * 2 * tile_n + hd * (HEADS ? 8 * A.D : A.D / 2);
+    const int first_s = part * 2 * tile_s + (HEADS ? 2 * keys * row_bytes + hd * 16 * blocks
+                                                   : numbers * 16 + (s0 & 15) + hd * blocks);
     int kn[KP], kc[KP], vn[C::NC], vc[C::NC];
 #pragma unroll
     for (int y = 0; y < KP; ++y) {
         int b = DP == 64 ? g * 8 : y * 64 + g * 16;
         if (b >= A.D / 2) b = 0;
-        kn[y] = (part * 32 + a) * row_bytes + hn + b;
-        kc[y] = (part * 32 + a) * row_bytes + hs + b / 16;
+        kn[y] = first_n + a * key_n + b;
+        kc[y] = first_s + a * key_s + b / 16;
     }
 #pragma unroll
     for (int c = 0; c < C::NC; ++c) {
         int b = (c * 16 + a) * C::VE / 2;
         if (b >= A.D / 2) b = 0;
-        vn[c] = (keys + part * 32 + 4 * g) * row_bytes + hn + b;
-        vc[c] = (keys + part * 32 + 4 * g) * row_bytes + hs + b / 16;
+        vn[c] = first_n + 2 * kp * tile_n + 4 * g * key_n + b;
+        vc[c] = first_s + 2 * kp * tile_s + 4 * g * key_s + b / 16;
     }
 
     auto compute = [&](int32_t k0, const char* buf, const char* flags) {
@@ -1483,12 +1517,12 @@ __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, ch
 #pragma unroll
             for (int x = 0; x < X; ++x) {
                 if constexpr (DP == 64) {
-                    const u32x2 w = *reinterpret_cast<const u32x2*>(buf + n + x * 16 * row_bytes);
+                    const u32x2 w = *reinterpret_cast<const u32x2*>(buf + n + x * tile_n);
                     S.k[x][y] = u32x4{w.x, w.y, 0, 0};
                 } else {
-                    S.k[x][y] = *reinterpret_cast<const u32x4*>(buf + n + x * 16 * row_bytes);
+                    S.k[x][y] = *reinterpret_cast<const u32x4*>(buf + n + x * tile_n);
                 }
-                S.ks[x][y] = *reinterpret_cast<const uint8_t*>(buf + c + x * 16 * row_bytes);
+                S.ks[x][y] = *reinterpret_cast<const uint8_t*>(buf + c + x * tile_s);
             }
         }
 #pragma unroll
@@ -1499,10 +1533,10 @@ __device__ void run_thin4_rows(const Args& A, const Piece& P, const Dest& to, ch
             for (int x = 0; x < X; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = (16 * x + i) * row_bytes;
+                    const int r = x * tile_n + i * key_n;
                     if constexpr (C::VE == 4) S.v[x][i][c] = *reinterpret_cast<const uint16_t*>(buf + n + r);
                     else S.v[x][i][c] = *reinterpret_cast<const uint32_t*>(buf + n + r);
-                    vs[x][i][c] = *reinterpret_cast<const uint8_t*>(buf + m + r);
+                    vs[x][i][c] = *reinterpret_cast<const uint8_t*>(buf + m + x * tile_s + i * key_s);
                 }
         }
         f32x4 s[X];
@@ -2178,7 +2212,7 @@ __device__ inline Mine plan_work(const Args& A, Plan* L, uint32_t block, uint32_
 }
 
 // LINES: 1 thin, 2 wide, 3 both; and of thin 4-bit tiles, 4 more: pages hold whole tiles of 16 keys, 8
-// more: rows by way of shared memory.
+// more: rows by way of shared memory, and 16 more: of head-major blocks.
 template <class T, int BITS, int DP, int LINES>
 struct Shared {
     using C = Cfg<T, BITS, DP>;
@@ -2193,7 +2227,7 @@ struct Shared {
 };
 
 template <class T, int BITS, int DP, int LINES>
-__global__ __launch_bounds__(kThreads, BITS == 4 && !(LINES & 2) ? kWaves4 : 2) void k_attend(const Args A) {
+__global__ __launch_bounds__(kThreads, 2) void k_attend(const Args A) {
     using C = Cfg<T, BITS, DP>;
     using S = Shared<T, BITS, DP, LINES>;
     __shared__ Plan plan;
@@ -2294,7 +2328,7 @@ __global__ __launch_bounds__(kThreads, BITS == 4 && !(LINES & 2) ? kWaves4 : 2) 
                 float* joins = reinterpret_cast<float*>(buf0);
                 if constexpr (C::FP4) {
                     if constexpr (LINES & 8) {
-                        if (!wide_line) run_thin4_rows<T, C, S::NB>(A, P, to, buf0, buf1, buf2, there);
+                        if (!wide_line) run_thin4_rows<T, C, S::NB, (LINES & 16) != 0>(A, P, to, buf0, buf1, buf2, there);
                     } else {
                         if (!wide_line) run_thin4<T, C, (LINES & 4) != 0>(A, P, to, joins);
                     }

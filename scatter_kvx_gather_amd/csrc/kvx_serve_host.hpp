@@ -384,8 +384,8 @@ kvx_status validate_read(const LayerRef& ref, int32_t block_layout, const kvx_po
 
 namespace at = kvx::attend;
 
-constexpr int64_t kUnits = 256;         // compute units of an MI355X
-constexpr int64_t kMostGrid = 2 * kUnits;
+constexpr int64_t kAttendGrid = 256;    // one workgroup per compute unit of an MI355X
+constexpr int32_t kRingReqs = 64;       // requests from which head-major 4-bit blocks go through the ring
 constexpr int64_t kJoinPlaces = 2048;   // waves of a join that shares rows among waves
 
 // The average query rows per kv head of a batch's contexts (and those of its
@@ -409,7 +409,6 @@ struct AttendShape {
     bool pre_wide, own_wide;
     int32_t wide_rows;
     int32_t slot_rows;
-    int32_t grid;                       // workgroups of k_attend
     int64_t placed, plan, splits, slot_ml, slot_o, row_ml, row_o, bytes;    // offsets into the workspace
 };
 
@@ -432,10 +431,6 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     s->wide_rows = s->DP <= 128 ? 256 : 128;
     // of the larger tile whichever this batch takes, so that a smaller batch needs no more
     s->slot_rows = std::max(s->wide_rows, at::kWaves * at::kThinRows);
-    // one workgroup per compute unit, and as many as its registers hold of 4-bit thin tiles alone
-    const bool fp4 = layout->dtype == KVX_FP4;
-    s->grid = static_cast<int32_t>(kUnits * (fp4 && !s->own_wide && !s->pre_wide ? at::kWaves4 / 2 : 1));
-    const int64_t most = fp4 ? kMostGrid : kUnits;
     int64_t end = 0;
     auto take = [&](int64_t count, int64_t size) {
         const int64_t at0 = end;
@@ -446,9 +441,9 @@ kvx_status attend_shape(const kvx_layout* layout, const Geom& g, int32_t num_req
     };
     s->placed = take(static_cast<int64_t>(num_reqs) + num_groups, sizeof(at::Placed));
     s->plan = take(6, 8);
-    s->splits = take(most, sizeof(at::Split));
-    s->slot_ml = take(2 * most * s->slot_rows, 8);
-    s->slot_o = take(2 * most * s->slot_rows, 4 * static_cast<int64_t>(D));
+    s->splits = take(kAttendGrid, sizeof(at::Split));
+    s->slot_ml = take(2 * kAttendGrid * s->slot_rows, 8);
+    s->slot_o = take(2 * kAttendGrid * s->slot_rows, 4 * static_cast<int64_t>(D));
     int64_t out_rows = 0;
     if (!mul_ok(tokens, q_heads, &out_rows)) return KVX_E_RANGE;
     if (num_groups == 0) out_rows = 0;
@@ -473,7 +468,9 @@ AttendKernels attend_kernels(int lines) {
                : lines == 5  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 5>)
                : lines == 7  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 7>)
                : lines == 9  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 9>)
-                             : reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 11>);
+               : lines == 11 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 11>)
+               : lines == 25 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 25>)
+                             : reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 27>);
     else if constexpr (DP > 128 && BITS == 16)
         main = reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 2>);
     else
@@ -524,15 +521,16 @@ bool rows_meet(const StridedRows& a, const StridedRows& b) {
     return false;
 }
 
-// The most 16-byte pieces that a set of thin heads has of a 4-bit NHD row: its
-// numbers, and the pieces that hold its scales.
-int32_t row_pieces(const at::Args& a, int64_t s_base, int32_t D) {
+// The most 16-byte pieces that a set of thin heads has of a 4-bit row: its
+// numbers, and in NHD blocks the pieces that hold its scales.
+int32_t row_pieces(const at::Args& a, int32_t block_layout, int64_t s_base, int32_t D) {
     int32_t most = 1;
     for (int32_t set = 0; set < a.sets; ++set) {
         const int32_t kv0 = set * a.hs / a.parts;
         const int32_t n = std::min((set * a.hs + a.hs - 1) / a.parts, a.H - 1) - kv0 + 1;
         const int64_t at0 = (s_base + int64_t(kv0) * (D / 32)) % 16;
-        most = std::max<int32_t>(most, n * D / 32 + static_cast<int32_t>((at0 + n * (D / 32) + 15) / 16));
+        const int32_t scales = block_layout == KVX_HND ? 0 : static_cast<int32_t>((at0 + n * (D / 32) + 15) / 16);
+        most = std::max<int32_t>(most, n * D / 32 + scales);
     }
     return most;
 }
@@ -859,8 +857,13 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.by_hs = magic_of(a.hs);
     a.by_parts = magic_of(a.parts);
     a.by_gv = magic_of(a.gv);
-    a.pieces = fp4 ? row_pieces(a, ref.s_base, layout->head_dim) : 1;
+    a.pieces = fp4 ? row_pieces(a, block_layout, ref.s_base, layout->head_dim) : 1;
     a.by_pieces = magic_of(a.pieces);
+    const int32_t blocks = std::max(1, layout->head_dim / 32);
+    a.set_heads = block_layout == KVX_HND ? a.pieces / blocks : 1;
+    a.by_set_heads = magic_of(std::max(1, a.set_heads));
+    a.by_blocks = magic_of(blocks);
+    a.by_half = magic_of(16 * blocks);
     a.wide_tokens = s.wide_rows / s.G;
     a.pre_wide = s.pre_wide;
     a.own_wide = s.own_wide;
@@ -871,7 +874,10 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     // 28.1 / 22.9 / 26.5, 64 of 64 keys 19.1 / 20.5 / 16.5, one of 8192 keys 33.1 /
     // 26.4 / 28.3.  Items of 40 to 100 (thin) and 320 to 600 units (wide) are
     // within 3% of each other on ragged batches; without them the workgroups
-    // with many short items end last.
+    // with many short items end last.  4-bit keys are read four times as fast, and an
+    // item's fixed time counts for more of them: with 64 / 128 / 176 units 64 requests
+    // of 512 to 4096 tokens take 57.5 / 54.5 / 56.1 us, 256 of 256 to 8192 249 / 244 /
+    // 243, 61 requests in 8 groups 34.6 / 30.2 / 30.5.
     a.thin_min_log2 = 6;
     a.wide_min_log2 = 8;
     a.thin_item = fp4 ? 128 : 64;
@@ -892,11 +898,24 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     a.slot_rows = s.slot_rows;
 
     int lines = s.own_wide || s.pre_wide ? 3 : 1;
-    // 4 bits: rows by way of shared memory, or the 16 rows of a tile in one page,
-    // their offsets inside it in 32 bits
-    if (fp4 && block_layout == KVX_NHD && a.hs > 1 && a.kp * a.pieces <= at::stage4_loads(s.DP))
-        lines |= 8;
-    else if (fp4 && pool->page_size % 16 == 0 && a.page_shift >= 0 && ref.page_stride < (int64_t(1) << 31)) lines |= 4;
+    // 4-bit thin tiles, rows by way of shared memory (the ring) against registers.
+    // NHD rows of several heads: the ring (256 requests of 256 to 8192 tokens, 8
+    // kv heads of 128 dims: 241 us against 340); of one head, whose rows are little
+    // more than what its waves need: registers.  Head-major blocks whose pages hold
+    // whole tiles, up to 128 dims: the ring for many requests (256: 257 : 301, 64:
+    // 55.5 : 55.7), registers for few, whose short pieces feel its start (one
+    // request of 131071 tokens 52.7 : 49.9); above 128 dims, where two buffers are
+    // all that fits, registers (276 : 270).  There the 16 rows of a tile in one
+    // page, their offsets inside it in 32 bits, are addressed in scalar registers.
+    const bool tiled = pool->page_size % 16 == 0 && a.page_shift >= 0;
+    const bool hnd = block_layout == KVX_HND;
+    const int32_t loads = a.kp * a.pieces + (hnd ? (a.kp * a.pieces + 15) / 16 : 0);
+    const bool ring = a.hs > 1 && loads <= at::stage4_loads(s.DP) &&
+                      (!hnd || (tiled && a.kp <= 2 && s.DP <= 128 && a.num_reqs >= kRingReqs));
+    if (fp4 && ring)
+        lines |= hnd ? 24 : 8;
+    else if (fp4 && tiled && ref.page_stride < (int64_t(1) << 31))
+        lines |= 4;
     const AttendKernels k = x.dtype == KVX_BF16 ? attend_kernels<__bf16>(layout->dtype, s.DP, lines)
                                                 : attend_kernels<_Float16>(layout->dtype, s.DP, lines);
     if (log_enabled())
@@ -904,7 +923,7 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
                      "kvx: attend reqs=%d groups=%d tokens=%lld heads=%d/%d dim=%d prefix=%s own=%s\n",
                      a.num_reqs, ng, static_cast<long long>(a.T), x.q_heads, g.H, a.D,
                      ng == 0 ? "none" : (s.pre_wide ? "wide" : "thin"), s.own_wide ? "wide" : "thin");
-    KVX_TRY(launch_one(k.main, s.grid, at::kThreads, a, stream));
+    KVX_TRY(launch_one(k.main, kAttendGrid, at::kThreads, a, stream));
     if (ng > 0) {
         const int32_t per_head = (a.gv + 256 / s.DP - 1) / (256 / s.DP);
         const int32_t units = heads * per_head;
@@ -921,7 +940,9 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
                    ? KVX_OK
                    : KVX_E_HIP;
     }
-    int32_t pieces = s.grid, parts = lines & 2 ? at::kJoinParts : 2;
+    // workgroups for each piece that is split off: a thin tile's few rows take two
+    // (as many as a wide one's: 64 requests of 4-bit pools 56.7 us, with two 55.2)
+    int32_t pieces = static_cast<int32_t>(kAttendGrid), parts = lines & 2 ? at::kJoinParts : 2;
     const int64_t grid = int64_t(pieces) * parts +
                          (a.num_reqs + 64 * at::kJoinWaves - 1) / (64 * at::kJoinWaves);
     void* params[] = {&a, &pieces, &parts};

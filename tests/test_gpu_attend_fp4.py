@@ -186,6 +186,36 @@ def test_many_pieces(D, H, G, page, new, prefix):
         c.check(out, lse)
 
 
+@pytest.mark.parametrize("layout,page", [("nhd", 1), ("nhd", 16), ("hnd", 16), ("hnd", 64), ("hnd", 48)])
+@pytest.mark.parametrize("H,G,D", [(2, 3, 32), (3, 2, 64), (4, 4, 128), (5, 2, 96), (8, 4, 128), (8, 1, 64),
+                                   (12, 2, 128), (11, 1, 96), (3, 20, 64), (4, 2, 160), (2, 4, 256)])
+@pytest.mark.parametrize("prefix", [0, 75])
+def test_many_requests(layout, page, H, G, D, prefix):
+    """Batches that go through shared memory in both block layouts: ragged
+    contexts, empty ones, pages out of range, blocks of NaN in the newest rows."""
+    say("fp4 many requests", layout, page, H, G, D, prefix)
+    n = 70
+    rng = np.random.default_rng(H * 100 + D)
+    new = rng.choice([1, 1, 1, 2, 3, 0], n).tolist()
+    ctx = [max(x, int(rng.choice([0, 1, 15, 17, 31, 33, 64, 90, 150]))) for x in new]
+    extra = dict(members=[0, n], prefix=[prefix]) if prefix else {}
+    c = Fp4Case(8, new=new, ctx=ctx, H=H, G=G, D=D, page=page, layout=layout, bad=0.04,
+                k_scale=0.5, v_scale=2.0, **extra)
+    for r in range(0, n, 9):
+        rows = [x for x in c.b.rows(c.b.pg_off[r], c.b.ids, ctx[r])[-2:] if x is not None]
+        for x in rows:
+            c.scales[1][x, r % H, 0] = f4.NAN_SCALE
+    c.decode()
+    c.upload()
+    skipped = torch.zeros(1, dtype=torch.int64, device=DEV)
+    out, lse = c.run(skipped=skipped)
+    torch.cuda.synchronize()
+    c.check(out, lse)
+    assert skipped.item() == c.b.skipped()
+    again, lse2 = c.run()
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
 def test_scores_that_grow():
     """Maxima that rise along the keys (the accumulators are rescaled often)."""
     say("fp4 growing scores")
