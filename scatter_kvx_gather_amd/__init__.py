@@ -4,9 +4,9 @@ step around a pool: page tables built from lengths, rows appended and read back,
 attention with shared prefixes, over pools of 16, 8 and 4 bits.
 
 A thin ctypes binding over ``libkvx.so`` (C ABI and contract: include/kvx.h,
-include/kvx_serve.h and include/kvx_read.h).  It only marshals arguments -- torch tensors become device pointers and sizes,
-streams become ``hipStream_t`` handles -- and every byte is moved by the HIP
-kernels in the library.  PyTorch is used for device memory and streams only.
+include/kvx_serve.h and include/kvx_read.h).  It only marshals arguments --
+torch tensors become device pointers and sizes, streams become ``hipStream_t``
+handles -- and every byte is moved by the HIP kernels in the library.  PyTorch is used for device memory and streams only.
 
 There is no CPU fallback: if the library is missing or a call fails, an
 exception is raised.
