@@ -144,7 +144,8 @@ typedef struct kvx_attention {
  * those of out and lse keep their contents, so that one captured call serves
  * batches of up to total_tokens.  A sum over more
  * keys than one workgroup takes is joined in an order that depends on the
- * lengths alone, so results repeat bit for bit.
+ * lengths alone (over a KVX_FP4 pool also on the tables' num_ids, from which the
+ * kernel for small or large batches is chosen), so results repeat bit for bit.
  *
  * The pool holds the type of q, KVX_FP8 (e4m3) or KVX_FP4; f32 pools, num_kv = 1
  * and head_dim above 256 are KVX_E_UNSUPPORTED.  head_dim * element size is a

@@ -385,7 +385,8 @@ kvx_status validate_read(const LayerRef& ref, int32_t block_layout, const kvx_po
 namespace at = kvx::attend;
 
 constexpr int64_t kAttendGrid = 256;    // one workgroup per compute unit of an MI355X
-constexpr int32_t kRingReqs = 64;       // requests from which head-major 4-bit blocks go through the ring
+constexpr double kRingBytes = 64 << 20;         // of 4-bit keys and values, from which they go
+constexpr double kRingBytesHnd = 192 << 20;     // through the ring; in head-major blocks
 constexpr int64_t kJoinPlaces = 2048;   // waves of a join that shares rows among waves
 
 // The average query rows per kv head of a batch's contexts (and those of its
@@ -899,19 +900,27 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
 
     int lines = s.own_wide || s.pre_wide ? 3 : 1;
     // 4-bit thin tiles, rows by way of shared memory (the ring) against registers.
-    // NHD rows of several heads: the ring (256 requests of 256 to 8192 tokens, 8
-    // kv heads of 128 dims: 241 us against 340); of one head, whose rows are little
-    // more than what its waves need: registers.  Head-major blocks whose pages hold
-    // whole tiles, up to 128 dims: the ring for many requests (256: 257 : 301, 64:
-    // 55.5 : 55.7), registers for few, whose short pieces feel its start (one
-    // request of 131071 tokens 52.7 : 49.9); above 128 dims, where two buffers are
-    // all that fits, registers (276 : 270).  There the 16 rows of a tile in one
-    // page, their offsets inside it in 32 bits, are addressed in scalar registers.
+    // The ring keeps more loads under way, in whole rows; registers start sooner
+    // and have a step's products and loads in one chain.  So large batches take the
+    // ring, by the bytes that their tables have room for: what the host knows, and
+    // what is read unless a table is made for more (a captured step's).  us, ring :
+    // registers, keys in memory / in the 256 MiB cache, 8 kv heads of 128 dims, 32
+    // requests, NHD: 40 MB 31.1 : 30.6 / 29.5 : 26.3, 80 MB 37.9 : 40.2 / 36.1 : 32.1,
+    // 160 MB 51.7 : 59.8 / 50.3 : 57.0, 256 requests of 256 to 8192 tokens (1.2 GB)
+    // 241 : 340, 4 of 64 to 512 tokens 21 : 18; HND: 80 MB 39.5 : 38.0 / 37.8 : 31.4,
+    // 160 MB 54.3 : 55.2 / 53.4 : 52.0, 240 MB 69.1 : 72.0 (of 64 dims 84.7 : 83.3),
+    // 1.2 GB 257 : 301.  Rows of one head are little more than what its waves need,
+    // and head-major blocks of more than 128 dims leave two buffers at most (276 :
+    // 270): registers.  Head-major tiles have to lie in one page.  Registers address
+    // the 16 rows of a tile in one page, their offsets inside it in 32 bits, in
+    // scalar registers.
     const bool tiled = pool->page_size % 16 == 0 && a.page_shift >= 0;
     const bool hnd = block_layout == KVX_HND;
     const int32_t loads = a.kp * a.pieces + (hnd ? (a.kp * a.pieces + 15) / 16 : 0);
+    const double room = 2.0 * g.H * static_cast<double>(g.Db + ref.s_bytes) * pool->page_size *
+                        (static_cast<double>(a.own.num_ids) + static_cast<double>(a.pre.num_ids));
     const bool ring = a.hs > 1 && loads <= at::stage4_loads(s.DP) &&
-                      (!hnd || (tiled && a.kp <= 2 && s.DP <= 128 && a.num_reqs >= kRingReqs));
+                      (hnd ? tiled && a.kp <= 2 && s.DP <= 128 && room >= kRingBytesHnd : room >= kRingBytes);
     if (fp4 && ring)
         lines |= hnd ? 24 : 8;
     else if (fp4 && tiled && ref.page_stride < (int64_t(1) << 31))

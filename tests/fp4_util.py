@@ -6,13 +6,22 @@ import torch
 
 import scatter_kvx_gather_amd as kvx
 from tests import fp4_ref as f4
-from tests.serve_util import DEV, Case
+from tests.serve_util import DEV, Case, ints
+
+
+def room_for_large(H, D, page):
+    """Page ids whose 4-bit rows are 256 MiB: a table with so many counts as a
+    large batch's, whatever its requests use."""
+    return int((256 << 20) / (2 * H * D * 17 / 32 * page)) + 1
 
 
 class Fp4Case(Case):
     """A Case whose pool holds 4 bits: `codes` and `scales` are [rows, H, D] and
     [rows, H, D / 32] for K and V, and kv the values that they stand for.  Rows that
-    no list holds a token in are blocks of NaN."""
+    no list holds a token in are blocks of NaN.  `roomy`: the table has room for many
+    more pages, as a step that is captured for larger batches has."""
+
+    roomy = False
 
     def __init__(self, *args, spread=3, **kw):
         self.codes = None
@@ -68,3 +77,6 @@ class Fp4Case(Case):
         self.kv, self.codes, self.joint, self.layout, self.pool_type = kv, codes, joint, layout, kind
         self.store, self.pool = store, pool
         self.lay = kvx.Layout(self.layers, 2, H, D, "fp4")
+        if self.roomy:
+            ids = np.concatenate([self.b.ids, np.full(room_for_large(H, D, B), -1)])
+            self.table = kvx.Table(ints(self.b.pg_off, torch.int64), ints(ids, torch.int32))

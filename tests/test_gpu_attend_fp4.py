@@ -7,11 +7,19 @@ import torch
 
 import scatter_kvx_gather_amd as kvx
 from tests import fp4_ref as f4
-from tests.fp4_util import Fp4Case
+from tests.fp4_util import Fp4Case, room_for_large
 from tests.gpu_util import say
 from tests.serve_util import DEV, ints
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=[False, True], ids=["small", "roomy"], autouse=True)
+def roomy(request, monkeypatch):
+    """Every test with a table of its own size and with one that has room for a
+    large batch, whose rows go another way."""
+    monkeypatch.setattr(Fp4Case, "roomy", request.param)
+    return request.param
 
 
 def run(name, scale=None, causal=True, **kw):
@@ -186,6 +194,7 @@ def test_many_pieces(D, H, G, page, new, prefix):
         c.check(out, lse)
 
 
+@pytest.mark.parametrize("roomy", [True], indirect=True)
 @pytest.mark.parametrize("layout,page", [("nhd", 1), ("nhd", 16), ("hnd", 16), ("hnd", 64), ("hnd", 48)])
 @pytest.mark.parametrize("H,G,D", [(2, 3, 32), (3, 2, 64), (4, 4, 128), (5, 2, 96), (8, 4, 128), (8, 1, 64),
                                    (12, 2, 128), (11, 1, 96), (3, 20, 64), (4, 2, 160), (2, 4, 256)])
@@ -261,7 +270,7 @@ def test_rows_behind_the_last_request():
     assert (o[T:] == 5.0).all() and (z[T:] == 6.0).all()
 
 
-def test_step_in_a_graph_and_on_another_stream():
+def test_step_in_a_graph_and_on_another_stream(roomy):
     """append, read and attend captured once and replayed while slots, rows,
     lengths and tables change, eager work between; two graphs with a workspace
     each; and the same calls on a stream of their own."""
@@ -279,10 +288,11 @@ def test_step_in_a_graph_and_on_another_stream():
         s["pool"] = kvx.Pool(s["store"], P, page, slot_stride=R)
         s["slots"] = torch.zeros(n, dtype=torch.int64, device=DEV)
         s["ctx"] = torch.zeros(n, dtype=torch.int32, device=DEV)
-        s["ids"] = torch.zeros(P, dtype=torch.int32, device=DEV)
+        room = torch.full((P + roomy * room_for_large(H, D, page),), -1, dtype=torch.int32, device=DEV)
+        s["ids"] = room[:P]
         s["tok"] = torch.arange(n + 1, device=DEV)
         s["off"] = torch.arange(0, 10 * n + 1, 10, device=DEV)
-        s["table"], s["reqs"] = kvx.Table(s["off"], s["ids"]), kvx.Requests(s["tok"], n)
+        s["table"], s["reqs"] = kvx.Table(s["off"], room), kvx.Requests(s["tok"], n)
         s["k"], s["v"], s["q"] = rand(n, H, D), rand(n, H, D), rand(n, H * G, D)
         s["bk"], s["bv"] = torch.zeros_like(s["k"]), torch.zeros_like(s["v"])
         s["out"] = torch.zeros_like(s["q"])
