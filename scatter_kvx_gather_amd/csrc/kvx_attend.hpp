@@ -1372,12 +1372,30 @@ __device__ void run_thin4(const Args& A, const Piece& P, const Dest& to, float* 
 // those past the last load row 0 to a place of their own, so that at least NJ a
 // wave are under way everywhere.  Stages past the last load row 0.  Page ids are
 // loaded NB stages before their use: loads return in order.
+//
+// A lane looks up one key's page, so a wave has the offsets of the 64 rows from its
+// first one on.  Of up to 64 keys a stage that is every key; of 128 (four parts)
+// the rows of a wave's loads have to be no more than 64 (rows4_fit).  With 160 and 192
+// dims of one kv head and 17 to 32 query heads they are 86 and 74: registers.
 constexpr int stage4_loads(int DP) { return DP == 64 ? 20 : (DP == 128 ? 36 : 70); }
+constexpr int stage4_wave(int DP) { return DP == 64 ? 2 : (DP == 128 ? 4 : 8); }    // the fewest loads of a wave
+
+// Whether every row of an NHD stage, kp parts and `pieces` pieces a row, is of a
+// key that the wave which loads it has looked up.
+constexpr bool rows4_fit(int DP, int kp, int pieces) {
+    if (32 * kp <= 64) return true;
+    const int n = stage4_wave(DP), loads = kp * pieces, extra = loads > n * kWaves ? loads - n * kWaves : 0;
+    for (int wave = 0; wave < kWaves; ++wave) {
+        const int load0 = wave * n + (wave < extra ? wave : extra), end = load0 + n + (wave < extra ? 1 : 0);
+        if ((end * 64 - 1) / pieces - load0 * 64 / pieces >= 64) return false;
+    }
+    return true;
+}
 
 template <class C>
 struct Stage4 {
     static constexpr int DP = C::KS * 32;
-    static constexpr int NJ = DP == 64 ? 2 : (DP == 128 ? 4 : 8);       // the fewest loads of a wave
+    static constexpr int NJ = stage4_wave(DP);
     static constexpr int LOADS = stage4_loads(DP);                      // the most of a stage
     static constexpr int BUF = (LOADS + 1) * 1024;
 };

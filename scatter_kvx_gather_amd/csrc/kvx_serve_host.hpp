@@ -911,16 +911,17 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     // 160 MB 54.3 : 55.2 / 53.4 : 52.0, 240 MB 69.1 : 72.0 (of 64 dims 84.7 : 83.3),
     // 1.2 GB 257 : 301.  Rows of one head are little more than what its waves need,
     // and head-major blocks of more than 128 dims leave two buffers at most (276 :
-    // 270): registers.  Head-major tiles have to lie in one page.  Registers address
-    // the 16 rows of a tile in one page, their offsets inside it in 32 bits, in
-    // scalar registers.
+    // 270): registers.  Head-major tiles have to lie in one page, and the rows of a
+    // wave's loads among those that it looks up.  Registers address the 16 rows of a
+    // tile in one page, their offsets inside it in 32 bits, in scalar registers.
     const bool tiled = pool->page_size % 16 == 0 && a.page_shift >= 0;
     const bool hnd = block_layout == KVX_HND;
     const int32_t loads = a.kp * a.pieces + (hnd ? (a.kp * a.pieces + 15) / 16 : 0);
     const double room = 2.0 * g.H * static_cast<double>(g.Db + ref.s_bytes) * pool->page_size *
                         (static_cast<double>(a.own.num_ids) + static_cast<double>(a.pre.num_ids));
     const bool ring = a.hs > 1 && loads <= at::stage4_loads(s.DP) &&
-                      (hnd ? tiled && a.kp <= 2 && s.DP <= 128 && room >= kRingBytesHnd : room >= kRingBytes);
+                      (hnd ? tiled && a.kp <= 2 && s.DP <= 128 && room >= kRingBytesHnd
+                           : at::rows4_fit(s.DP, a.kp, a.pieces) && room >= kRingBytes);
     if (fp4 && ring)
         lines |= hnd ? 24 : 8;
     else if (fp4 && tiled && ref.page_stride < (int64_t(1) << 31))
@@ -929,9 +930,11 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
                                                 : attend_kernels<_Float16>(layout->dtype, s.DP, lines);
     if (log_enabled())
         std::fprintf(stderr,
-                     "kvx: attend reqs=%d groups=%d tokens=%lld heads=%d/%d dim=%d prefix=%s own=%s\n",
+                     "kvx: attend reqs=%d groups=%d tokens=%lld heads=%d/%d dim=%d prefix=%s own=%s "
+                     "thin_keys=%s pieces=%d waves_a_head=%d\n",
                      a.num_reqs, ng, static_cast<long long>(a.T), x.q_heads, g.H, a.D,
-                     ng == 0 ? "none" : (s.pre_wide ? "wide" : "thin"), s.own_wide ? "wide" : "thin");
+                     ng == 0 ? "none" : (s.pre_wide ? "wide" : "thin"), s.own_wide ? "wide" : "thin",
+                     (lines & 8) != 0 ? "ring" : "registers", a.pieces, a.kp);
     KVX_TRY(launch_one(k.main, kAttendGrid, at::kThreads, a, stream));
     if (ng > 0) {
         const int32_t per_head = (a.gv + 256 / s.DP - 1) / (256 / s.DP);
