@@ -463,20 +463,23 @@ struct AttendKernels {
 template <class T, int BITS, int DP>
 AttendKernels attend_kernels(int lines) {
     const void* main;
-    if constexpr (BITS == 4)
-        main = lines == 1    ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 1>)
-               : lines == 3  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 3>)
-               : lines == 5  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 5>)
-               : lines == 7  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 7>)
-               : lines == 9  ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 9>)
-               : lines == 11 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 11>)
-               : lines == 25 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 25>)
-                             : reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 27>);
-    else if constexpr (DP > 128 && BITS == 16)
+    if constexpr (BITS == 4) {
+        main = lines == 1   ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 1>)
+               : lines == 3 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 3>)
+               : lines == 5 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 5>)
+               : lines == 7 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 7>)
+               : lines == 9 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 9>)
+                            : reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 11>);
+        if constexpr (DP <= 128)        // head-major blocks of more dims go through registers
+            main = lines == 25   ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 25>)
+                   : lines == 27 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 27>)
+                                 : main;
+    } else if constexpr (DP > 128 && BITS == 16) {
         main = reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 2>);
-    else
+    } else {
         main = lines == 1 ? reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 1>)
                           : reinterpret_cast<const void*>(&at::k_attend<T, BITS, DP, 3>);
+    }
     return {main, reinterpret_cast<const void*>(&at::k_attend_join<T, DP, false>),
             reinterpret_cast<const void*>(&at::k_attend_join<T, DP, true>),
             reinterpret_cast<const void*>(&at::k_attend_join_items<T, DP>)};
