@@ -148,9 +148,11 @@ typedef enum kvx_dtype {
  * In head-major blocks (kvx_block_layout) a page holds its numbers as
  * [kv_heads][page_size][head_dim / 2] and behind them its scales as
  * [kv_heads][page_size][head_dim / 32].  kvx_gather, kvx_scatter and
- * kvx_gather_scatter copy such rows whole (of head-major blocks, pages whose
- * slots all take part); kvx_gather_scatter_heads and the permutes refuse them
- * (KVX_E_UNSUPPORTED). */
+ * kvx_gather_scatter copy such rows whole.  A slot's bytes of a head-major block
+ * are not its row, so between such pools they copy pages whose slots all take
+ * part, at one page size; nothing checks that, and a page that is filled in part
+ * arrives with other bytes (kvx_read and kvx_append move its rows).
+ * kvx_gather_scatter_heads and the permutes refuse KVX_FP4 (KVX_E_UNSUPPORTED). */
 typedef struct kvx_layout {
     int32_t num_layers;     /* >= 1 */
     int32_t num_kv;         /* 2 for separate K and V planes, 1 for one latent plane per layer */

@@ -20,13 +20,15 @@ extern "C" {
  * pool's, rows are copied bit by bit and the scales are 1 (KVX_E_UNSUPPORTED
  * otherwise).  KVX_FP8 and KVX_FP4 pools are also read as f16, bf16 or f32: the
  * 32-bit products of the values with k_scale and v_scale, rounded to nearest even
- * (NaN stays NaN, what passes the type's range is an infinity); other pairs are
- * KVX_E_UNSUPPORTED, and so is KVX_FP4 as dtype.  Scales are finite, positive
+ * (NaN stays NaN, what passes the type's range is an infinity).  Every scale byte
+ * of a KVX_FP4 pool is read, whoever wrote it: a value is first rounded to 32 bits,
+ * which the largest few pass (infinities).  Other pairs are KVX_E_UNSUPPORTED, and
+ * so is KVX_FP4 as dtype.  Scales are finite, positive
  * and from 2^-64 to 2^64 (KVX_E_RANGE).  A slot outside the pool leaves its rows
  * of k and v as they were and is counted once in *skipped (if not NULL).  Rows of
- * k and v share no byte with one another (KVX_E_OVERLAP, by address), and none
- * lies in a slot that the call reads (unchecked; KVX_VALIDATE=1 returns
- * KVX_E_OVERLAP).  The layout has num_kv = 2.  One launch. */
+ * k and v share no byte with one another (KVX_E_OVERLAP, by address), none lies in
+ * a slot that the call reads (unchecked; KVX_VALIDATE=1 returns KVX_E_OVERLAP), and
+ * none over the slots or the counter (unchecked).  The layout has num_kv = 2.  One launch. */
 typedef struct kvx_rows_out {
     void* k;
     void* v;

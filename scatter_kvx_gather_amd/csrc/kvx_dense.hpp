@@ -274,7 +274,7 @@ __global__ __launch_bounds__(kAppendThreads) void k_read(const DenseArgs A) {
                     pair(2 * i + 1, __builtin_amdgcn_cvt_pk_f32_fp8(w[kv][i], true));
                 }
             } else {
-                // an exponent of 255 makes NaN of any number
+                // the conversion takes the exponent's bits: 0 is 2^-127, and 255 makes NaN
                 const float unit = __builtin_bit_cast(float, byte[kv] << 23);
                 pair(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[kv][0], unit, 0));
                 pair(1, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[kv][0], unit, 1));

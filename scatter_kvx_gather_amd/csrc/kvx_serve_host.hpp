@@ -912,7 +912,11 @@ kvx_status kvx_attend(const kvx_layout* layout, int32_t layer, const kvx_pool* p
     // 160 MB 51.7 : 59.8 / 50.3 : 57.0, 256 requests of 256 to 8192 tokens (1.2 GB)
     // 241 : 340, 4 of 64 to 512 tokens 21 : 18; HND: 80 MB 39.5 : 38.0 / 37.8 : 31.4,
     // 160 MB 54.3 : 55.2 / 53.4 : 52.0, 240 MB 69.1 : 72.0 (of 64 dims 84.7 : 83.3),
-    // 1.2 GB 257 : 301.  Rows of one head are little more than what its waves need,
+    // 1.2 GB 257 : 301.  Fewer heads and more dims gain from the ring later: NHD with 2
+    // kv heads 80 MB 42.6 : 39.2, 160 MB 56.7 : 56.8 (in 256 requests 49.2 : 44.8, 64.3 :
+    // 63.9), with 8 of 256 dims 42.3 : 42.2, 56.2 : 59.7 (52.8 : 50.5, 68.3 : 69.9), with 8
+    // of 64 dims sooner, 41.0 : 45.6; one bound for all costs them up to 10% between 64
+    // and 160 MB.  Rows of one head are little more than what its waves need,
     // and head-major blocks of more than 128 dims leave two buffers at most (276 :
     // 270): registers.  Head-major tiles have to lie in one page, and the rows of a
     // wave's loads among those that it looks up.  Registers address the 16 rows of a
